@@ -287,7 +287,7 @@ def _quantize4(x, group):
     """Rows [..., dim] -> (words, s, b) in float32 steps."""
     g = x.float().unflatten(-1, (x.shape[-1] // group, group))
     lo, hi = g.amin(-1, keepdim=True), g.amax(-1, keepdim=True)
-    s = (hi - lo) / 15.0
+    s = (hi - lo) / torch.full_like(lo, 15.0)      # a tensor: torch multiplies by a number's reciprocal
     q = torch.clamp(torch.round((g - lo) / torch.where(s == 0, torch.ones_like(s), s)), 0, 15)
     q = torch.where(s == 0, torch.zeros_like(q), q).to(torch.int64).flatten(-2)
     return _pack(q, 4), s[..., 0].to(x.dtype), lo[..., 0].to(x.dtype)
