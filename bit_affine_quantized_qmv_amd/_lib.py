@@ -25,7 +25,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqmm.so")
 # Every symbol include/qmm.h declares.
 EXPORTS = ("qmm_abi_version", "qmm_last_error", "qmm_quantize", "qmv", "qmm_t", "qmm_plan", "qmm_gather_qmv",
            "qmm_dequantize", "qmm_embedding", "qmm_qmv_argmax", "qmm_qmv_argmax_noalloc", "qmm_topk",
-           "qmm_qmv_topk")
+           "qmm_qmv_topk", "qmm_kv_append", "qmm_kv_read", "qmm_kv_attend", "qmm_kv_attend_workspace_bytes")
 
 
 class TensorDesc(ctypes.Structure):
@@ -57,6 +57,34 @@ class Plan(ctypes.Structure):
                 ("row_stride", ctypes.c_int64),
                 ("family", ctypes.c_int32),
                 ("kind", ctypes.c_int32)]
+
+
+class KVCacheDesc(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p),
+                ("pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int32),
+                ("heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32),
+                ("group_size", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class KVAttendDesc(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p),
+                ("q_batch_stride", ctypes.c_int64),
+                ("q_token_stride", ctypes.c_int64),
+                ("q_head_stride", ctypes.c_int64),
+                ("batch", ctypes.c_int64),
+                ("q_len", ctypes.c_int64),
+                ("q_heads", ctypes.c_int32),
+                ("causal", ctypes.c_int32),
+                ("window", ctypes.c_int64),
+                ("scale", ctypes.c_float),
+                ("block_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64),
+                ("max_blocks", ctypes.c_int64),
+                ("lengths", ctypes.c_void_p),
+                ("max_length", ctypes.c_int64)]
 
 
 class QmmError(RuntimeError):
@@ -114,6 +142,15 @@ def load() -> ctypes.CDLL:
     lib.qmm_plan.argtypes = [ctypes.POINTER(TensorDesc), ctypes.POINTER(WeightDesc),
                              ctypes.POINTER(TensorDesc), ctypes.c_uint32, ctypes.c_int32,
                              ctypes.POINTER(Plan)]
+    lib.qmm_kv_append.restype = ctypes.c_int32
+    lib.qmm_kv_append.argtypes = [ctypes.POINTER(KVCacheDesc), P, ctypes.c_int64, ctypes.c_int64, P, ctypes.c_int64,
+                                  ctypes.c_int64, P, ctypes.c_int64, P]
+    lib.qmm_kv_read.restype = ctypes.c_int32
+    lib.qmm_kv_read.argtypes = [ctypes.POINTER(KVCacheDesc), P, ctypes.c_int64, P, P, P]
+    lib.qmm_kv_attend.restype = ctypes.c_int32
+    lib.qmm_kv_attend.argtypes = [ctypes.POINTER(KVCacheDesc), ctypes.POINTER(KVAttendDesc), P, P, ctypes.c_int64, P]
+    lib.qmm_kv_attend_workspace_bytes.restype = ctypes.c_int64
+    lib.qmm_kv_attend_workspace_bytes.argtypes = [ctypes.POINTER(KVCacheDesc), ctypes.POINTER(KVAttendDesc)]
     _lib = lib
     return lib
 

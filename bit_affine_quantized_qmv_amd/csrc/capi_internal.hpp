@@ -22,4 +22,15 @@ int32_t prepare_qmv_argmax(const void* x, const qmm_tensor_desc_t* x_desc, const
                            const qmm_tensor_desc_t* y_desc, int32_t* out_index, float* out_value, MatArgs* out,
                            int64_t* rows);
 
+// Run an entry point's body; nothing it throws (a failed allocation of a message) crosses the
+// C boundary.
+template <class F>
+auto guarded(F&& body) noexcept -> decltype(body()) {
+  try {
+    return body();
+  } catch (...) {
+    return QMM_ERR_HIP;
+  }
+}
+
 }  // namespace qmm

@@ -1,0 +1,510 @@
+// Attention over the 4-bit key/value cache, for one element type (included by
+// kv_attend_bf16.hip and kv_attend_fp16.hip).
+//
+// With k_j = s_jg c_jd + b_jg (codes c, groups g of the head dimension) the score of query q is
+//     q . k_j = sum_g ( s_jg * sum_{d in g} q_d c_jd  +  b_jg * sum_{d in g} q_d ),
+// and the output, with p_j = exp2(score_j - m) for a running maximum m and V's own s, b, c,
+//     o_d = ( sum_j (p_j s_jg) c_jd  +  sum_j p_j b_jg ) / sum_j p_j        (g the group of d).
+// Both sums over codes run on the matrix cores with the codes as exact integers; scales and
+// biases enter in float32.  Nothing is dequantized to memory, and each code is unpacked once
+// for all the query rows of a wave.
+//
+// The score product takes tokens as its rows (K codes are the first operand) and query rows
+// as its columns, so a lane's accumulator holds four consecutive tokens of one query row --
+// the layout that the second product needs for its right operand, whose contraction index is
+// the token: probabilities never move between lanes.  A step is 32 tokens (two 16-token
+// tiles): contraction slot (h, e) of the second product is token 4h + e of the first tile for
+// e < 4, 4h + e - 4 of the second one otherwise.
+//
+// Softmax: m, the sum of p, the bias sums and both accumulators are float32.  m is raised only
+// when a score exceeds it by more than kSlack (in powers of two), so most steps rescale
+// nothing; p is then at most 2^kSlack.  p_j s_jg goes to the matrix cores as two operands of
+// the element type, its leading bits and the rest (split2), so that the product carries 16
+// (bf16) or 22 (fp16) bits of it: with one operand, a row that attends to one token would
+// return that token's codes with an error of up to 2^-8 (bf16) of their span.
+#pragma once
+
+#include <cfloat>
+
+#include "device_common.hpp"
+#include "kv_cache.hpp"
+
+namespace qmm {
+namespace kv {
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kStep = 32;              // tokens per wave and step
+constexpr float kNone = -FLT_MAX;      // running maximum before any token
+
+// Largest exponent of an unnormalised probability.  fp16: p * s must stay below 65504 for
+// every scale a cache of fp16 rows can have (range / 15 <= 131008 / 15 = 8734): 2^2.9 * 8734.
+template <class T>
+constexpr float slack() { return T::kDtype == QMM_BF16 ? 8.0f : 2.9f; }
+
+// Two float32 values as element-type pairs hi + lo: hi their leading bits (truncated), lo the
+// rest rounded to nearest.
+template <class T>
+__device__ inline void split2(float x, float y, uint32_t* hi, uint32_t* lo) {
+  if constexpr (T::kDtype == QMM_BF16) {
+    const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+    *hi = __builtin_amdgcn_perm(b, a, 0x07060302u);
+    *lo = T::pack2(x - __uint_as_float(a & 0xFFFF0000u), y - __uint_as_float(b & 0xFFFF0000u));
+  } else {
+    const auto t = __builtin_amdgcn_cvt_pkrtz(x, y);
+    *hi = __builtin_bit_cast(uint32_t, t);
+    *lo = T::pack2(x - (float)t[0], y - (float)t[1]);
+  }
+}
+
+template <int N>
+__device__ inline void load_words(uint32_t (&r)[N], const uint32_t* p) {
+  if constexpr (N == 2) {
+    const uint2 u = *(const uint2*)p;
+    r[0] = u.x;
+    r[1] = u.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const u32x4 u = *(const u32x4*)(p + 4 * i);
+      r[4 * i] = u.x;
+      r[4 * i + 1] = u.y;
+      r[4 * i + 2] = u.z;
+      r[4 * i + 3] = u.w;
+    }
+  }
+}
+
+// One side (K or V) of a 32-token step in registers: codes and (s, b) words of the lane's
+// tokens, for the two 16-token tiles.
+template <int D, int GS>
+struct Side {
+  uint32_t code[2][D / 32];
+  uint32_t sb[2][D / GS][4];
+};
+
+template <class T, int D, int GS, int RT, bool BY_ROWS>
+__global__ __launch_bounds__(kThreads) void attend_kernel(const AttendArgs a) {
+  constexpr int KC = D / 32;          // 32-element steps of a score; code words per lane and tile
+  constexpr int NT = D / 16;          // 16-element output tiles
+  constexpr int NG = D / GS;
+  constexpr int CPG = GS / 32;
+  constexpr int kRows = 16 * RT;      // query rows per wave
+  constexpr int kPitch = D + 4;       // LDS row of the merge, padded against bank conflicts
+  extern __shared__ float lds[];
+
+  const int lane = threadIdx.x & 63, col = lane & 15, h = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int split = blockIdx.x;
+  const int head = blockIdx.y % a.c.heads, row_tile = blockIdx.y / a.c.heads;
+  const int64_t b = blockIdx.z;
+  const int base = BY_ROWS ? (row_tile * kWaves + wave) * kRows : row_tile * kRows;
+  if (BY_ROWS && base >= a.rows) return;   // no barrier follows in this form
+
+  int len = a.lengths[b];
+  bool bad = len < 0 || len > a.max_length;
+  if (bad) len = 0;
+  // token ranges: [lo_min, hi_max) is seen by some row of the wave, [lo_max, hi_min) by all
+  const int off = len - a.q_len;
+  const int i_first = base / a.rep, i_last = (min(a.rows, base + kRows) - 1) / a.rep;
+  const int hi_max = a.causal ? max(0, off + i_last + 1) : len;
+  const int hi_min = a.causal ? max(0, off + i_first + 1) : len;
+  const int lo_min = a.window ? max(0, off + i_first - a.window + 1) : 0;
+  const int lo_max = a.window ? max(0, off + i_last - a.window + 1) : 0;
+  const int c0 = (lo_min & ~(kStep - 1)) + split * a.chunk;
+  const int c1 = min(c0 + a.chunk, hi_max);
+  const int stride = BY_ROWS ? kStep : kStep * kWaves;
+
+  // query operands: column col of row tile t is query row base + 16 t + col
+  typename T::v8 q[RT][KC];
+  float qsum[RT][NG];
+  int row_lo[RT], row_hi[RT];
+  const uint32_t one2 = T::pack2(1.0f, 1.0f);
+  const u32x4 ones = {one2, one2, one2, one2};
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    const int r = min(base + 16 * t + col, a.rows - 1);   // rows past the last repeat it and are not stored
+    const int i = r / a.rep, g = r - i * a.rep;
+    const uint16_t* qp = (const uint16_t*)a.q + b * a.q_batch_stride + (int64_t)i * a.q_token_stride +
+                         (int64_t)(head * a.rep + g) * a.q_head_stride + 8 * h;
+#pragma unroll
+    for (int c = 0; c < KC; ++c) q[t][c] = as_v8<T>(interleave_even_odd(*(const u32x4*)(qp + 32 * c)));
+#pragma unroll
+    for (int gi = 0; gi < NG; ++gi) {
+      f32x4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < CPG; ++c) d = T::mfma(as_v8<T>(ones), q[t][gi * CPG + c], d);
+      qsum[t][gi] = d[0];
+    }
+    row_hi[t] = a.causal ? off + i + 1 : len;
+    row_lo[t] = a.window ? off + i - a.window + 1 : 0;
+  }
+
+  float m[RT], l[RT], bsum[RT][NG];
+  f32x4 acc[RT][NT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    m[t] = kNone;
+    l[t] = 0.f;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) bsum[t][g] = 0.f;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  // Word offset of the 16-token tile that starts at token t0, and whether its page is real.
+  // Tiles that no row sees read page 0 (their tokens are masked); a tile that is needed and
+  // has no page of the pool poisons the wave's outputs.
+  const int32_t* table = a.table + b * a.table_stride;
+  const int64_t page_words = 2 * a.c.side;
+  auto tile_base = [&](int t0, int* token) -> const uint32_t* {
+    const bool needed = t0 < hi_max && t0 + 16 > lo_min;
+    int page = 0, in_page = 0;
+    if (needed) {
+      const int blk = t0 / a.c.page_size;
+      in_page = t0 - blk * a.c.page_size;
+      page = __builtin_amdgcn_readfirstlane(table[blk]);
+      if (page < 0 || page >= a.c.pages) {
+        bad = true;
+        page = 0;
+      }
+    }
+    *token = in_page;
+    return a.c.data + ((int64_t)page * a.c.heads + head) * page_words;
+  };
+  const int code_at = h * KC;
+  Side<D, GS> ks, vs;
+  auto load_side = [&](Side<D, GS>& s, int tile, const uint32_t* p, int token, bool value) {
+    if (value)
+      load_words<KC>(s.code[tile], p + (token / 4 + h) * (16 * KC) + col * KC);
+    else
+      load_words<KC>(s.code[tile], p + (token + col) * (D / 8) + code_at);
+    const uint32_t* sb = p + (int64_t)a.c.page_size * (D / 8) + token + 4 * h;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) load_words<4>(s.sb[tile][g], sb + g * a.c.page_size);
+  };
+  const uint32_t* base_next[2] = {nullptr, nullptr};
+  int token_next[2] = {0, 0};
+  auto find = [&](int t0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) base_next[i] = tile_base(t0 + 16 * i, &token_next[i]);
+  };
+  auto load_k = [&]() {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) load_side(ks, i, base_next[i], token_next[i], false);
+  };
+  auto load_v = [&]() {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) load_side(vs, i, base_next[i] + a.c.side, token_next[i], true);
+  };
+
+  const int first = BY_ROWS ? c0 : c0 + kStep * wave;
+  if (first < c1) {
+    find(first);
+    load_k();
+    load_v();
+  }
+  for (int t0 = first; t0 < c1; t0 += stride) {
+    const bool more = t0 + stride < c1;
+    // ---- scores: sc[t][i][r] of token t0 + 16 i + 4 h + r
+    float sc[RT][2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      u32x4 kc[KC];
+#pragma unroll
+      for (int c = 0; c < KC; ++c) kc[c] = codes4_to_v8<T>(ks.code[i][c]);
+      float s[NG][4], bb[NG][4];
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          s[g][r] = T::to_f32(ks.sb[i][g][r] & 0xFFFFu);
+          bb[g][r] = T::to_f32(ks.sb[i][g][r] >> 16);
+        }
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          f32x4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < CPG; ++c) d = T::mfma(as_v8<T>(kc[g * CPG + c]), q[t][g * CPG + c], d);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float x = g == 0 ? bb[0][r] * qsum[t][0] : __builtin_fmaf(bb[g][r], qsum[t][g], sc[t][i][r]);
+            sc[t][i][r] = __builtin_fmaf(s[g][r], d[r], x);
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sc[t][i][r] *= a.scale_log2;
+      }
+    }
+    if (more) {
+      find(t0 + stride);
+      load_k();
+    }
+    // ---- rows that do not see every token of the step
+    const bool masked = t0 < lo_max || t0 + kStep > hi_min;
+    uint32_t seen[RT];
+    if (masked) {
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        seen[t] = 0u;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int token = t0 + 16 * i + 4 * h + r;
+            const bool ok = token >= row_lo[t] && token < row_hi[t];
+            seen[t] |= ok ? 1u << (4 * i + r) : 0u;
+            sc[t][i][r] = ok ? sc[t][i][r] : -__builtin_inff();
+          }
+      }
+    }
+    // ---- probabilities
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      float top = fmaxf(fmaxf(sc[t][0][0], sc[t][0][1]), fmaxf(sc[t][0][2], sc[t][0][3]));
+      top = fmaxf(top, fmaxf(fmaxf(sc[t][1][0], sc[t][1][1]), fmaxf(sc[t][1][2], sc[t][1][3])));
+      if (__builtin_amdgcn_ballot_w64(top > m[t] + slack<T>()) != 0ull) {
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float raised = fmaxf(m[t], top);
+        const float f = __builtin_amdgcn_exp2f(m[t] - raised);
+        m[t] = raised;
+        l[t] *= f;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) bsum[t][g] *= f;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) acc[t][i] *= f;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          sc[t][i][r] = __builtin_amdgcn_exp2f(sc[t][i][r] - m[t]);
+          l[t] += sc[t][i][r];
+        }
+    }
+    // ---- second product, group by group
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      u32x4 hi[RT], lo[RT];
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        float x[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float s = T::to_f32(vs.sb[i][g][r] & 0xFFFFu), bv = T::to_f32(vs.sb[i][g][r] >> 16);
+            x[i][r] = sc[t][i][r] * s;
+            float pb = sc[t][i][r] * bv;
+            if (masked) {   // whatever a masked token's scales hold, it adds nothing
+              const bool ok = (seen[t] >> (4 * i + r)) & 1u;
+              x[i][r] = ok ? x[i][r] : 0.f;
+              pb = ok ? pb : 0.f;
+            }
+            bsum[t][g] += pb;
+          }
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          uint32_t uh, ul;
+          split2<T>(x[n >> 1][2 * (n & 1)], x[n >> 1][2 * (n & 1) + 1], &uh, &ul);
+          hi[t][n] = uh;
+          lo[t][n] = ul;
+        }
+      }
+#pragma unroll
+      for (int j = g * CPG; j < (g + 1) * CPG; ++j) {
+        const uint32_t w0 = vs.code[0][j], w1 = vs.code[1][j];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const uint32_t e0 = (n ? w0 >> 4 : w0) & 0x0F0F0F0Fu, e1 = (n ? w1 >> 4 : w1) & 0x0F0F0F0Fu;
+          const u32x4 vc = {T::fp8x2_lo(e0), T::fp8x2_hi(e0), T::fp8x2_lo(e1), T::fp8x2_hi(e1)};
+#pragma unroll
+          for (int t = 0; t < RT; ++t) {
+            acc[t][2 * j + n] = T::mfma(as_v8<T>(vc), as_v8<T>(lo[t]), acc[t][2 * j + n]);
+            acc[t][2 * j + n] = T::mfma(as_v8<T>(vc), as_v8<T>(hi[t]), acc[t][2 * j + n]);
+          }
+        }
+      }
+    }
+    if (more) load_v();
+  }
+
+  // ---- the lanes' shares of the sums, and the bias term: element d = 16 i + 4 h + r of row col
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    l[t] += __shfl_xor(l[t], 16);
+    l[t] += __shfl_xor(l[t], 32);
+    if (bad) {
+      l[t] = __builtin_nanf("");
+      m[t] = 0.f;
+    }
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      bsum[t][g] += __shfl_xor(bsum[t][g], 16);
+      bsum[t][g] += __shfl_xor(bsum[t][g], 32);
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[t][i] += bsum[t][i * 16 / GS];
+  }
+
+  const int64_t row0 = (b * a.c.heads + head) * a.rows;
+  float* part_ml = a.part + (int64_t)gridDim.z * a.c.heads * a.rows * a.splits * D;
+  auto store4 = [&](int r, int d, f32x4 o, float sum) {   // four elements of one row
+    if (a.splits > 1) {
+      *(f32x4*)(a.part + ((row0 + r) * a.splits + split) * D + d) = o;
+    } else {
+      const float inv = sum == 0.f ? 0.f : 1.0f / sum;    // a row that sees nothing is zero
+      const int i = r / a.rep, g = r - i * a.rep;
+      uint2 u;
+      u.x = T::pack2(o[0] * inv, o[1] * inv);
+      u.y = T::pack2(o[2] * inv, o[3] * inv);
+      *(uint2*)((uint16_t*)a.out + ((b * a.q_len + i) * (int64_t)a.q_heads + head * a.rep + g) * D + d) = u;
+    }
+  };
+  if constexpr (BY_ROWS) {
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      const int r = base + 16 * t + col;
+      if (r >= a.rows) continue;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) store4(r, 16 * i + 4 * h, acc[t][i], l[t]);
+      if (a.splits > 1 && h == 0) {
+        float* ml = part_ml + ((row0 + r) * a.splits + split) * 2;
+        ml[0] = m[t];
+        ml[1] = l[t];
+      }
+    }
+  } else {
+    // the four waves' sums meet in LDS: [wave][row][D], then [wave][row] maxima and sums
+    float* ml_s = lds + kWaves * kRows * kPitch;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      const int r = wave * kRows + 16 * t + col;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) *(f32x4*)(lds + r * kPitch + 16 * i + 4 * h) = acc[t][i];
+      if (h == 0) {
+        ml_s[2 * r] = m[t];
+        ml_s[2 * r + 1] = l[t];
+      }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < kRows * (D / 4); e += kThreads) {
+      const int rr = e / (D / 4), d = (e - rr * (D / 4)) * 4;
+      const int r = base + rr;
+      if (r >= a.rows) break;
+      float top = kNone;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) top = fmaxf(top, ml_s[2 * (w * kRows + rr)]);
+      float sum = 0.f;
+      f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float f = __builtin_amdgcn_exp2f(ml_s[2 * (w * kRows + rr)] - top);
+        sum = __builtin_fmaf(f, ml_s[2 * (w * kRows + rr) + 1], sum);
+        o += f * *(const f32x4*)(lds + (w * kRows + rr) * kPitch + d);
+      }
+      store4(r, d, o, sum);
+      if (a.splits > 1 && d == 0) {
+        float* ml = part_ml + ((row0 + r) * a.splits + split) * 2;
+        ml[0] = top;
+        ml[1] = sum;
+      }
+    }
+  }
+}
+
+// Joins the splits of one query row: o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s.
+// D/4 lanes hold the row's elements, the other lanes of the workgroup further splits.
+template <class T, int D>
+__global__ __launch_bounds__(kThreads) void attend_join_kernel(const AttendArgs a) {
+  constexpr int kLanes = D / 4, kGroups = kThreads / kLanes;
+  __shared__ float top_s[kWaves];
+  __shared__ float sum_s[kGroups];
+  __shared__ f32x4 o_s[kGroups][kLanes];
+  const int64_t row = blockIdx.x;                        // ((batch, head), query row)
+  const int lane = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
+  const float* o_part = a.part + row * a.splits * D;
+  const float* ml = a.part + a.batch * a.c.heads * a.rows * a.splits * D + row * a.splits * 2;
+  float top = kNone;
+  for (int s = threadIdx.x; s < a.splits; s += kThreads) top = fmaxf(top, ml[2 * s]);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+  if ((threadIdx.x & 63) == 0) top_s[threadIdx.x >> 6] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(top_s[0], top_s[1]), fmaxf(top_s[2], top_s[3]));
+  float sum = 0.f;
+  f32x4 o = {0.f, 0.f, 0.f, 0.f};
+  for (int s = grp; s < a.splits; s += kGroups) {
+    const float m = ml[2 * s];
+    if (m == kNone) continue;                            // no token of the split was seen
+    const float f = __builtin_amdgcn_exp2f(m - top);
+    sum = __builtin_fmaf(f, ml[2 * s + 1], sum);
+    o += f * *(const f32x4*)(o_part + (int64_t)s * D + 4 * lane);
+  }
+  o_s[grp][lane] = o;
+  if (lane == 0) sum_s[grp] = sum;
+  __syncthreads();
+  if (grp != 0) return;
+  for (int g = 1; g < kGroups; ++g) {
+    o += o_s[g][lane];
+    sum += sum_s[g];
+  }
+  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+  const int64_t bh = row / a.rows;
+  const int r = (int)(row - bh * a.rows);
+  const int64_t b = bh / a.c.heads;
+  const int head = (int)(bh - b * a.c.heads), i = r / a.rep, g = r - i * a.rep;
+  uint2 u;
+  u.x = T::pack2(o[0] * inv, o[1] * inv);
+  u.y = T::pack2(o[2] * inv, o[3] * inv);
+  *(uint2*)((uint16_t*)a.out + ((b * a.q_len + i) * (int64_t)a.q_heads + head * a.rep + g) * D + 4 * lane) = u;
+}
+
+template <class T, int D, int GS, int RT, bool BY_ROWS>
+hipError_t launch_form(const AttendArgs& a, const AttendPlan& p, hipStream_t stream) {
+  const int lds = BY_ROWS ? 0 : (kWaves * 16 * RT * (D + 4) + kWaves * 16 * RT * 2) * 4;
+  if (lds > 64 * 1024) {
+    const hipError_t e = hipFuncSetAttribute((const void*)attend_kernel<T, D, GS, RT, BY_ROWS>,
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+  }
+  const dim3 grid((unsigned)p.splits, (unsigned)(a.c.heads * p.row_tiles), (unsigned)a.batch);
+  hipLaunchKernelGGL((attend_kernel<T, D, GS, RT, BY_ROWS>), grid, dim3(kThreads), lds, stream, a);
+  return hipGetLastError();
+}
+
+template <class T, int D, int GS>
+hipError_t launch_shape(const AttendArgs& a, const AttendPlan& p, hipStream_t stream) {
+  hipError_t e;
+  if (p.by_rows)
+    e = launch_form<T, D, GS, (D == 256 ? 2 : 4), true>(a, p, stream);
+  else
+    e = p.tile_rows == 16 ? launch_form<T, D, GS, 1, false>(a, p, stream) : launch_form<T, D, GS, 2, false>(a, p, stream);
+  if (e != hipSuccess || p.splits == 1) return e;
+  hipLaunchKernelGGL((attend_join_kernel<T, D>), dim3((unsigned)(a.batch * a.c.heads * a.rows)), dim3(kThreads), 0,
+                     stream, a);
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t launch_attend(const AttendArgs& a, const AttendPlan& p, hipStream_t stream) {
+  const int gs = a.c.group_size;
+  switch (a.c.head_dim) {
+    case 64: return gs == 32 ? launch_shape<T, 64, 32>(a, p, stream) : launch_shape<T, 64, 64>(a, p, stream);
+    case 128:
+      return gs == 32   ? launch_shape<T, 128, 32>(a, p, stream)
+             : gs == 64 ? launch_shape<T, 128, 64>(a, p, stream)
+                        : launch_shape<T, 128, 128>(a, p, stream);
+    case 256:
+      return gs == 32   ? launch_shape<T, 256, 32>(a, p, stream)
+             : gs == 64 ? launch_shape<T, 256, 64>(a, p, stream)
+                        : launch_shape<T, 256, 128>(a, p, stream);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace kv
+}  // namespace qmm

@@ -269,6 +269,90 @@ int32_t qmm_plan(const qmm_tensor_desc_t* x_desc, const qmm_weight_desc_t* w,
                  const qmm_tensor_desc_t* y_desc, uint32_t flags, int32_t entry,
                  qmm_plan_t* out);
 
+/* ---- A key/value cache held in 4 bits, and attention over it.
+ * The cache keeps, per token slot and kv head, one K and one V row of head_dim values in the
+ * weights' codec with 4-bit codes: x = s * q + b per group of group_size consecutive values,
+ * s and b in dtype (quantizing the K and V rows a decode step appends is the min/max codec of
+ * qmm_quantize, row by row).  It is paged: slot = page * page_size + offset, and a block table
+ * names each sequence's pages in order.
+ * data: DEVICE, 16-byte aligned, pages * heads * QMM_KV_PAGE_WORDS words; the words' order is
+ * the library's own (rows go in with qmm_kv_append and come out with qmm_kv_read).  Any
+ * content is a valid empty cache: tokens outside a sequence's length are never used.
+ * Limits: head_dim in {64, 128, 256}; group_size in {32, 64, 128} and <= head_dim; page_size a
+ * multiple of 16, at most 65536; heads 1..4096; pages >= 1 and pages * page_size < 2^31. */
+typedef struct {
+  uint32_t* data;
+  int64_t pages;
+  int32_t page_size;   /* tokens per page */
+  int32_t heads;       /* kv heads        */
+  int32_t head_dim;
+  int32_t group_size;
+  int32_t dtype;       /* qmm_dtype_t     */
+} qmm_kv_cache_t;
+/* Words of one page of one head: codes and (s, b) pairs of its K and V rows. */
+#define QMM_KV_PAGE_WORDS(page_size, head_dim, group_size) \
+  (2 * (int64_t)(page_size) * ((head_dim) / 8 + (head_dim) / (group_size)))
+
+/* Quantize `tokens` new K and V rows per head into the cache: row (t, h) of k and v goes to
+ * slots[t] of head h.  Per group, in float32: s = (max - min) / 15, b = min,
+ * q = clamp(round_half_even((x - b) / s), 0, 15) (0 when s == 0); s and b are then rounded to
+ * dtype.  k, v: DEVICE, dtype, element (t, h, d) at t * token_stride + h * head_stride + d;
+ * 16-byte aligned, strides >= 0 and multiples of 8; finite values.  slots: DEVICE int32
+ * [tokens], distinct; a slot outside [0, pages * page_size) is skipped (nothing is written for
+ * it), so negative slots can pad a batch.  tokens == 0 is a no-op.  One kernel is enqueued. */
+int32_t qmm_kv_append(const qmm_kv_cache_t* cache, const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                      const void* v, int64_t v_token_stride, int64_t v_head_stride, const int32_t* slots,
+                      int64_t tokens, void* stream);
+
+/* The values the cache stands for at `count` slots: k and v, DEVICE, dense
+ * [count, heads, head_dim] of dtype, 16-byte aligned, round(fma(s, q, b)) of each element.  A
+ * slot outside [0, pages * page_size) gives NaN rows.  count == 0 is a no-op.  One kernel. */
+int32_t qmm_kv_read(const qmm_kv_cache_t* cache, const int32_t* slots, int64_t count, void* k, void* v,
+                    void* stream);
+
+/* Queries of one attention call over the cache.  Query i (0 <= i < q_len) of sequence n sits at
+ * position p = lengths[n] - q_len + i (the queries are the last q_len of the sequence's tokens,
+ * already appended).  It sees the cached tokens j in [0, lengths[n]); with `causal` only
+ * j <= p; with window > 0 (which needs causal) only j > p - window.
+ *     out = sum_j softmax_j(scale * q . k_j) v_j   over the tokens it sees, 0 if it sees none
+ * (an empty sequence, or p < 0: queries padded on the left).  Query head h reads kv head
+ * h / (q_heads / heads). */
+typedef struct {
+  const void* q;           /* DEVICE, dtype, element (n, i, h, d) at the strides below + d;
+                            * 16-byte aligned, strides >= 0 and multiples of 8              */
+  int64_t q_batch_stride, q_token_stride, q_head_stride;
+  int64_t batch;           /* sequences, at most 65535                                       */
+  int64_t q_len;           /* queries per sequence                                           */
+  int32_t q_heads;         /* a multiple of the cache's heads                                */
+  int32_t causal;
+  int64_t window;
+  float scale;
+  const int32_t* block_table; /* DEVICE int32 [batch, table_stride]: page of tokens
+                            * [j * page_size, (j + 1) * page_size) of sequence n at
+                            * n * table_stride + j.  Only entries of tokens that are seen are
+                            * read; one outside [0, pages) makes the outputs that need it NaN. */
+  int64_t table_stride;
+  int64_t max_blocks;      /* entries per sequence, <= table_stride                          */
+  const int32_t* lengths;  /* DEVICE int32 [batch]; a length outside [0, max_length] makes
+                            * the sequence's outputs NaN                                     */
+  int64_t max_length;      /* the most tokens any sequence has, known to the host: sizes the
+                            * launch; <= max_blocks * page_size                              */
+} qmm_kv_attend_t;
+
+/* Attention over the cache: out, DEVICE, dense [batch, q_len, q_heads, head_dim] of dtype,
+ * 16-byte aligned.  Scores, softmax and sums are float32.  workspace: DEVICE, 16-byte aligned,
+ * any content, at least qmm_kv_attend_workspace_bytes(cache, args) bytes (NULL when that is
+ * 0); one workspace serves any number of calls in stream order, calls that may overlap need
+ * their own.  The result depends only on the inputs (no atomics).  batch == 0 or q_len == 0 is
+ * a no-op.  One kernel is enqueued, or two when the tokens are split over workgroups. */
+int32_t qmm_kv_attend(const qmm_kv_cache_t* cache, const qmm_kv_attend_t* args, void* out, void* workspace,
+                      int64_t workspace_bytes, void* stream);
+
+/* Host-only: workspace bytes of a qmm_kv_attend call (its pointers may be NULL), or a negative
+ * error code.  Monotone in max_length: the bytes for the longest length serve every shorter
+ * one, with any window. */
+int64_t qmm_kv_attend_workspace_bytes(const qmm_kv_cache_t* cache, const qmm_kv_attend_t* args);
+
 #ifdef __cplusplus
 }
 #endif
