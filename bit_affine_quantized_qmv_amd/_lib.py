@@ -25,7 +25,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqmm.so")
 # Every symbol include/qmm.h declares.
 EXPORTS = ("qmm_abi_version", "qmm_last_error", "qmm_quantize", "qmv", "qmm_t", "qmm_plan", "qmm_gather_qmv",
            "qmm_dequantize", "qmm_embedding", "qmm_qmv_argmax", "qmm_qmv_argmax_noalloc", "qmm_topk",
-           "qmm_qmv_topk", "qmm_kv_append", "qmm_kv_read", "qmm_kv_attend", "qmm_kv_attend_workspace_bytes")
+           "qmm_qmv_topk", "qmm_kv_append", "qmm_kv_read", "qmm_kv_attend", "qmm_kv_attend_workspace_bytes", "qmm_sample")
 
 
 class TensorDesc(ctypes.Structure):
@@ -85,6 +85,17 @@ class KVAttendDesc(ctypes.Structure):
                 ("max_blocks", ctypes.c_int64),
                 ("lengths", ctypes.c_void_p),
                 ("max_length", ctypes.c_int64)]
+
+
+class SampleParams(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_void_p),
+                ("top_k", ctypes.c_void_p),
+                ("top_p", ctypes.c_void_p),
+                ("min_p", ctypes.c_void_p),
+                ("temperature_all", ctypes.c_float),
+                ("top_k_all", ctypes.c_int32),
+                ("top_p_all", ctypes.c_float),
+                ("min_p_all", ctypes.c_float)]
 
 
 class QmmError(RuntimeError):
@@ -151,6 +162,9 @@ def load() -> ctypes.CDLL:
     lib.qmm_kv_attend.argtypes = [ctypes.POINTER(KVCacheDesc), ctypes.POINTER(KVAttendDesc), P, P, ctypes.c_int64, P]
     lib.qmm_kv_attend_workspace_bytes.restype = ctypes.c_int64
     lib.qmm_kv_attend_workspace_bytes.argtypes = [ctypes.POINTER(KVCacheDesc), ctypes.POINTER(KVAttendDesc)]
+    lib.qmm_sample.restype = ctypes.c_int32
+    lib.qmm_sample.argtypes = [P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                               ctypes.POINTER(SampleParams), P, P, P, P, P]
     _lib = lib
     return lib
 

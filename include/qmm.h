@@ -353,6 +353,41 @@ int32_t qmm_kv_attend(const qmm_kv_cache_t* cache, const qmm_kv_attend_t* args, 
  * one, with any window. */
 int64_t qmm_kv_attend_workspace_bytes(const qmm_kv_cache_t* cache, const qmm_kv_attend_t* args);
 
+/* Settings of qmm_sample, per row: each is a DEVICE array [rows] (4-byte aligned) or, where the
+ * pointer is NULL, one number for every row. */
+typedef struct {
+  const float* temperature;   /* T; <= 0 or NaN: the first largest logit, whatever u is        */
+  const int32_t* top_k;       /* keep the top_k largest; <= 0: all                             */
+  const float* top_p;         /* keep the shortest prefix reaching this share; >= 1: all       */
+  const float* min_p;         /* keep weights of at least min_p times the largest; <= 0: all   */
+  float temperature_all;
+  int32_t top_k_all;
+  float top_p_all;
+  float min_p_all;
+} qmm_sample_params_t;
+
+/* Draw one column per logits row from given uniform numbers.  Logits that are NaN or -inf are
+ * never drawn; the others weigh W_i = floor(2^40 * exp((l_i - max l) / T)), the quotient and
+ * exponential in float32 (1 for l_i == max l).  In order of descending logit, equal ones by
+ * lower column, a row keeps its top_k first columns; of those the shortest prefix whose weights
+ * reach floor(top_p * 2^24) / 2^24 of their sum; of those the columns with
+ * exp((l_i - max l) / T) >= min_p.  The largest always stays.  The drawn column is the first,
+ * in column order, at which the running sum of the kept weights exceeds floor(u * 2^24) / 2^24
+ * of their whole sum.  Sums are exact integers: the result depends on nothing but the inputs.
+ * out_index: DEVICE int32 [rows], -1 for a row with nothing to draw (all NaN or -inf);
+ * out_prob: DEVICE float32 [rows] or NULL, the drawn column's share of the kept weights (0 with
+ * index -1).  u: DEVICE float32 [rows], clamped to [0, 1 - 2^-24] (NaN: 0).
+ * logits: DEVICE [rows, row_stride] of dtype (QMM_BF16 or QMM_FP16), 2-byte aligned,
+ * row_stride >= n.  Need 0 < n <= QMM_SAMPLE_MAX_N and rows <= 65535; rows == 0 is a no-op.
+ * workspace: DEVICE, 8-byte aligned, QMM_SAMPLE_WORKSPACE_BYTES(rows) of any content; one
+ * serves any number of calls in stream order, calls that may overlap need their own.
+ * Three kernels are enqueued; nothing is allocated. */
+#define QMM_SAMPLE_MAX_N (1 << 22)
+#define QMM_SAMPLE_WORKSPACE_BYTES(rows) (26624 * (int64_t)(rows))
+int32_t qmm_sample(const void* logits, int32_t dtype, int64_t rows, int64_t n, int64_t row_stride,
+                   const qmm_sample_params_t* params, const float* u, int32_t* out_index, float* out_prob,
+                   void* workspace, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
