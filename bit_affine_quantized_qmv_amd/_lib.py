@@ -25,7 +25,8 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqmm.so")
 # Every symbol include/qmm.h declares.
 EXPORTS = ("qmm_abi_version", "qmm_last_error", "qmm_quantize", "qmv", "qmm_t", "qmm_plan", "qmm_gather_qmv",
            "qmm_dequantize", "qmm_embedding", "qmm_qmv_argmax", "qmm_qmv_argmax_noalloc", "qmm_topk",
-           "qmm_qmv_topk", "qmm_kv_append", "qmm_kv_read", "qmm_kv_attend", "qmm_kv_attend_workspace_bytes", "qmm_sample")
+           "qmm_qmv_topk", "qmm_kv_append", "qmm_kv_read", "qmm_kv_attend", "qmm_kv_attend_workspace_bytes", "qmm_sample", "qmm_moe",
+           "qmm_moe_workspace_bytes")
 
 
 class TensorDesc(ctypes.Structure):
@@ -85,6 +86,28 @@ class KVAttendDesc(ctypes.Structure):
                 ("max_blocks", ctypes.c_int64),
                 ("lengths", ctypes.c_void_p),
                 ("max_length", ctypes.c_int64)]
+
+
+class ExpertStack(ctypes.Structure):
+    _fields_ = [("w", WeightDesc),
+                ("num_experts", ctypes.c_int64),
+                ("w_expert_stride", ctypes.c_int64),
+                ("sb_expert_stride", ctypes.c_int64)]
+
+
+class MoeDesc(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p),
+                ("x_stride", ctypes.c_int64),
+                ("router_logits", ctypes.c_void_p),
+                ("router_stride", ctypes.c_int64),
+                ("tokens", ctypes.c_int64),
+                ("top_k", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32),
+                ("dtype", ctypes.c_int32),
+                ("gate", ctypes.POINTER(ExpertStack)),
+                ("up", ctypes.POINTER(ExpertStack)),
+                ("down", ctypes.POINTER(ExpertStack)),
+                ("y_stride", ctypes.c_int64)]
 
 
 class SampleParams(ctypes.Structure):
@@ -165,6 +188,10 @@ def load() -> ctypes.CDLL:
     lib.qmm_sample.restype = ctypes.c_int32
     lib.qmm_sample.argtypes = [P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                                ctypes.POINTER(SampleParams), P, P, P, P, P]
+    lib.qmm_moe.restype = ctypes.c_int32
+    lib.qmm_moe.argtypes = [ctypes.POINTER(MoeDesc), P, P, ctypes.c_int64, P]
+    lib.qmm_moe_workspace_bytes.restype = ctypes.c_int64
+    lib.qmm_moe_workspace_bytes.argtypes = [ctypes.c_int64] * 5
     _lib = lib
     return lib
 

@@ -12,7 +12,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libqmm.so")
 SOURCES = ["decode_b4.hip", "decode_b8.hip", "decode_bn.hip", "decode.cpp", "prefill.hip", "dequant.hip", "quantize.hip", "topk.hip", "noalloc.hip",
-           "kv_cache.hip", "kv_attend_bf16.hip", "kv_attend_fp16.hip", "kv_capi.cpp", "sample.hip", "sample_capi.cpp",
+           "kv_cache.hip", "kv_attend_bf16.hip", "kv_attend_fp16.hip", "kv_capi.cpp", "sample.hip", "sample_capi.cpp", "moe_b4.hip", "moe_b8.hip", "moe_bn.hip", "moe_capi.cpp",
            "dispatch.cpp", "capi.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -353,6 +353,54 @@ int32_t qmm_kv_attend(const qmm_kv_cache_t* cache, const qmm_kv_attend_t* args, 
  * one, with any window. */
 int64_t qmm_kv_attend_workspace_bytes(const qmm_kv_cache_t* cache, const qmm_kv_attend_t* args);
 
+/* ---- A mixture-of-experts layer for a few tokens.
+ * Expert stack: num_experts quantized weights that share N, K, group_size, bits and dtype
+ * (w describes expert 0; expert e's codes are w_expert_stride words further, its scales and
+ * biases sb_expert_stride elements), as in qmm_gather_qmv. */
+typedef struct {
+  qmm_weight_desc_t w;
+  int64_t num_experts;
+  int64_t w_expert_stride;   /* words, >= N * w_row_stride                  */
+  int64_t sb_expert_stride;  /* elements, >= N * sb_row_stride              */
+} qmm_expert_stack_t;
+
+/* Per token t, with S_t its top_k largest router logits (equal ones: the lower expert; NaN
+ * counts as largest):
+ *     p_e = softmax of the router logits over S_t (renormalize) or over all experts,
+ *     y_t = sum_{e in S_t} p_e * ( silu(Wg_e x_t) * (Wu_e x_t) ) Wd_e^T,  silu(g) = g / (1 + exp(-g)).
+ * gate, up: [inter, hidden] per expert, sharing bits and group_size; down: [hidden, inter],
+ * any bits and group_size.  4- and 8-bit codes: w_packed 16-byte aligned, w_row_stride and
+ * w_expert_stride multiples of 4 words; other widths: any word. */
+typedef struct {
+  const void* x;               /* DEVICE [tokens, x_stride] of dtype, 16-byte aligned, x_stride % 8 == 0 */
+  int64_t x_stride;
+  const void* router_logits;   /* DEVICE [tokens, router_stride] of dtype, 2-byte aligned               */
+  int64_t router_stride;
+  int64_t tokens;              /* at most QMM_DECODE_MAX_ROWS                                           */
+  int32_t top_k;               /* at most QMM_MOE_MAX_TOP_K                                             */
+  int32_t renormalize;
+  int32_t dtype;
+  const qmm_expert_stack_t* gate;
+  const qmm_expert_stack_t* up;
+  const qmm_expert_stack_t* down;
+  int64_t y_stride;            /* elements between rows of y, >= hidden                                 */
+} qmm_moe_t;
+
+#define QMM_MOE_MAX_EXPERTS 512
+#define QMM_MOE_MAX_TOP_K 32
+
+/* The layer: y DEVICE [tokens, y_stride] of dtype, 2-byte aligned.  Products and sums in
+ * float32; p * silu(g) * u is rounded once to dtype before the product with Wd.  workspace:
+ * DEVICE, 16-byte aligned, qmm_moe_workspace_bytes(...) bytes of any content; one serves any
+ * number of calls in stream order, calls that may overlap need their own.  The result depends
+ * only on the inputs (no atomics).  tokens == 0 is a no-op.  Two kernels are enqueued, or
+ * three when the second product is split over workgroups. */
+int32_t qmm_moe(const qmm_moe_t* args, void* y, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Host-only: workspace bytes of qmm_moe for these sizes, or a negative error code.  Grows with
+ * every argument. */
+int64_t qmm_moe_workspace_bytes(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, int64_t inter);
+
 /* Settings of qmm_sample, per row: each is a DEVICE array [rows] (4-byte aligned) or, where the
  * pointer is NULL, one number for every row. */
 typedef struct {
