@@ -13,10 +13,15 @@
 // The draw runs over the kept columns in index order: u times their sum, located by sums over
 // ever shorter ranges.
 //
-// Three kernels, because the weights need the row's maximum and the histogram needs the whole
+// Four kernels, because the weights need the row's maximum and the threshold needs the whole
 // row: (1) each chunk's largest key and its first column; (2) each chunk's weights, into the
-// row's histogram or, for a row without top-k and top-p, as the chunk's sum; (3) one workgroup
-// per row finds the threshold and draws.
+// row's histogram or, for a row without top-k and top-p, as the chunk's sum; (3) the
+// threshold's bin, and each chunk's columns from that bin up, the candidates; (4) one
+// workgroup per row, with the candidates in its LDS, finds the threshold and draws.  Where
+// there are more candidates than LDS holds, (3) has left each chunk's weight above the bin and
+// its columns of each key in the bin, from which (4) finds the threshold and the chunk to draw
+// from.  What touches every column is spread over the chunks' workgroups: one workgroup takes
+// about 10 us for 10 instructions on each of 150000 columns.
 #include "device_common.hpp"
 #include "sample.hpp"
 
@@ -104,6 +109,22 @@ __device__ inline void load_keys(const uint16_t* row, int64_t i, int64_t end, bo
   }
 }
 
+// f(key) for the runs of columns at i, i + step, .. below end (key 0 past it); four runs are
+// loaded before the first is used.
+template <bool FP16, class F>
+__device__ inline void each_key(const uint16_t* row, int64_t i, int64_t end, int64_t step, bool vec, F&& f) {
+  constexpr int kAhead = 4;
+  for (; i < end; i += kAhead * step) {
+    uint32_t k[kAhead][kRun];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) load_keys<FP16>(row, i + j * step, end, vec, k[j]);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+      for (int e = 0; e < kRun; ++e) f(k[j][e]);
+  }
+}
+
 __device__ inline u64 shfl_xor64(u64 v, int d) {
   const uint32_t lo = __shfl_xor((uint32_t)v, d), hi = __shfl_xor((uint32_t)(v >> 32), d);
   return ((u64)hi << 32) | lo;
@@ -142,6 +163,7 @@ __global__ __launch_bounds__(kChunkThreads) void chunk_top_kernel(const SampleAr
     s.mass[i] = 0ull;
     s.count[i] = 0u;
   }
+  if (chunk == 0 && threadIdx.x == 0) s.found = 0u;
   const uint16_t* x = (const uint16_t*)a.logits + row * a.row_stride;
   const bool vec = ((uintptr_t)x & 15u) == 0u;
   const int64_t begin = chunk * a.chunk, end = min(a.n, begin + a.chunk);
@@ -229,98 +251,283 @@ struct Cut {
   uint32_t c;
 };
 
+// Shared state of a bin search.
+template <int THREADS>
+struct BinSearch {
+  u64 mass[THREADS / 64];
+  uint32_t count[THREADS / 64];
+  int bin;
+  u64 above_mass, total_mass;
+  uint32_t above_count;
+};
+
+// The bin (from the top) in which the running count reaches `want_count` or, when that is 0,
+// the running mass reaches want_mass(total mass); with the count and mass of the bins above
+// it.  Each thread owns consecutive bins, thread order being descending.  bin = -1: not
+// reached.
+template <int THREADS, class W>
+__device__ inline void find_bin(const RowSpace& s, uint32_t want_count, W&& want_mass, BinSearch<THREADS>& sh) {
+  constexpr int kPer = kBins / THREADS;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  u64 m[kPer], mt = 0;
+  uint32_t n[kPer], nt = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    m[i] = s.mass[kBins - 1 - (kPer * threadIdx.x + i)];
+    n[i] = s.count[kBins - 1 - (kPer * threadIdx.x + i)];
+    mt += m[i];
+    nt += n[i];
+  }
+  u64 mi = mt;
+  uint32_t ni = nt;
+  for (int d = 1; d < 64; d <<= 1) {
+    const u64 mo = shfl_up64(mi, d);
+    const uint32_t no = __shfl_up(ni, d);
+    if (lane >= d) {
+      mi += mo;
+      ni += no;
+    }
+  }
+  if (threadIdx.x == 0) sh.bin = -1;
+  if (lane == 63) {
+    sh.mass[wave] = mi;
+    sh.count[wave] = ni;
+  }
+  __syncthreads();
+  u64 mb = mi - mt, total = 0;
+  uint32_t nb = ni - nt;
+#pragma unroll
+  for (int w = 0; w < THREADS / 64; ++w) {
+    if (w < wave) {
+      mb += sh.mass[w];
+      nb += sh.count[w];
+    }
+    total += sh.mass[w];
+  }
+  const u64 need = want_mass(total);
+  if (threadIdx.x == 0) sh.total_mass = total;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const bool crosses = want_count ? nb < want_count && nb + n[i] >= want_count : mb < need && mb + m[i] >= need;
+    if (crosses) {
+      sh.bin = kBins - 1 - (kPer * (int)threadIdx.x + i);
+      sh.above_mass = mb;
+      sh.above_count = nb;
+    }
+    mb += m[i];
+    nb += n[i];
+  }
+  __syncthreads();
+}
+
+// Smallest key whose relative weight reaches min_p (keys' weights rise with the key), found by
+// one wave, 64 keys at a time.  Keys without a weight of their own (-inf and below) count as 0.
+template <class T>
+__device__ inline uint32_t smallest_key(uint32_t top_key, float top, float t, float min_p, int lane) {
+  constexpr uint32_t kLeast = 0x10000u - (T::kDtype == 2 ? 0xFC00u : 0xFF80u);   // key of the lowest finite value
+  if (!(min_p > 0.0f)) return 1u;
+  uint32_t lo = 0u;      // keys up to lo fail
+  for (int shift = 10; shift >= 0; shift = shift > 4 ? shift - 6 : (shift > 0 ? 0 : -1)) {
+    const uint32_t key = lo + ((uint32_t)(lane + 1) << shift);
+    const bool ok = key >= top_key || (key >= kLeast && weight<T>(key, top_key, top, t) >= min_p);
+    const u64 fails = __ballot(!ok);
+    const int n = fails == ~0ull ? 64 : __ffsll(~fails) - 1;   // leading lanes that fail
+    lo += (uint32_t)n << shift;
+  }
+  return lo + 1u;
+}
+
+// Chunk-parallel: the row's threshold bin (the same in every workgroup of the row), and the
+// chunk's columns that can lie above the threshold.
+template <class T>
+__global__ __launch_bounds__(kChunkThreads) void collect_kernel(const SampleArgs a) {
+  constexpr bool FP16 = T::kDtype == 2;
+  __shared__ BinSearch<kChunkThreads> sh;
+  __shared__ uint32_t wave_n[kChunkThreads / 64], first, low[kLow];
+  __shared__ u64 wave_mass[kChunkThreads / 64];
+  const int64_t row = blockIdx.y;
+  const int chunk = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  RowSpace& s = a.space[row];
+  const Row r = row_settings(a, row);
+  const u64 top_word = row_top(s, a.chunks, lane);
+  const uint32_t top_key = (uint32_t)(top_word >> 32);
+  const bool settled = top_key == 0u || r.greedy || !r.threshold();
+  if (settled) {
+    if (chunk == 0 && threadIdx.x == 0) {
+      s.plan.top = top_word;
+      s.plan.mode = top_key == 0u ? kNothing : (r.greedy ? kGreedy : kFree);
+    }
+    return;
+  }
+  const float top = key_value<T>(top_key);
+  int32_t mode = kAll, bin = 0;
+  if (r.k) {
+    find_bin(s, r.k, [](u64) { return 0ull; }, sh);
+    if (sh.bin >= 0) {
+      mode = kByCount;
+      bin = sh.bin;
+    }
+    __syncthreads();                       // sh is used again
+  }
+  if (mode == kAll && r.units < (1u << kUnitBits)) {
+    find_bin(s, 0u, [&](u64 total) { return max(1ull, share(total, r.units)); }, sh);
+    mode = kByMass;
+    bin = sh.bin;
+  }
+  const uint32_t min_key = smallest_key<T>(top_key, top, r.t, r.min_p, lane);
+  uint32_t edge = max(1u, (uint32_t)bin << kShift);
+  int32_t low_bin = bin;
+  if (mode != kByCount) {                  // with top-k the share is of the weights below min_p too
+    edge = max(edge, min_key);
+    low_bin = max(bin, (int32_t)(min_key >> kShift));
+  }
+  // more columns above the bin than the last kernel holds: none are stored
+  const bool store = mode == kAll || low_bin != bin || sh.above_count <= (uint32_t)kCandidates;
+  if (threadIdx.x < kLow) low[threadIdx.x] = 0u;
+  __syncthreads();
+  if (chunk == 0 && threadIdx.x == 0) {
+    RowPlan p;
+    p.top = top_word;
+    p.above_mass = sh.above_mass;          // (not used in mode kAll)
+    p.total_mass = sh.total_mass;
+    p.above_count = sh.above_count;
+    p.mode = mode;
+    p.bin = bin;
+    p.low_bin = low_bin;
+    p.min_key = min_key;
+    s.plan = p;
+    if (!store) s.found = kCandidates + 1;
+  }
+  const uint16_t* x = (const uint16_t*)a.logits + row * a.row_stride;
+  const bool vec = ((uintptr_t)x & 15u) == 0u;
+  const int64_t begin = chunk * a.chunk, end = min(a.n, begin + a.chunk);
+  u64 mass = 0;
+  for (int64_t base = begin; base < end; base += kRun * kChunkThreads) {
+    const int64_t i = base + kRun * threadIdx.x;
+    uint32_t k[kRun], n = 0;
+    float w[kRun];
+    load_keys<FP16>(x, i, end, vec, k);
+#pragma unroll
+    for (int e = 0; e < kRun; ++e) {
+      w[e] = k[e] >= edge ? weight<T>(k[e], top_key, top, r.t) : 0.0f;
+      n += k[e] >= edge ? 1u : 0u;
+      if ((int)(k[e] >> kShift) > low_bin) mass += weight_int(w[e]);
+      if (k[e] && (int)(k[e] >> kShift) == low_bin) atomicAdd(&low[k[e] & (kLow - 1)], 1u);
+    }
+    if (!store) continue;
+    uint32_t at = n;
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint32_t o = __shfl_up(at, d);
+      if (lane >= d) at += o;
+    }
+    if (lane == 63) wave_n[wave] = at;
+    at -= n;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      uint32_t all = 0;
+      for (int v = 0; v < kChunkThreads / 64; ++v) all += wave_n[v];
+      first = all ? atomicAdd(&s.found, all) : 0u;   // n <= 2^22: no wrap
+    }
+    __syncthreads();
+    at += first;
+    for (int v = 0; v < wave; ++v) at += wave_n[v];
+#pragma unroll
+    for (int e = 0; e < kRun; ++e)
+      if (k[e] >= edge) {
+        if (at < (uint32_t)kCandidates) {
+          s.candidate[at] = ((u64)k[e] << 32) | (uint32_t)(i + e);
+          s.weight[at] = w[e];
+        }
+        ++at;
+      }
+    __syncthreads();                       // wave_n and first are used again
+  }
+  mass = wave_sum64(mass);
+  if (lane == 0) wave_mass[wave] = mass;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int v = 1; v < kChunkThreads / 64; ++v) mass += wave_mass[v];
+    s.chunk_mass[chunk] = mass;
+  }
+  if (threadIdx.x < kLow) s.chunk_low[chunk][threadIdx.x] = low[threadIdx.x];
+}
+
 // Shared state of the row kernel.
 struct RowShared {
-  u64 scan_mass[kRowWaves];
-  uint32_t scan_count[kRowWaves];
+  BinSearch<kRowThreads> search;
   uint32_t low[kLow];
   u64 part_mass[kRowWaves];
   uint32_t part_ties[kRowWaves];
-  // results that one thread finds and all read
-  int bin;
-  u64 above_mass;
-  uint32_t above_count;
+  u64 slot_mass[64];
+  uint32_t slot_count[64];
   Cut cut;
   u64 kept_mass;
   int64_t begin, end;
   u64 target, before_mass, total;
   uint32_t before_ties;
+  u64 low_weight[kLow];
+  u64 chunk_mass[kMaxChunks];
+  uint32_t chunk_ties[kMaxChunks];
 };
 
-// The bin (from the top) in which the running count reaches `want_count` or, when that is 0,
-// the running mass reaches `want_mass`; with the count and mass of the bins above it.  Thread
-// i owns bins 2047 - 2i and 2046 - 2i, so thread order is descending.  bin = -1: not reached.
-__device__ inline void find_bin(const RowSpace& s, uint32_t want_count, u64 want_mass, RowShared& sh) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int b0 = kBins - 1 - 2 * threadIdx.x;
-  const u64 m0 = s.mass[b0], m1 = s.mass[b0 - 1];
-  const uint32_t n0 = s.count[b0], n1 = s.count[b0 - 1];
-  u64 m = m0 + m1;
-  uint32_t n = n0 + n1;
-  for (int d = 1; d < 64; d <<= 1) {
-    const u64 mo = shfl_up64(m, d);
-    const uint32_t no = __shfl_up(n, d);
-    if (lane >= d) {
-      m += mo;
-      n += no;
-    }
-  }
-  if (threadIdx.x == 0) sh.bin = -1;
-  if (lane == 63) {
-    sh.scan_mass[wave] = m;
-    sh.scan_count[wave] = n;
-  }
-  __syncthreads();
-  u64 mb = m - m0 - m1;
-  uint32_t nb = n - n0 - n1;
-  for (int w = 0; w < wave; ++w) {
-    mb += sh.scan_mass[w];
-    nb += sh.scan_count[w];
-  }
-  const auto crosses = [&](u64 mass_b, uint32_t count_b, u64 mm, uint32_t nn) {
-    return want_count ? (count_b < want_count && count_b + nn >= want_count)
-                      : (mass_b < want_mass && mass_b + mm >= want_mass);
-  };
-  if (crosses(mb, nb, m0, n0)) {
-    sh.bin = b0;
-    sh.above_mass = mb;
-    sh.above_count = nb;
-  } else if (crosses(mb + m0, nb + n0, m1, n1)) {
-    sh.bin = b0 - 1;
-    sh.above_mass = mb + m0;
-    sh.above_count = nb + n0;
-  }
-  __syncthreads();
-}
-
-// Columns of each key of one bin, into sh.low.
+// Columns of each key of one bin, into sh.low, from the whole row.
 template <bool FP16>
 __device__ inline void count_low(const uint16_t* x, int64_t n, bool vec, int bin, RowShared& sh) {
   if (threadIdx.x < kLow) sh.low[threadIdx.x] = 0u;
   __syncthreads();
-  for (int64_t i = kRun * threadIdx.x; i < n; i += kRun * kRowThreads) {
-    uint32_t k[kRun];
-    load_keys<FP16>(x, i, n, vec, k);
-#pragma unroll
-    for (int e = 0; e < kRun; ++e)
-      if (k[e] && (int)(k[e] >> kShift) == bin) atomicAdd(&sh.low[k[e] & (kLow - 1)], 1u);
-  }
+  each_key<FP16>(x, kRun * threadIdx.x, n, kRun * kRowThreads, vec, [&](uint32_t key) {
+    if (key && (int)(key >> kShift) == bin) atomicAdd(&sh.low[key & (kLow - 1)], 1u);
+  });
   __syncthreads();
+}
+
+// The cut inside a bin, by the first wave: lane i takes the bin's i-th key from the top, of
+// which sh.low columns exist (`have` of them under the cut `within`).  By count: where `left`
+// columns are reached; by mass: where the weight `left` is reached.  Nothing changes if it is
+// not reached.  *kept: weight of the bin's columns inside a cut by count.
+template <class T, class IW>
+__device__ inline void cut_bin(int bin, bool by_count, u64 left, Cut within, IW&& int_weight, RowShared& sh,
+                               u64 above_mass) {
+  if (threadIdx.x >= 64) return;
+  const int lane = threadIdx.x;
+  const uint32_t key = ((uint32_t)bin << kShift) + (uint32_t)(kLow - 1 - (lane & (kLow - 1)));
+  uint32_t have = lane < kLow ? sh.low[key & (kLow - 1)] : 0u;
+  have = key < within.t ? 0u : (key == within.t ? min(within.c, have) : have);
+  const u64 w = have ? int_weight(key) : 0ull;
+  const u64 step = by_count ? (u64)have : have * w;
+  u64 incl = step, mass = have * w;
+  for (int d = 1; d < 64; d <<= 1) {
+    const u64 o = shfl_up64(incl, d), mo = shfl_up64(mass, d);
+    if (lane >= d) {
+      incl += o;
+      mass += mo;
+    }
+  }
+  const u64 before = incl - step;
+  if (before < left && incl >= left) {     // one lane at most
+    const uint32_t c = by_count ? (uint32_t)(left - before) : (uint32_t)((left - before + w - 1) / w);
+    sh.cut = Cut{key, c};
+    if (by_count) sh.kept_mass = above_mass + mass - (have - c) * w;
+  }
 }
 
 template <class T>
 __global__ __launch_bounds__(kRowThreads) void row_kernel(const SampleArgs a) {
   constexpr bool FP16 = T::kDtype == 2;
   __shared__ RowShared sh;
+  extern __shared__ u64 cand[];            // [kCandidates], then their weights
+  float* const rel = (float*)(cand + kCandidates);
   const int64_t row = blockIdx.x;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const RowSpace& s = a.space[row];
   const Row r = row_settings(a, row);
-  const u64 top_word = row_top(s, a.chunks, lane);
-  const uint32_t top_key = (uint32_t)(top_word >> 32);
-  if (top_key == 0u || r.greedy) {
+  const RowPlan plan = s.plan;
+  const uint32_t found = s.found;
+  const uint32_t top_key = (uint32_t)(plan.top >> 32);
+  const int mode = plan.mode;
+  if (mode == kNothing || mode == kGreedy) {
     if (threadIdx.x == 0) {
-      a.out_index[row] = top_key ? (int32_t)(0xFFFFFFFFu - (uint32_t)top_word) : -1;
+      a.out_index[row] = top_key ? (int32_t)(0xFFFFFFFFu - (uint32_t)plan.top) : -1;
       if (a.out_prob) a.out_prob[row] = top_key ? 1.0f : 0.0f;
     }
     return;
@@ -328,116 +535,234 @@ __global__ __launch_bounds__(kRowThreads) void row_kernel(const SampleArgs a) {
   const float top = key_value<T>(top_key);
   const uint16_t* x = (const uint16_t*)a.logits + row * a.row_stride;
   const bool vec = ((uintptr_t)x & 15u) == 0u;
+  const bool threshold = mode != kFree;
   const auto int_weight = [&](uint32_t key) { return weight_int(weight<T>(key, top_key, top, r.t)); };
+  const uint32_t u_units = min(units_of(a.u[row]), (1u << kUnitBits) - 1u);
+
+  // ---- candidates in LDS: every column that can be drawn, when they fit
+  const bool held = threshold && found <= (uint32_t)kCandidates;
+  if (held) {
+    for (uint32_t i = threadIdx.x; i < found; i += kRowThreads) {
+      cand[i] = s.candidate[i];
+      rel[i] = s.weight[i];
+    }
+  }
+  // f(key, column, relative weight) for this thread's candidates (each reads what it wrote)
+  const auto each_candidate = [&](auto&& f) {
+    for (uint32_t i = threadIdx.x; i < found; i += kRowThreads) {
+      const u64 c = cand[i];
+      f((uint32_t)(c >> 32), (uint32_t)c, rel[i]);
+    }
+  };
+  // otherwise the chunks' sums lead to the chunk; only a top-k too wide to be held with a top-p
+  // inside it, whose bin the chunks do not know, is drawn from the whole row
+  const bool whole = threshold && !held && mode == kByCount && r.units < (1u << kUnitBits);
+  const auto low_of = [&](int bin) {
+    if (threshold && !held && !whole) {
+      if (threadIdx.x < kLow) sh.low[threadIdx.x] = 0u;
+      __syncthreads();
+      if (bin == plan.low_bin) {           // else min-p cuts above this bin
+        for (int c = threadIdx.x / kLow; c < a.chunks; c += kRowThreads / kLow) {
+          const uint32_t n = s.chunk_low[c][threadIdx.x % kLow];
+          if (n) atomicAdd(&sh.low[threadIdx.x % kLow], n);
+        }
+      }
+      __syncthreads();
+      return;
+    }
+    if (!held) {
+      count_low<FP16>(x, a.n, vec, bin, sh);
+      return;
+    }
+    if (threadIdx.x < kLow) sh.low[threadIdx.x] = 0u;
+    __syncthreads();
+    each_candidate([&](uint32_t key, uint32_t, float) {
+      if ((int)(key >> kShift) == bin) atomicAdd(&sh.low[key & (kLow - 1)], 1u);
+    });
+    __syncthreads();
+  };
 
   // ---- the cut
-  const bool threshold = r.threshold();
   Cut cut = {0u, 0u};                      // every key above 0: everything that can be drawn
   if (threshold) {
-    int k_bin = -1;
-    u64 k_above = 0;
-    if (r.k) {
-      find_bin(s, r.k, 0ull, sh);
-      k_bin = sh.bin;                      // -1: fewer than k columns can be drawn
-      k_above = sh.above_mass;
-    }
-    if (k_bin >= 0) {
-      count_low<FP16>(x, a.n, vec, k_bin, sh);
-      if (threadIdx.x == 0) {
-        uint32_t left = r.k - sh.above_count;
-        u64 kept = sh.above_mass;
-        for (int i = kLow - 1; i >= 0; --i) {
-          const uint32_t key = (uint32_t)(k_bin << kShift) + i, have = min(left, sh.low[i]);
-          if (have == 0u) continue;
-          kept += have * int_weight(key);
-          left -= have;
-          if (left == 0u) {
-            sh.cut = Cut{key, have};
-            break;
-          }
-        }
-        sh.kept_mass = kept;
-      }
-    } else {
-      u64 m = 0;
-      for (int i = threadIdx.x; i < kBins; i += kRowThreads) m += s.mass[i];
-      m = wave_sum64(m);
-      if (lane == 0) sh.part_mass[wave] = m;
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        m = 0;
-        for (int w = 0; w < kRowWaves; ++w) m += sh.part_mass[w];
-        sh.kept_mass = m;
-        sh.cut = cut;
-      }
-    }
-    __syncthreads();
-    cut = sh.cut;
-    const u64 kept = sh.kept_mass;
-    __syncthreads();                       // every thread has them before sh.cut changes
-    if (r.units < (1u << kUnitBits)) {
-      u64 need = share(kept, r.units);
-      need = need ? need : 1ull;           // the first column always stays
-      int bin = k_bin;
-      u64 above = k_above;
-      if (k_bin < 0 || need <= k_above) {
-        find_bin(s, 0u, need, sh);
-        bin = sh.bin;
-        above = sh.above_mass;
-        count_low<FP16>(x, a.n, vec, bin, sh);
-      }
-      if (threadIdx.x == 0) {
-        u64 left = need - above;
-        for (int i = kLow - 1; i >= 0; --i) {
-          const uint32_t key = (uint32_t)(bin << kShift) + i;
-          const uint32_t have = key < cut.t ? 0u : (key == cut.t ? min(cut.c, sh.low[i]) : sh.low[i]);
-          const u64 w = have ? int_weight(key) : 0ull;
-          if (w == 0ull) continue;
-          if (left <= have * w) {
-            sh.cut = Cut{key, (uint32_t)((left + w - 1) / w)};
-            break;
-          }
-          left -= have * w;
-        }
-      }
+    if (threadIdx.x == 0) sh.cut = cut;
+    if (mode != kAll) {
+      low_of(plan.bin);                    // (and a barrier)
+      if (mode == kByCount)
+        cut_bin<T>(plan.bin, true, r.k - plan.above_count, cut, int_weight, sh, plan.above_mass);
+      else
+        cut_bin<T>(plan.bin, false, max(1ull, share(plan.total_mass, r.units)) - plan.above_mass, cut, int_weight, sh,
+                   0ull);
       __syncthreads();
       cut = sh.cut;
     }
+    if (mode == kByCount && r.units < (1u << kUnitBits)) {
+      const u64 need = max(1ull, share(sh.kept_mass, r.units));
+      int bin = plan.bin;
+      u64 above = plan.above_mass;
+      __syncthreads();                     // every thread has the cut by count
+      if (need <= above) {
+        find_bin(s, 0u, [&](u64) { return need; }, sh.search);
+        bin = sh.search.bin;
+        above = sh.search.above_mass;
+        low_of(bin);
+      }
+      cut_bin<T>(bin, false, need - above, cut, int_weight, sh, 0ull);
+      __syncthreads();
+      cut = sh.cut;
+    }
+    if (cut.t < plan.min_key) cut = Cut{plan.min_key - 1u, 0u};   // min-p cuts higher
+  }
+  const u64 tie_w = cut.c ? int_weight(cut.t) : 0ull;
+
+  if (held) {
+    // ---- the draw among the candidates
+    u64 mass = 0;
+    uint32_t ties = 0;
+    each_candidate([&](uint32_t key, uint32_t, float w) {
+      if (key > cut.t) mass += weight_int(w);
+      ties += key == cut.t ? 1u : 0u;
+    });
+    mass = wave_sum64(mass);
+    for (int d = 1; d < 64; d <<= 1) ties += __shfl_xor(ties, d);
+    if (lane == 0) {
+      sh.part_mass[wave] = mass;
+      sh.part_ties[wave] = ties;
+    }
+    __syncthreads();
+    mass = 0;
+    ties = 0;
+#pragma unroll
+    for (int w = 0; w < kRowWaves; ++w) {
+      mass += sh.part_mass[w];
+      ties += sh.part_ties[w];
+    }
+    const u64 total = mass + cut.c * tie_w;      // c is at most the number of ties
+    u64 target = share(total, u_units);
+    // Columns are located six bits of their index at a time, from the highest that n needs.
+    int shift0 = 0;
+    while ((a.n - 1) >> (shift0 + 6)) shift0 += 6;
+    // The last column among the first c ties:
+    uint32_t limit = 0xFFFFFFFFu;
+    if (cut.c && cut.c < ties) {
+      uint32_t left = cut.c;
+      limit = 0u;
+      for (int shift = shift0; shift >= 0; shift -= 6) {
+        if (threadIdx.x < 64) sh.slot_count[threadIdx.x] = 0u;
+        __syncthreads();
+        each_candidate([&](uint32_t key, uint32_t col, float) {
+          if (key == cut.t && (col >> shift >> 6) == limit) atomicAdd(&sh.slot_count[(col >> shift) & 63u], 1u);
+        });
+        __syncthreads();
+        uint32_t incl = sh.slot_count[lane];
+        const uint32_t own = incl;
+        for (int d = 1; d < 64; d <<= 1) {
+          const uint32_t o = __shfl_up(incl, d);
+          if (lane >= d) incl += o;
+        }
+        const int at = __ffsll(__ballot(incl >= left)) - 1;
+        left -= __shfl(incl, at) - __shfl(own, at);
+        limit = (limit << 6) | (uint32_t)at;
+        __syncthreads();
+      }
+    }
+    // The column at which the running sum passes the target:
+    uint32_t prefix = 0u;
+    u64 last = 0;
+    for (int shift = shift0; shift >= 0; shift -= 6) {
+      if (threadIdx.x < 64) sh.slot_mass[threadIdx.x] = 0ull;
+      __syncthreads();
+      each_candidate([&](uint32_t key, uint32_t col, float w) {
+        const bool kept = key > cut.t || (key == cut.t && cut.c && col <= limit);
+        if (kept && (col >> shift >> 6) == prefix) atomicAdd(&sh.slot_mass[(col >> shift) & 63u], weight_int(w));
+      });
+      __syncthreads();
+      u64 incl = sh.slot_mass[lane];
+      const u64 own = incl;
+      for (int d = 1; d < 64; d <<= 1) {
+        const u64 o = shfl_up64(incl, d);
+        if (lane >= d) incl += o;
+      }
+      const int at = __ffsll(__ballot(incl > target)) - 1;
+      const u64 before = incl - own;
+      target -= ((u64)__shfl((uint32_t)(before >> 32), at) << 32) | __shfl((uint32_t)before, at);
+      last = ((u64)__shfl((uint32_t)(own >> 32), at) << 32) | __shfl((uint32_t)own, at);
+      prefix = (prefix << 6) | (uint32_t)at;
+      __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+      a.out_index[row] = (int32_t)prefix;
+      if (a.out_prob) a.out_prob[row] = (float)((double)last / (double)total);
+    }
+    return;
   }
 
-  // ---- the draw: sums over 16 equal parts of a range, then of the part that holds the target
-  const float tie_rel = cut.t ? weight<T>(cut.t, top_key, top, r.t) : 0.0f;
-  const u64 tie_w = tie_rel >= r.min_p ? weight_int(tie_rel) : 0ull;
+  // ---- the draw from the row itself: sums over 16 equal parts of a range, then of the part
+  // that holds the target
   const auto above_weight = [&](uint32_t key) -> u64 {
     if (key <= cut.t) return 0ull;
     const float w = weight<T>(key, top_key, top, r.t);
-    return w >= r.min_p ? weight_int(w) : 0ull;
+    return threshold || w >= r.min_p ? weight_int(w) : 0ull;   // a cut includes min_p
   };
-  bool first = true;
-  if (threadIdx.x == 0) {
-    sh.begin = 0;
-    sh.end = a.n;
-    sh.before_mass = 0ull;
-    sh.before_ties = 0u;
-    if (!threshold) {                      // the chunks' sums are there already
-      u64 total = 0;
-      for (int c = 0; c < a.chunks; ++c) total += s.chunk_mass[c];
-      sh.total = total;
-      sh.target = share(total, min(units_of(a.u[row]), (1u << kUnitBits) - 1u));
-      u64 before = 0;
-      for (int c = 0; c < a.chunks; ++c) {
-        const u64 m = s.chunk_mass[c];
-        if (before + m > sh.target) {
-          sh.begin = c * a.chunk;
-          sh.end = min(a.n, sh.begin + a.chunk);
-          break;
-        }
-        before += m;
+  bool first = whole;
+  if (whole) {
+    if (threadIdx.x == 0) {
+      sh.begin = 0;
+      sh.end = a.n;
+      sh.before_mass = 0ull;
+      sh.before_ties = 0u;
+    }
+  } else {
+    // each chunk's kept weight but for its ties, and its ties: eight threads per chunk
+    if (threadIdx.x < kLow) {
+      const uint32_t key = ((uint32_t)plan.low_bin << kShift) + threadIdx.x;
+      sh.low_weight[threadIdx.x] = threshold && key > cut.t && key <= top_key ? int_weight(key) : 0ull;
+    }
+    __syncthreads();
+    const bool tied = threshold && cut.c && (int)(cut.t >> kShift) == plan.low_bin;
+    for (int c = threadIdx.x / 8; c < a.chunks; c += kRowThreads / 8) {
+      u64 m = 0;
+      if (threshold)
+        for (int i = threadIdx.x % 8; i < kLow; i += 8) m += s.chunk_low[c][i] * sh.low_weight[i];
+      for (int d = 1; d < 8; d <<= 1) m += shfl_xor64(m, d);
+      if (threadIdx.x % 8 == 0) {
+        sh.chunk_mass[c] = m + s.chunk_mass[c];
+        sh.chunk_ties[c] = tied ? s.chunk_low[c][cut.t & (kLow - 1)] : 0u;
       }
-      sh.before_mass = before;
+    }
+    __syncthreads();
+    if (wave == 0) {                       // two chunks per lane
+      const int c0 = 2 * lane, c1 = c0 + 1;
+      const uint32_t t0 = c0 < a.chunks ? sh.chunk_ties[c0] : 0u, t1 = c1 < a.chunks ? sh.chunk_ties[c1] : 0u;
+      uint32_t ti = t0 + t1;
+      for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t o = __shfl_up(ti, d);
+        if (lane >= d) ti += o;
+      }
+      const uint32_t tb = ti - t0 - t1;    // ties before the lane's chunks
+      const auto ties_kept = [&](uint32_t before, uint32_t n) { return min(n, cut.c > before ? cut.c - before : 0u); };
+      const u64 m0 = c0 < a.chunks ? sh.chunk_mass[c0] + ties_kept(tb, t0) * tie_w : 0ull;
+      const u64 m1 = c1 < a.chunks ? sh.chunk_mass[c1] + ties_kept(tb + t0, t1) * tie_w : 0ull;
+      u64 incl = m0 + m1;
+      for (int d = 1; d < 64; d <<= 1) {
+        const u64 o = shfl_up64(incl, d);
+        if (lane >= d) incl += o;
+      }
+      const u64 total = ((u64)__shfl((uint32_t)(incl >> 32), 63) << 32) | __shfl((uint32_t)incl, 63);
+      const u64 target = share(total, u_units), before = incl - m0 - m1;
+      if (before <= target && incl > target) {       // one lane
+        const bool second = before + m0 <= target;
+        sh.begin = (c0 + (second ? 1 : 0)) * a.chunk;
+        sh.end = min(a.n, sh.begin + a.chunk);
+        sh.before_mass = before + (second ? m0 : 0ull);
+        sh.before_ties = tb + (second ? t0 : 0u);
+      }
+      if (lane == 0) {
+        sh.total = total;
+        sh.target = target;
+      }
     }
   }
-  if (!threshold) first = false;
   __syncthreads();
   while (first || sh.end - sh.begin > kStep) {
     const int64_t begin = sh.begin, end = sh.end;
@@ -445,18 +770,13 @@ __global__ __launch_bounds__(kRowThreads) void row_kernel(const SampleArgs a) {
     const int64_t p0 = begin + wave * part, p1 = min(end, p0 + part);
     u64 mass = 0;
     uint32_t ties = 0;
-    for (int64_t i = p0 + kRun * lane; i < p1; i += kStep) {
-      uint32_t k[kRun];
-      load_keys<FP16>(x, i, p1, vec, k);
-#pragma unroll
-      for (int e = 0; e < kRun; ++e) {
-        if (k[e] == 0u || k[e] < cut.t) continue;
-        if (k[e] == cut.t)
-          ++ties;
-        else
-          mass += above_weight(k[e]);
-      }
-    }
+    each_key<FP16>(x, p0 + kRun * lane, p1, kStep, vec, [&](uint32_t key) {
+      if (key == 0u || key < cut.t) return;
+      if (key == cut.t)
+        ++ties;
+      else
+        mass += above_weight(key);
+    });
     mass = wave_sum64(mass);
     for (int d = 1; d < 64; d <<= 1) ties += __shfl_xor(ties, d);
     if (lane == 0) {
@@ -478,7 +798,7 @@ __global__ __launch_bounds__(kRowThreads) void row_kernel(const SampleArgs a) {
           t += sh.part_ties[w];
         }
         sh.total = total;
-        sh.target = share(total, min(units_of(a.u[row]), (1u << kUnitBits) - 1u));
+        sh.target = share(total, u_units);
       }
       u64 before = sh.before_mass;
       uint32_t t = sh.before_ties;
@@ -550,7 +870,13 @@ hipError_t launch(const SampleArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL((chunk_weights_kernel<T>), chunks, dim3(kChunkThreads), 0, stream, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((row_kernel<T>), dim3((unsigned)a.rows), dim3(kRowThreads), 0, stream, a);
+  hipLaunchKernelGGL((collect_kernel<T>), chunks, dim3(kChunkThreads), 0, stream, a);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  constexpr int kLds = kCandidates * 12;
+  e = hipFuncSetAttribute((const void*)row_kernel<T>, hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((row_kernel<T>), dim3((unsigned)a.rows), dim3(kRowThreads), kLds, stream, a);
   return hipGetLastError();
 }
 

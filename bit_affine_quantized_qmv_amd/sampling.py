@@ -8,7 +8,7 @@ import torch
 from . import _lib
 from .api import _dtype_code, _stream
 
-_WORKSPACE_BYTES = 26624    # per row
+_WORKSPACE_BYTES = 190520    # per row
 
 
 def sample_workspace(rows: int, device) -> torch.Tensor:

@@ -429,9 +429,9 @@ typedef struct {
  * row_stride >= n.  Need 0 < n <= QMM_SAMPLE_MAX_N and rows <= 65535; rows == 0 is a no-op.
  * workspace: DEVICE, 8-byte aligned, QMM_SAMPLE_WORKSPACE_BYTES(rows) of any content; one
  * serves any number of calls in stream order, calls that may overlap need their own.
- * Three kernels are enqueued; nothing is allocated. */
+ * Four kernels are enqueued; nothing is allocated. */
 #define QMM_SAMPLE_MAX_N (1 << 22)
-#define QMM_SAMPLE_WORKSPACE_BYTES(rows) (26624 * (int64_t)(rows))
+#define QMM_SAMPLE_WORKSPACE_BYTES(rows) (190520 * (int64_t)(rows))
 int32_t qmm_sample(const void* logits, int32_t dtype, int64_t rows, int64_t n, int64_t row_stride,
                    const qmm_sample_params_t* params, const float* u, int32_t* out_index, float* out_prob,
                    void* workspace, void* stream);
