@@ -10,6 +10,8 @@ namespace moe {
 constexpr int kMaxTokens = 32;
 constexpr int kMaxExperts = 512;
 constexpr int kMaxTopK = 32;
+constexpr int kWaves = 4;             // per workgroup
+constexpr int kMaxSplits = 16;
 
 // A stack of quantized weights, [experts][N][K].
 struct Stack {
@@ -40,20 +42,19 @@ struct MoeArgs {
   uint16_t* y;               // [tokens, y_stride]
   int64_t y_stride;
   // workspace
-  int32_t* active;           // [1 + experts]: number of experts in use, then their indices, ascending
-  int16_t* row_of;           // [experts in use][kMaxTokens]: row of h of the token with this expert, or -1
-  uint16_t* h;               // [tokens * top_k][inter]: w * silu(gate) * up
-  float* part;               // [splits][tokens][hidden] sums of the second kernel's splits
-  // launch shape
-  int32_t parts;             // waves that share one tile of the first kernel, each a part of K
-  int32_t splits;            // workgroups that share one tile of the second kernel
-  int32_t cuts;              // pieces of each expert's K in the second kernel
+  int32_t* pair_expert;      // [tokens * top_k]: pair t * top_k + i is token t's i-th largest router logit
+  float* pair_share;         // [tokens * top_k]: its unnormalised weight
+  uint16_t* h;               // [tokens * top_k][2][inter]: silu(gate) * up, leading bits and the rest
+  float* out;                // [tokens * top_k][splits][hidden]: each pair's product with down
+  // waves that share one tile, each a part of K, and workgroups per expert, in the first and
+  // the second kernel; stretches of K that different workgroups of the second kernel take
+  int32_t parts, down_parts, blocks, down_blocks, splits;
 };
 
 hipError_t launch_b4(const MoeArgs& a, hipStream_t stream, bool down);
 hipError_t launch_b8(const MoeArgs& a, hipStream_t stream, bool down);
 hipError_t launch_bn(const MoeArgs& a, hipStream_t stream, bool down);
-hipError_t launch_join(const MoeArgs& a, hipStream_t stream);
+hipError_t launch_sum(const MoeArgs& a, hipStream_t stream);
 
 }  // namespace moe
 }  // namespace qmm

@@ -1,5 +1,5 @@
-// Mixture-of-experts layer, 2-, 3-, 5- and 6-bit expert weights, and the join of the second
-// kernel's splits.
+// Mixture-of-experts layer, 2-, 3-, 5- and 6-bit expert weights, and the sum over a
+// token's choices.
 #include "moe_impl.hpp"
 
 namespace qmm {
@@ -17,28 +17,34 @@ hipError_t launch_bn(const MoeArgs& a, hipStream_t stream, bool down) {
 
 namespace {
 
-constexpr int kJoinThreads = 256;
+constexpr int kSumThreads = 256;
 
-// y = the splits' sums added in split order, rounded to dtype.
+// y_t = sum of t's pairs, each by its share, in the order of its choices, rounded to dtype.
 template <class T>
-__global__ __launch_bounds__(kJoinThreads) void join_kernel(const MoeArgs a) {
-  const int64_t i = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x;
-  const int64_t n = (int64_t)a.tokens * a.hidden;
-  if (i >= n) return;
-  float v = 0.f;
-  for (int s = 0; s < a.splits; ++s) v += a.part[s * n + i];
-  const int64_t t = i / a.hidden;
-  a.y[t * a.y_stride + (i - t * a.hidden)] = T::from_f32(v);
+__global__ __launch_bounds__(kSumThreads) void sum_kernel(const MoeArgs a) {
+  const int n = (int)(blockIdx.x * kSumThreads + threadIdx.x), t = blockIdx.y;
+  if (n >= a.hidden) return;
+  const float* o = a.out + (int64_t)t * a.top_k * a.splits * a.hidden + n;
+  const float* share = a.pair_share + t * a.top_k;
+  float v = 0.f, sum = 0.f;
+  for (int i = 0; i < a.top_k; ++i) {
+    float w = 0.f;
+#pragma unroll 4
+    for (int z = 0; z < a.splits; ++z) w += o[(int64_t)(i * a.splits + z) * a.hidden];
+    v = __builtin_fmaf(share[i], w, v);
+    sum += share[i];
+  }
+  a.y[t * a.y_stride + n] = T::from_f32(a.renormalize ? v / sum : v);
 }
 
 }  // namespace
 
-hipError_t launch_join(const MoeArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)(((int64_t)a.tokens * a.hidden + kJoinThreads - 1) / kJoinThreads));
+hipError_t launch_sum(const MoeArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)((a.hidden + kSumThreads - 1) / kSumThreads), (unsigned)a.tokens);
   if (a.dtype == 1)
-    hipLaunchKernelGGL(join_kernel<Bf16>, grid, dim3(kJoinThreads), 0, stream, a);
+    hipLaunchKernelGGL(sum_kernel<Bf16>, grid, dim3(kSumThreads), 0, stream, a);
   else
-    hipLaunchKernelGGL(join_kernel<Fp16>, grid, dim3(kJoinThreads), 0, stream, a);
+    hipLaunchKernelGGL(sum_kernel<Fp16>, grid, dim3(kSumThreads), 0, stream, a);
   return hipGetLastError();
 }
 

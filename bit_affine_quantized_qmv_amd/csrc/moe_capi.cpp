@@ -16,15 +16,18 @@ static_assert(kMaxTokens == QMM_DECODE_MAX_ROWS && kMaxExperts == QMM_MOE_MAX_EX
                   kMaxTopK == QMM_MOE_MAX_TOP_K,
               "limits of the ABI");
 
-constexpr int kMaxSplits = 8;
-
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 
-// Workspace regions, in this order: active, row_of, h, part.
-int64_t active_bytes(int64_t experts) { return align256(4 * (1 + experts)); }
-int64_t row_of_bytes(int64_t experts) { return align256(2 * experts * kMaxTokens); }
-int64_t h_bytes(int64_t tokens, int64_t top_k, int64_t inter) { return align256(2 * tokens * top_k * inter); }
-int64_t part_bytes(int64_t tokens, int64_t hidden) { return align256(4 * kMaxSplits * tokens * hidden); }
+// Workspace regions, in this order: pair_expert, pair_share, h, out.
+int64_t pair_bytes(int64_t tokens, int64_t top_k) { return align256(4 * tokens * top_k); }
+int64_t h_bytes(int64_t tokens, int64_t top_k, int64_t inter) { return align256(4 * tokens * top_k * inter); }
+int64_t out_bytes(int64_t tokens, int64_t top_k, int64_t hidden, int64_t splits) {
+  return align256(4 * tokens * top_k * splits * hidden);
+}
+
+// Stretches of inter that different workgroups of the second kernel take: about 6144 columns
+// each, of which LDS holds two tokens' operands at once.
+int64_t splits_of(int64_t inter) { return std::min<int64_t>(kMaxSplits, (inter + 6143) / 6144); }
 
 int32_t check_stack(const char* name, const qmm_expert_stack_t* k, int64_t n, int64_t cols, int32_t experts,
                     int32_t dtype, Stack* out) {
@@ -90,8 +93,7 @@ int64_t qmm_moe_workspace_bytes(int64_t tokens, int64_t experts, int64_t top_k, 
     const int32_t rc = moe::check_sizes(tokens, experts, top_k, hidden, inter);
     if (rc != QMM_OK) return rc;
     report(QMM_OK, "");
-    return moe::active_bytes(experts) + moe::row_of_bytes(experts) + moe::h_bytes(tokens, top_k, inter) +
-           moe::part_bytes(tokens, hidden);
+    return 2 * moe::pair_bytes(tokens, top_k) + moe::h_bytes(tokens, top_k, inter) + moe::out_bytes(tokens, top_k, hidden, moe::splits_of(inter));
   });
 }
 
@@ -133,36 +135,37 @@ int32_t qmm_moe(const qmm_moe_t* m, void* y, void* workspace, int64_t workspace_
     a.dtype = m->dtype;
     a.y = (uint16_t*)y;
     a.y_stride = m->y_stride;
-    const int64_t need = moe::active_bytes(experts) + moe::row_of_bytes(experts) +
-                         moe::h_bytes(m->tokens, m->top_k, inter) + moe::part_bytes(m->tokens, hidden);
+    const int64_t need = 2 * moe::pair_bytes(m->tokens, m->top_k) + moe::h_bytes(m->tokens, m->top_k, inter) +
+                         moe::out_bytes(m->tokens, m->top_k, hidden, moe::splits_of(inter));
     if (workspace_bytes < need)
       return report(QMM_ERR_SHAPE, "moe: workspace of " + std::to_string(workspace_bytes) + " bytes, needs " +
                                        std::to_string(need));
     char* ws = (char*)workspace;
-    a.active = (int32_t*)ws;
-    ws += moe::active_bytes(experts);
-    a.row_of = (int16_t*)ws;
-    ws += moe::row_of_bytes(experts);
+    a.pair_expert = (int32_t*)ws;
+    ws += moe::pair_bytes(m->tokens, m->top_k);
+    a.pair_share = (float*)ws;
+    ws += moe::pair_bytes(m->tokens, m->top_k);
     a.h = (uint16_t*)ws;
     ws += moe::h_bytes(m->tokens, m->top_k, inter);
-    a.part = (float*)ws;
+    a.out = (float*)ws;
 
-    // Experts that can be in use at once.
-    const int64_t used = std::min<int64_t>(experts, m->tokens * m->top_k);
-    // First kernel: enough waves for 16 per compute unit, each of at least two slots.
-    const int64_t tiles = (inter + 15) / 16 * used, slots = moe::slots_of(hidden, a.gate.bits, a.gate.group_size);
-    a.parts = 1;
-    while (a.parts < 8 && tiles * a.parts < 4096 && slots >= 4 * a.parts) a.parts *= 2;
-    // Second kernel: workgroups for every compute unit, pieces for every wave of them.
-    const int64_t cols = (hidden + 15) / 16, slots2 = moe::slots_of(inter, a.down.bits, a.down.group_size);
-    a.splits = 1;
-    while (a.splits < moe::kMaxSplits && cols * a.splits < 256 && used * slots2 >= 32 * a.splits) a.splits *= 2;
-    a.cuts = 1;
-    while (used * a.cuts < 8 * a.splits && slots2 >= 4 * a.cuts) a.cuts *= 2;
+    a.splits = (int32_t)moe::splits_of(inter);
+    // Waves per tile: each with at least four slots.  Workgroups per expert: three for every
+    // compute unit in all, each with several tiles.
+    const int64_t used = std::min<int64_t>(experts, m->tokens * m->top_k);   // experts in use at most
+    const auto parts = [](int64_t slots) { return slots >= 16 ? 4 : (slots >= 8 ? 2 : 1); };
+    const auto blocks = [&](int64_t tiles, int64_t part, int64_t per_tile) {
+      const int64_t units = (tiles * part + moe::kWaves - 1) / moe::kWaves;
+      return (int32_t)std::min(units, std::max<int64_t>(1, 768 / (used * per_tile)));
+    };
+    a.parts = parts(moe::slots_of(hidden, a.gate.bits, a.gate.group_size));
+    a.down_parts = parts(moe::slots_of(inter, a.down.bits, a.down.group_size) / a.splits);
+    a.blocks = blocks((inter + 15) / 16, a.parts, 1);
+    a.down_blocks = blocks((hidden + 31) / 32, a.down_parts, a.splits);
     hipStream_t s = (hipStream_t)stream;
     hipError_t e = moe::launch(a, a.gate.bits, false, s);
     if (e == hipSuccess) e = moe::launch(a, a.down.bits, true, s);
-    if (e == hipSuccess && a.splits > 1) e = moe::launch_join(a, s);
+    if (e == hipSuccess) e = moe::launch_sum(a, s);
     return report_launch(e);
   });
 }

@@ -1,22 +1,30 @@
 // Mixture-of-experts layer for up to 32 tokens over quantized expert stacks:
 //     S_t  = the top_k largest router logits of token t (equal ones: lower expert),
 //     w_te = softmax over S_t (renormalize) or over all experts, taken at e,
-//     y_t  = sum_{e in S_t}  ( w_te silu(Wg_e x_t) * (Wu_e x_t) ) Wd_e^T.
+//     y_t  = sum_{e in S_t}  w_te ( silu(Wg_e x_t) * (Wu_e x_t) ) Wd_e^T.
 //
 // The layer reads each chosen expert's weights once and little else, so it is bound by that
-// stream (and, for one token, by latency).  Two kernels: the products with Wg and Wu together,
-// since both take x and the activation needs both, then the product with Wd.
+// stream (and, for one token, by latency).  Three kernels: the products with Wg and Wu
+// together, since both take x and the activation needs both; the product with Wd, for every
+// (token, choice) pair; and the sum over a token's choices.
 //
-// Both kernels give every wave one 16-row tile of weights (16 rows of Wg and the same of Wu,
-// or 16 rows of Wd) and one stretch of K, and load the activations' operands straight from
-// global memory: x and h are small and stay in L2, only the rows of tokens that use the
-// expert are loaded, and no wave waits for another before its weights are in flight.  The
-// matrix-core operand's 16 (or 32) activation rows are the call's tokens, rows of tokens
-// that do not use the expert being zero: sums over several experts then stay in the same
-// accumulators.  Arithmetic per output as in the decode kernels, s * sum xq + b * sum x per
-// group with exact integer codes and float32 sums; here sum x comes from a second product
-// with an all-ones operand, which costs nothing beside the weight stream.
-// h = w silu(g) u is rounded once to dtype, as the second product's operand.
+// Routing is not a kernel of its own.  A workgroup of the first kernel works for one expert e
+// and only has to know which tokens chose it: token t did if fewer than top_k of its logits
+// beat logit e, one pass over the logits.  The weights stay unnormalised, exp(l_te - max l_t),
+// until the last kernel has every chosen expert of a token and divides by their sum.
+//
+// Streams: a wave takes two 16-row tiles of weights (the same rows of Wg and Wu, or 32 rows of
+// Wd) and a stretch of K, with kDepth slots of loads in flight.  The activations of the
+// expert's tokens (up to 16 per pass over the weights; an expert seldom has more) are staged
+// in LDS in operand order: fetched from global memory they would share the memory counter
+// with the weights, which retires loads in order, and take the registers of three more slots.
+// No load is conditional: addresses are clamped into the row, and what a clamp repeats is
+// multiplied by zero.
+// Arithmetic per output as in the decode kernels, s * sum xq + b * sum x per group with exact
+// integer codes and float32 sums; sum x comes from a product with an all-ones operand.
+// h = silu(g) u reaches the second product as two operands of the element type, its leading
+// bits and the rest: the one rounding that a single operand would add is as large as the
+// output's own.
 #pragma once
 
 #include "decode_impl.hpp"
@@ -26,15 +34,15 @@ namespace qmm {
 namespace moe {
 
 using decode::generic_lane_offsets;
-using decode::load_slot;
+using decode::SbRegs;
 using decode::Slot;
 using decode::slot_codes;
 using decode::SlotData;
 using decode::slot_reorder;
 
-constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kExpertRegs = kMaxExperts / 64;   // router logits of one token per lane
+constexpr int kWorkgroups = 3;       // per compute unit: 168 registers per thread
+constexpr int kXBytes = 40 * 1024;   // LDS of the staged activations
 
 // Order key of a 16-bit float: larger values have larger keys, NaN the largest.
 template <class T>
@@ -45,369 +53,493 @@ __device__ inline uint32_t order_key(uint32_t b) {
   return (b & 0x8000u) ? (~b & 0xFFFFu) : (b | 0x8000u);
 }
 
+// Largest v of the wave, in every lane: row-local steps, then the row broadcasts.
 __device__ inline uint32_t wave_max(uint32_t v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint32_t o = __shfl_xor(v, d);
-    v = o > v ? o : v;
-  }
-  return v;
-}
-__device__ inline float wave_sum(float v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-  return v;
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));    // quad_perm [1,0,3,2]
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));    // quad_perm [2,3,0,1]
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));   // row_half_mirror
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));   // row_mirror
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false));   // row_bcast:15
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false));   // row_bcast:31
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-// The call's routing, in LDS.
-struct Routing {
-  uint32_t chosen[kMaxTokens][kMaxExperts / 32];   // bit e: token uses expert e
-  float top[kMaxTokens];                           // largest router logit
-  float inv[kMaxTokens];                           // 1 / the softmax sum
-  uint32_t any[kMaxExperts / 32];                  // experts that some token uses
+// The expert with rank n (0: the largest logit) of a token's logits, by one wave: n + 1 rounds
+// of the largest (key, lower expert first) word below the last one.
+template <class T>
+__device__ inline int expert_of_rank(const uint16_t* logits, int experts, int n, int lane) {
+  constexpr int kRegs = kMaxExperts / 64;
+  uint32_t word[kRegs];
+#pragma unroll
+  for (int j = 0; j < kRegs; ++j) {
+    const int e = 64 * j + lane;
+    word[j] = e < experts ? (order_key<T>(logits[e]) << 9) | (uint32_t)(kMaxExperts - 1 - e) : 0u;
+  }
+  uint32_t best = 0xFFFFFFFFu;
+  for (int i = 0; i <= n; ++i) {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int j = 0; j < kRegs; ++j) m = word[j] < best ? max(m, word[j]) : m;
+    best = wave_max(m);
+  }
+  return kMaxExperts - 1 - (int)(best & (kMaxExperts - 1));
+}
+
+// The tokens that chose an expert, in LDS, ascending.
+struct Users {
+  int16_t token[kMaxTokens];
+  int16_t pair[kMaxTokens];     // t * top_k + which of t's choices it is
+  float share[kMaxTokens];      // exp(l_te - max l_t), over the sum of all experts unless renormalised
+  int16_t pair_of[kMaxTokens];  // by token, -1: not chosen
+  float share_of[kMaxTokens];
+  int count;
 };
 
-// Fill r (every workgroup does: a token's choice costs one wave top_k rounds of a maximum).
+// Compact pair_of (and share_of) into the ascending lists, by the first wave; with the barriers.
+__device__ inline void list_users(const MoeArgs& a, Users& u) {
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    const bool use = (int)threadIdx.x < a.tokens && u.pair_of[threadIdx.x] >= 0;
+    const uint64_t m = __ballot(use);
+    if (use) {
+      const int i = __popcll(m & ((1ull << threadIdx.x) - 1));
+      u.token[i] = (int16_t)threadIdx.x;
+      u.pair[i] = u.pair_of[threadIdx.x];
+      u.share[i] = u.share_of[threadIdx.x];
+    }
+    if (threadIdx.x == 0) u.count = __popcll(m);
+  }
+  __syncthreads();
+}
+
+// Fill u from the router logits; 8 to 64 lanes per token.
 template <class T>
-__device__ inline void route(const MoeArgs& a, Routing& r) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int t = wave; t < a.tokens; t += kWaves) {
+__device__ inline void find_users(const MoeArgs& a, int e, Users& u) {
+  const int per = a.tokens > 16 ? 8 : (a.tokens > 8 ? 16 : (a.tokens > 4 ? 32 : 64));   // tokens * per <= kThreads
+  const int t = threadIdx.x / per, i = threadIdx.x & (per - 1);
+  if (t < a.tokens) {
     const uint16_t* logits = a.router + t * a.router_stride;
-    // (key, lowest expert first) words; experts are below 2^9
-    uint32_t word[kExpertRegs];
-    float v[kExpertRegs];
-#pragma unroll
-    for (int j = 0; j < kExpertRegs; ++j) {
-      const int e = 64 * j + lane;
-      word[j] = 0u;
-      v[j] = 0.f;
-      if (64 * j < a.experts && e < a.experts) {
-        const uint32_t b = logits[e];
-        word[j] = (order_key<T>(b) << 9) | (uint32_t)(kMaxExperts - 1 - e);
-        v[j] = T::to_f32(b);
-      }
+    const uint32_t mine = (order_key<T>(logits[e]) << 9) | (uint32_t)(kMaxExperts - 1 - e);
+    uint32_t top = 0u;
+    int beats = 0;
+#pragma unroll 4
+    for (int j = i; j < a.experts; j += per) {
+      const uint32_t key = order_key<T>(logits[j]);
+      beats += ((key << 9) | (uint32_t)(kMaxExperts - 1 - j)) > mine ? 1 : 0;
+      top = max(top, key);
     }
-    uint32_t mine = 0u;            // lane i < 16 collects bits 32 i .. 32 i + 31
-    float top = 0.f, sum = 0.f;
-    for (int i = 0; i < a.top_k; ++i) {
-      uint32_t best = 0u;
-#pragma unroll
-      for (int j = 0; j < kExpertRegs; ++j) best = word[j] > best ? word[j] : best;
-      best = wave_max(best);
-      const int e = kMaxExperts - 1 - (int)(best & (kMaxExperts - 1));
-      const float l = T::to_f32(logits[e]);
-      if (i == 0) top = l;
-      sum += expf(l - top);
-      if (lane == (e >> 5)) mine |= 1u << (e & 31);
-#pragma unroll
-      for (int j = 0; j < kExpertRegs; ++j) word[j] = word[j] == best ? 0u : word[j];
+    for (int d = 1; d < per; d <<= 1) {
+      beats += __shfl_xor(beats, d);
+      top = max(top, (uint32_t)__shfl_xor(top, d));
     }
+    const float top_l = T::to_f32((top & 0x8000u) ? (top & 0x7FFFu) : (~top & 0xFFFFu));
+    float sum = 1.0f;
     if (!a.renormalize) {
       sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < kExpertRegs; ++j)
-        if (64 * j + lane < a.experts) sum += expf(v[j] - top);
-      sum = wave_sum(sum);
+#pragma unroll 4
+      for (int j = i; j < a.experts; j += per) sum += expf(T::to_f32(logits[j]) - top_l);
+      for (int d = 1; d < per; d <<= 1) sum += __shfl_xor(sum, d);
     }
-    if (lane < kMaxExperts / 32) r.chosen[t][lane] = mine;
-    if (lane == 0) {
-      r.top[t] = top;
-      r.inv[t] = 1.0f / sum;
+    if (i == 0) {
+      u.pair_of[t] = beats < a.top_k ? (int16_t)(t * a.top_k + beats) : (int16_t)-1;
+      u.share_of[t] = expf(T::to_f32(logits[e]) - top_l) / sum;
     }
   }
-  __syncthreads();
-  if (threadIdx.x < kMaxExperts / 32) {
-    uint32_t m = 0u;
-    for (int t = 0; t < a.tokens; ++t) m |= r.chosen[t][threadIdx.x];
-    r.any[threadIdx.x] = m;
-  }
-  __syncthreads();
+  list_users(a, u);
 }
 
-// Bits of m[0 .. e) that are set.
-__device__ inline int rank_of(const uint32_t* m, int e) {
-  int n = 0;
-  for (int i = 0; i < e >> 5; ++i) n += __popc(m[i]);
-  return n + __popc(m[e >> 5] & ((1u << (e & 31)) - 1u));
+// Fill u from the first kernel's pairs.
+__device__ inline void read_users(const MoeArgs& a, int e, Users& u) {
+  if (threadIdx.x < kMaxTokens) u.pair_of[threadIdx.x] = -1;
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.tokens * a.top_k; i += kThreads)
+    if (a.pair_expert[i] == e) u.pair_of[i / a.top_k] = (int16_t)i;
+  list_users(a, u);
 }
 
-// One wave's products of TN weight tiles with MT * 16 activation rows over slots [s0, s1).
-template <class T, int BITS, int GS, int TN, int MT>
+// [x0 .. x7] -> [x0, x2, x4, x6, x1, x3, x5, x7], the order in which 4-bit codes are expanded.
+__device__ inline u32x4 even_odd(u32x4 u) {
+  return u32x4{__builtin_amdgcn_perm(u.y, u.x, 0x05040100u), __builtin_amdgcn_perm(u.w, u.z, 0x05040100u),
+               __builtin_amdgcn_perm(u.y, u.x, 0x07060302u), __builtin_amdgcn_perm(u.w, u.z, 0x07060302u)};
+}
+
+// One wave's weight stream of two 16-row tiles.  NARROW: a slot's scales and biases are read
+// one halfword at a time (rows, experts or arrays that do not start on a slot's groups, or a K
+// that is no multiple of the slot).
+template <class T, int BITS, int GS, bool NARROW>
 struct Stream {
   using S = Slot<BITS, GS>;
+  static constexpr int TN = 2;
+  static constexpr int kBits = BITS;
   static constexpr int kSteps = S::kSteps;
-  static constexpr int kDepth = MT == 1 ? 4 : 2;      // slots in flight
-  static constexpr int kSub8 = BITS == 8;
+  static constexpr int KG = S::kGroups;
+  static constexpr int kDepth = S::kWords <= 4 ? 4 : 2;      // slots in flight: 8 KB of 4- and 8-bit codes
+  static constexpr int kSlotX = kSteps * 4;                  // 16-byte operand entries of a slot per row
 
-  const uint32_t* w[TN];      // the lane's weight row of each tile
+  const uint32_t* w[TN];          // the lane's weight row of each tile
   const uint16_t* s[TN];
   const uint16_t* b[TN];
-  const uint16_t* x[MT];      // the lane's activation row, null: zeros
-  int K, row_words, lg, gword;
+  int K, row_words, groups, lg, col, gword;
   uint32_t gshift;
-  bool narrow;
+  SlotData<BITS, GS> ring[kDepth][TN];
 
-  struct Data {
-    SlotData<BITS, GS> d[TN];
-    u32x4 x[MT][kSteps];
-  };
-
-  __device__ inline void setup(const MoeArgs& a, int k) {
+  __device__ inline void setup(int k) {
     K = k;
     lg = (threadIdx.x & 63) >> 4;
+    col = threadIdx.x & 15;
     row_words = (K * BITS) >> 5;
+    groups = K / GS;
     gword = 0;
     gshift = 0u;
     if constexpr (BITS != 4 && BITS != 8) generic_lane_offsets<BITS>(lg, gword, gshift);
   }
-  // tile t: rows [16 * tile, ..) of expert e of a stack with n rows
+  // tile t of the loads to come: the lane's row `row` of expert e of a stack with n rows (rows past the last repeat it)
   __device__ inline void tile(int t, const Stack& k, int e, int64_t row, int64_t n) {
     const int64_t rr = row < n ? row : n - 1;
     w[t] = k.w + e * k.w_expert_stride + rr * k.w_row_stride;
     s[t] = k.s + e * k.sb_expert_stride + rr * k.sb_row_stride;
     b[t] = k.b + e * k.sb_expert_stride + rr * k.sb_row_stride;
   }
-  __device__ inline void load(Data& r, int slot) const {
+  __device__ inline void load_sb(SbRegs<KG>& r, const uint16_t* p, int slot) const {
+    if constexpr (KG == 1) {
+      r.v[0] = p[slot];
+    } else if constexpr (NARROW) {
 #pragma unroll
-    for (int t = 0; t < TN; ++t)
-      load_slot<BITS, GS>(r.d[t], w[t] + (int64_t)slot * S::kRowWordsPerSlot, s[t] + slot * S::kGroups,
-                          b[t] + slot * S::kGroups, lg, gword, row_words - slot * S::kRowWordsPerSlot,
-                          K - slot * S::kSpan, narrow);
-    const int sub = kSub8 && (lg == 1 || lg == 2) ? 3 - lg : lg;   // 8-bit words arrive with groups 1 and 2 swapped
-#pragma unroll
-    for (int c = 0; c < kSteps; ++c) {
-      const int k = slot * S::kSpan + 32 * c + 8 * sub;
-#pragma unroll
-      for (int m = 0; m < MT; ++m) r.x[m][c] = x[m] != nullptr && k < K ? *(const u32x4*)(x[m] + k) : u32x4{0u, 0u, 0u, 0u};
+      for (int i = 0; i < KG / 2; ++i)
+        r.v[i] = p[min(slot * KG + 2 * i, groups - 1)] | ((uint32_t)p[min(slot * KG + 2 * i + 1, groups - 1)] << 16);
+    } else if constexpr (KG == 2) {
+      r.v[0] = *(const uint32_t*)(p + slot * KG);
+    } else {
+      const uint2 u = *(const uint2*)(p + slot * KG);
+      r.v[0] = u.x;
+      r.v[1] = u.y;
     }
   }
-  __device__ inline void consume(const Data& r, int slot, f32x4 (&acc)[TN][MT]) const {
+  __device__ inline void load(SlotData<BITS, GS> (&d)[TN], int slot) const {
+#pragma unroll
+    for (int t = 0; t < TN; ++t) {
+      if constexpr (BITS == 4 || BITS == 8) {
+#pragma unroll
+        for (int v = 0; v < S::kVec; ++v)
+          d[t].v[v] = *(const u32x4*)(w[t] + min(slot * S::kRowWordsPerSlot + 16 * v + 4 * lg, row_words - 4));
+      } else {
+#pragma unroll
+        for (int c = 0; c < kSteps; ++c) {
+          const int at = slot * S::kRowWordsPerSlot + c * BITS + gword;
+          d[t].w[2 * c] = w[t][min(at, row_words - 1)];
+          d[t].w[2 * c + 1] = w[t][min(at + 1, row_words - 1)];
+        }
+      }
+      load_sb(d[t].s, s[t], slot);
+      load_sb(d[t].b, b[t], slot);
+    }
+  }
+  // x: the chunk's staged operands, entry (((slot - x0) * kSteps + step) * 4 + lane group) << xrl,
+  // plus `plane` entries for the rest; 2^xrl rows.
+  template <int PLANES>
+  __device__ inline void consume(const SlotData<BITS, GS> (&d)[TN], int slot, const u32x4* x, int plane, int xrl,
+                                 f32x4 (&acc)[TN]) const {
     constexpr int SPG = GS / 32;
     const uint32_t one2 = T::pack2(1.0f, 1.0f);
     const u32x4 ones = {one2, one2, one2, one2};
     const f32x4 zero4 = {0.f, 0.f, 0.f, 0.f};
+    const bool whole = (slot + 1) * S::kSpan <= K;
     decode::SlotCodes<BITS, GS> rc[TN];
 #pragma unroll
-    for (int t = 0; t < TN; ++t) rc[t] = slot_reorder<BITS, GS>(r.d[t]);
-    f32x4 part[TN][MT], sum[MT];
+    for (int t = 0; t < TN; ++t) rc[t] = slot_reorder<BITS, GS>(d[t]);
+    const int row = col & ((1 << xrl) - 1);
+    f32x4 part[TN], sum;
 #pragma unroll
     for (int c = 0; c < kSteps; ++c) {
       typename T::v8 q[TN];
 #pragma unroll
-      for (int t = 0; t < TN; ++t) q[t] = as_v8<T>(slot_codes<T, BITS, GS>(r.d[t], rc[t], c, gshift));
+      for (int t = 0; t < TN; ++t) q[t] = as_v8<T>(slot_codes<T, BITS, GS>(d[t], rc[t], c, gshift));
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const typename T::v8 av = as_v8<T>(BITS == 4 ? interleave_even_odd(r.x[m][c]) : r.x[m][c]);
-        sum[m] = T::mfma(av, as_v8<T>(ones), c % SPG == 0 ? zero4 : sum[m]);
+      for (int p = 0; p < PLANES; ++p) {
+        const typename T::v8 av = as_v8<T>(x[p * plane + ((c * 4 + lg) << xrl) + row]);
+        const bool fresh = c % SPG == 0 && p == 0;
+        sum = T::mfma(av, as_v8<T>(ones), fresh ? zero4 : sum);
 #pragma unroll
-        for (int t = 0; t < TN; ++t) part[t][m] = T::mfma(av, q[t], c % SPG == 0 ? zero4 : part[t][m]);
+        for (int t = 0; t < TN; ++t) part[t] = T::mfma(av, q[t], fresh ? zero4 : part[t]);
       }
       if ((c + 1) % SPG == 0) {
         const int g = c / SPG;
-        // groups past K (the last slot of a K that is no multiple of the span) scale by zero
-        const bool ok = slot * S::kSpan + g * GS < K;
+        const bool ok = whole || slot * S::kSpan + g * GS < K;   // groups past K scale by zero
 #pragma unroll
         for (int t = 0; t < TN; ++t) {
-          const float sv = ok ? T::to_f32(r.d[t].s.get(g)) : 0.f, bv = ok ? T::to_f32(r.d[t].b.get(g)) : 0.f;
+          const float sv = ok ? T::to_f32(d[t].s.get(g)) : 0.f, bv = ok ? T::to_f32(d[t].b.get(g)) : 0.f;
 #pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              acc[t][m][i] = __builtin_fmaf(sv, part[t][m][i], __builtin_fmaf(bv, sum[m][i], acc[t][m][i]));
+          for (int i = 0; i < 4; ++i)
+            acc[t][i] = __builtin_fmaf(sv, part[t][i], __builtin_fmaf(bv, sum[i], acc[t][i]));
         }
-      }
-    }
-  }
-  __device__ inline void run(int s0, int s1, f32x4 (&acc)[TN][MT]) const {
-    Data ring[kDepth];
-#pragma unroll
-    for (int i = 0; i < kDepth; ++i)
-      if (s0 + i < s1) load(ring[i], s0 + i);
-    for (int base = s0; base < s1; base += kDepth) {
-#pragma unroll
-      for (int i = 0; i < kDepth; ++i) {
-        if (base + i >= s1) break;
-        consume(ring[i], base + i, acc);
-        if (base + i + kDepth < s1) load(ring[i], base + i + kDepth);
       }
     }
   }
 };
 
 // Whether a slot's scales (and biases) can be read as one load: every row, expert and array
-// start aligned to the slot's groups.
-template <int KG>
-__device__ inline bool sb_aligned(const Stack& k) {
-  if constexpr (KG == 1) {
-    return true;
-  } else {
-    return (((uintptr_t)k.s | (uintptr_t)k.b) % (2 * KG)) == 0 && (uint64_t)(k.sb_row_stride * 2) % (2 * KG) == 0 &&
-           (uint64_t)(k.sb_expert_stride * 2) % (2 * KG) == 0;
-  }
+// start aligned to the slot's groups, and K whole slots.
+template <class S>
+inline bool sb_wide(const Stack& k, int64_t K) {
+  constexpr int w = 2 * S::kGroups;
+  if (S::kGroups == 1) return true;
+  return K % S::kSpan == 0 && (((uintptr_t)k.s | (uintptr_t)k.b) % w) == 0 && (k.sb_row_stride * 2) % w == 0 &&
+         (k.sb_expert_stride * 2) % w == 0;
 }
 
-// h[row of (t, e)][n] = w_te silu(g) u.  Workgroup (x, y): the y-th expert in use, tiles
-// [x * kWaves / parts, ..) of inter; `parts` waves share a tile, each a stretch of hidden, and
-// meet in LDS.
-template <class T, int BITS, int GS, int MT>
-__global__ __launch_bounds__(kThreads) void gate_up_kernel(const MoeArgs a) {
-  using S = Slot<BITS, GS>;
-  __shared__ Routing r;
-  __shared__ f32x4 hand[kWaves][2 * MT][64];
-  route<T>(a, r);
-  const int words = (a.experts + 31) >> 5;
-  int in_use = 0;
-  for (int i = 0; i < words; ++i) in_use += __popc(r.any[i]);
-  if (blockIdx.x == 0 && blockIdx.y == 0) {
-    // the plan that the second kernel reads
-    if (threadIdx.x == 0) a.active[0] = in_use;
-    for (int e = threadIdx.x; e < a.experts; e += kThreads) {
-      if (!((r.any[e >> 5] >> (e & 31)) & 1u)) continue;
-      const int n = rank_of(r.any, e);
-      a.active[1 + n] = e;
-      for (int t = 0; t < kMaxTokens; ++t) {
-        const bool use = t < a.tokens && ((r.chosen[t][e >> 5] >> (e & 31)) & 1u);
-        a.row_of[n * kMaxTokens + t] = use ? (int16_t)(t * a.top_k + rank_of(r.chosen[t], e)) : (int16_t)-1;
+// How a workgroup walks its tiles: tile units first, first + step, .. below units; a unit is
+// kWaves / parts tile pairs, one per group of `parts` waves, each of which takes an equal
+// stretch of every chunk of the slots [k0, k1); a chunk is what LDS holds of the activations.
+struct Walk {
+  int first, step, units;
+  int parts, part;
+  int k0, k1, chunk;
+};
+
+// The products of the walk's tiles with up to 16 rows of activations, PLANES operand planes
+// each.  row(m): address of row m < rows (plane p at + p * plane_stride).  set_tiles(st, unit)
+// points the stream's loads at a unit; finish(unit, acc) gets its sums, in the waves of part 0.
+// The ring of loads runs on over chunks and tiles.  With `started` its first loads are out.
+template <int PLANES, class St, class Row, class Tiles, class Finish>
+struct Products {
+  static constexpr int kDepth = St::kDepth, kSlotX = St::kSlotX;
+  St& st;
+  const Walk& w;
+  // the next slot to load
+  int unit, c0, at;
+
+  // slots of a wave's stretch of a chunk, a whole number of ring rounds
+  __device__ inline int stretch(int c) const {
+    const int n = min(w.chunk, w.k1 - c), per = (n + w.parts - 1) / w.parts;
+    return (per + kDepth - 1) / kDepth * kDepth;
+  }
+  __device__ inline void load_next(int i, Tiles& set_tiles) {
+    const int c1 = min(w.k1, c0 + w.chunk), per = (c1 - c0 + w.parts - 1) / w.parts;
+    st.load(st.ring[i], min(min(c0 + w.part * per + at, c0 + (w.part + 1) * per - 1), c1 - 1));
+    if (++at == stretch(c0)) {
+      at = 0;
+      c0 += w.chunk;
+      if (c0 >= w.k1) {
+        c0 = w.k0;
+        if (unit + w.step < w.units) unit += w.step;   // past the last unit its loads repeat
+        set_tiles(st, unit);
       }
     }
   }
-  const int n_th = blockIdx.y;
-  if (n_th >= in_use) return;                 // the same in the whole workgroup
-  int e = 0;                                  // the n_th expert in use
-  for (int i = 0, left = n_th; i < words; ++i) {
-    const int have = __popc(r.any[i]);
-    if (left < have) {
-      uint32_t m = r.any[i];
-      for (; left > 0; --left) m &= m - 1u;
-      e = 32 * i + __ffs(m) - 1;
-      break;
-    }
-    left -= have;
+  __device__ inline void start(Tiles& set_tiles) {
+    unit = w.first;
+    c0 = w.k0;
+    at = 0;
+    set_tiles(st, unit);
+#pragma unroll
+    for (int i = 0; i < kDepth; ++i) load_next(i, set_tiles);
   }
-  const int lane = threadIdx.x & 63, lg = lane >> 4, col = lane & 15;
-  const int wave = threadIdx.x >> 6;
-  const int part = wave % a.parts, group = wave / a.parts;
-  const int64_t n0 = ((int64_t)blockIdx.x * (kWaves / a.parts) + group) * 16;
-  const bool live = n0 < a.inter;
-  f32x4 acc[2][MT];
+  __device__ inline void stage(int rows, Row& row, int64_t plane_stride, u32x4* xs, int k, int n, int xrl) {
+    const int plane = (n * kSlotX) << xrl, entries = plane * PLANES;
+    constexpr int kBatch = 4;
+    for (int e0 = threadIdx.x; e0 < entries; e0 += kBatch * kThreads) {
+      u32x4 v[kBatch];
 #pragma unroll
-  for (int t = 0; t < 2; ++t)
+      for (int i = 0; i < kBatch; ++i) {
+        const int en = min(e0 + i * kThreads, entries - 1);
+        const int p = en >= plane ? 1 : 0, x = en - p * plane;
+        const int m = min(x & ((1 << xrl) - 1), rows - 1), kk = k * St::S::kSpan + 8 * (x >> xrl);
+        v[i] = *(const u32x4*)(row(m) + p * plane_stride + min(kk, st.K - 8));
+        if (kk >= st.K) v[i] = u32x4{0u, 0u, 0u, 0u};
+      }
 #pragma unroll
-    for (int m = 0; m < MT; ++m) acc[t][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (live) {
-    Stream<T, BITS, GS, 2, MT> st;
-    st.setup(a, a.hidden);
-    st.narrow = !sb_aligned<S::kGroups>(a.gate) || !sb_aligned<S::kGroups>(a.up);
-    st.tile(0, a.gate, e, n0 + col, a.inter);
-    st.tile(1, a.up, e, n0 + col, a.inter);
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int t = 16 * m + col;
-      const bool use = t < a.tokens && ((r.chosen[t][e >> 5] >> (e & 31)) & 1u);
-      st.x[m] = use ? a.x + t * a.x_stride : nullptr;
+      for (int i = 0; i < kBatch; ++i) {
+        const int en = e0 + i * kThreads;
+        if (en >= entries) break;
+        const int p = en >= plane ? 1 : 0, x = en - p * plane;
+        const int m = x & ((1 << xrl) - 1), k8 = x >> xrl;   // 8 consecutive k
+        xs[p * plane + (((k8 & ~3) + decode::lane_group_of_sub<St::kBits>(k8 & 3)) << xrl) + m] =
+            St::kBits == 4 ? even_odd(v[i]) : v[i];
+      }
     }
-    const int slots = (a.hidden + S::kSpan - 1) / S::kSpan, per = (slots + a.parts - 1) / a.parts;
-    st.run(part * per, min(slots, (part + 1) * per), acc);
   }
-  if (a.parts > 1) {
-    if (part != 0) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) hand[wave][t * MT + m][lane] = acc[t][m];
+  __device__ inline void run(int rows, Row row, int64_t plane_stride, Tiles set_tiles, Finish finish, int xrl,
+                             u32x4* xs, f32x4* hand, bool started) {
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    if (!started) start(set_tiles);
+    const bool resident = w.k1 - w.k0 <= w.chunk;     // one chunk: staged once for all tiles
+    if (resident) {
+      stage(rows, row, plane_stride, xs, w.k0, w.k1 - w.k0, xrl);
+      lds_barrier();
     }
-    __syncthreads();
-    if (part != 0) return;
-    for (int p = 1; p < a.parts; ++p)
+    for (int u = w.first; u < w.units; u += w.step) {
+      f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      for (int c = w.k0; c < w.k1; c += w.chunk) {
+        const int c1 = min(w.k1, c + w.chunk), per = (c1 - c + w.parts - 1) / w.parts;
+        const int s0 = c + w.part * per, s1 = min(c1, s0 + per), pad = stretch(c);
+        const int plane = ((c1 - c) * kSlotX) << xrl;
+        if (!resident) {
+          lds_barrier();
+          stage(rows, row, plane_stride, xs, c, c1 - c, xrl);
+          lds_barrier();
+        }
+        for (int base = s0; base < s0 + pad; base += kDepth) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) acc[t][m] += hand[wave + p][t * MT + m][lane];
+          for (int i = 0; i < kDepth; ++i) {
+            if (base + i < s1)
+              st.template consume<PLANES>(st.ring[i], base + i, xs + (((base + i - c) * kSlotX) << xrl), plane, xrl,
+                                          acc);
+            load_next(i, set_tiles);
+          }
+        }
+      }
+      if (w.parts > 1) {
+        if (w.part != 0) {
+          hand[(wave * 2 + 0) * 64 + lane] = acc[0];
+          hand[(wave * 2 + 1) * 64 + lane] = acc[1];
+        }
+        lds_barrier();
+        if (w.part == 0)
+          for (int p = 1; p < w.parts; ++p) {
+            acc[0] += hand[((wave + p) * 2 + 0) * 64 + lane];
+            acc[1] += hand[((wave + p) * 2 + 1) * 64 + lane];
+          }
+        lds_barrier();
+      }
+      if (w.part == 0) finish(u, acc);
+    }
+    lds_barrier();                                    // the next pass stages over xs
   }
-  const int64_t n = n0 + col;
-  if (n >= a.inter) return;
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = 16 * m + 4 * lg + i;
-      if (t >= a.tokens || !((r.chosen[t][e >> 5] >> (e & 31)) & 1u)) continue;
-      const float w = expf(T::to_f32(a.router[t * a.router_stride + e]) - r.top[t]) * r.inv[t];
-      const float g = acc[0][m][i];
-      const float v = w * (g / (1.0f + expf(-g))) * acc[1][m][i];
-      a.h[(int64_t)(t * a.top_k + rank_of(r.chosen[t], e)) * a.inter + n] = T::from_f32(v);
-    }
+};
+
+// log2 of the staged rows, and the slots of `rows` rows (PLANES planes) that LDS holds, whole
+// ring rounds of every part where that many fit.
+template <int PLANES, class St>
+__device__ inline int fit_chunk(int rows, int parts, int* xrl) {
+  int l = 0;
+  while ((1 << l) < rows) ++l;
+  *xrl = l;
+  const int fit = kXBytes / 16 / ((St::kSlotX * PLANES) << l), round = parts * St::kDepth;
+  return fit >= round ? fit / round * round : fit;
 }
 
-// y_t += h Wd^T over the experts.  Workgroup (x, y): tile x of hidden, split y; its waves and
-// the splits share the pieces (expert in use, one of `cuts` stretches of inter) evenly.  The
-// waves' sums meet in LDS, in wave order; the splits' in `part`, in split order.
-template <class T, int BITS, int GS, int MT>
-__global__ __launch_bounds__(kThreads) void down_kernel(const MoeArgs a) {
-  using S = Slot<BITS, GS>;
-  __shared__ f32x4 hand[kWaves][MT][64];
+// Workgroup (x, y) of both product kernels: y is an expert or, when the call has fewer (token,
+// choice) pairs than there are experts (`by_pair`), the pair whose expert it is, unless an
+// earlier token has the same; x the workgroup's first tile unit.
+
+// h rows of expert e's tokens.
+template <class T, int BITS, int GS, bool NARROW>
+__global__ __launch_bounds__(kThreads, kWorkgroups) void gate_up_kernel(const MoeArgs a, const int by_pair) {
+  using St = Stream<T, BITS, GS, NARROW>;
+  __shared__ Users u;
+  __shared__ u32x4 xs[kXBytes / 16];
+  __shared__ f32x4 hand[kWaves * 2 * 64];
   const int lane = threadIdx.x & 63, lg = lane >> 4, col = lane & 15;
-  const int wave = threadIdx.x >> 6;
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
-  f32x4 acc[1][MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) acc[0][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int slots = (a.inter + S::kSpan - 1) / S::kSpan, per = (slots + a.cuts - 1) / a.cuts;
-  const int pieces = a.active[0] * a.cuts, workers = kWaves * a.splits;
-  Stream<T, BITS, GS, 1, MT> st;
-  st.setup(a, a.inter);
-  st.narrow = !sb_aligned<S::kGroups>(a.down);
-  for (int p = blockIdx.y * kWaves + wave; p < pieces; p += workers) {
-    const int n_th = p / a.cuts, cut = p - n_th * a.cuts;
-    const int e = a.active[1 + n_th];
-    st.tile(0, a.down, e, n0 + col, a.hidden);
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int row = a.row_of[n_th * kMaxTokens + 16 * m + col];
-      st.x[m] = row >= 0 ? a.h + (int64_t)row * a.inter : nullptr;
-    }
-    st.run(cut * per, min(slots, (cut + 1) * per), acc);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = wave / a.parts, per = kWaves / a.parts;
+  int e = blockIdx.y, pair_token = 0;
+  if (by_pair) {
+    pair_token = blockIdx.y / a.top_k;
+    e = expert_of_rank<T>(a.router + pair_token * a.router_stride, a.experts, blockIdx.y - pair_token * a.top_k, lane);
   }
-  if (wave != 0) {
-#pragma unroll
-    for (int m = 0; m < MT; ++m) hand[wave][m][lane] = acc[0][m];
+  find_users<T>(a, e, u);
+  // the same in the whole workgroup: nobody uses the expert, or an earlier pair's workgroup does it
+  if (u.count == 0 || (by_pair && u.token[0] != pair_token)) return;
+  St st;
+  st.setup(a.hidden);
+  const auto column = [&](int unit) { return ((int64_t)unit * per + group) * 16 + col; };
+  const auto set_tiles = [&](St& t, int unit) {
+    t.tile(0, a.gate, e, column(unit), a.inter);
+    t.tile(1, a.up, e, column(unit), a.inter);
+  };
+  if (blockIdx.x == 0 && (int)threadIdx.x < u.count) {
+    a.pair_expert[u.pair[threadIdx.x]] = e;
+    a.pair_share[u.pair[threadIdx.x]] = u.share[threadIdx.x];
   }
-  __syncthreads();
-  if (wave != 0) return;
-  for (int w = 1; w < kWaves; ++w)
+  for (int r0 = 0; r0 < u.count; r0 += 16) {   // a second pass only for more than 16 tokens
+    const int rows = min(16, u.count - r0);
+    int xrl;
+    const int chunk = fit_chunk<1, St>(rows, a.parts, &xrl);
+    const Walk w{(int)blockIdx.x, (int)gridDim.x, (int)((a.inter + 16 * per - 1) / (16 * per)), a.parts,
+                 wave - group * a.parts, 0, (a.hidden + St::S::kSpan - 1) / St::S::kSpan, chunk};
+    const auto row = [&](int m) { return a.x + (int64_t)u.token[r0 + m] * a.x_stride; };
+    const auto finish = [&](int unit, const f32x4 (&acc)[2]) {
+      const int64_t n = column(unit);
+      if (n >= a.inter) return;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) acc[0][m] += hand[w][m][lane];
-  const int64_t n = n0 + col;
-  if (n >= a.hidden) return;
+      for (int i = 0; i < 4; ++i) {
+        const int r = r0 + 4 * lg + i;
+        if (r >= u.count) continue;
+        const float g = acc[0][i];
+        const float v = g / (1.0f + expf(-g)) * acc[1][i];
+        uint16_t* h = a.h + (int64_t)u.pair[r] * 2 * a.inter + n;
+        const uint16_t hi = T::from_f32(v);
+        h[0] = hi;
+        h[a.inter] = T::from_f32(v - T::to_f32(hi));
+      }
+    };
+    Products<1, St, decltype(row), decltype(set_tiles), decltype(finish)> p{st, w};
+    p.run(rows, row, 0, set_tiles, finish, xrl, xs, hand, false);
+  }
+}
+
+// out[pair][z] = h Wd_e^T over the z-th stretch of inter, of expert e's pairs, in float32.
+template <class T, int BITS, int GS, bool NARROW>
+__global__ __launch_bounds__(kThreads, kWorkgroups) void down_kernel(const MoeArgs a, const int by_pair) {
+  using St = Stream<T, BITS, GS, NARROW>;
+  __shared__ Users u;
+  __shared__ u32x4 xs[kXBytes / 16];
+  __shared__ f32x4 hand[kWaves * 2 * 64];
+  const int lane = threadIdx.x & 63, lg = lane >> 4, col = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = wave / a.down_parts, per = kWaves / a.down_parts;
+  const int e = by_pair ? __builtin_amdgcn_readfirstlane(a.pair_expert[blockIdx.y]) : (int)blockIdx.y;
+  read_users(a, e, u);
+  if (u.count == 0 || (by_pair && u.pair[0] != (int)blockIdx.y)) return;
+  St st;
+  st.setup(a.inter);
+  const auto column = [&](int unit) { return ((int64_t)unit * per + group) * 32 + col; };
+  const auto set_tiles = [&](St& t, int unit) {
+    t.tile(0, a.down, e, column(unit), a.hidden);
+    t.tile(1, a.down, e, column(unit) + 16, a.hidden);
+  };
+  const int slots = (a.inter + St::S::kSpan - 1) / St::S::kSpan, share = (slots + a.splits - 1) / a.splits;
+  const int z = blockIdx.z;
+  for (int r0 = 0; r0 < u.count; r0 += 16) {
+    const int rows = min(16, u.count - r0);
+    int xrl;
+    const int chunk = fit_chunk<2, St>(rows, a.down_parts, &xrl);
+    const Walk w{(int)blockIdx.x, (int)gridDim.x, (int)((a.hidden + 32 * per - 1) / (32 * per)), a.down_parts,
+                 wave - group * a.down_parts, z * share, min(slots, (z + 1) * share), chunk};
+    const auto row = [&](int m) { return a.h + (int64_t)u.pair[r0 + m] * 2 * a.inter; };
+    const auto finish = [&](int unit, const f32x4 (&acc)[2]) {
+      const int64_t n = column(unit);
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = 16 * m + 4 * lg + i;
-      if (t >= a.tokens) continue;
-      if (a.splits > 1)
-        a.part[((int64_t)blockIdx.y * a.tokens + t) * a.hidden + n] = acc[0][m][i];
-      else
-        a.y[t * a.y_stride + n] = T::from_f32(acc[0][m][i]);
-    }
+      for (int i = 0; i < 4; ++i) {
+        const int r = r0 + 4 * lg + i;
+        if (r >= u.count) continue;
+        float* o = a.out + ((int64_t)u.pair[r] * a.splits + z) * a.hidden + n;
+        if (n < a.hidden) o[0] = acc[0][i];
+        if (n + 16 < a.hidden) o[16] = acc[1][i];
+      }
+    };
+    Products<2, St, decltype(row), decltype(set_tiles), decltype(finish)> p{st, w};
+    p.run(rows, row, a.inter, set_tiles, finish, xrl, xs, hand, false);
+  }
 }
 
 template <class T, int BITS, int GS>
 hipError_t launch_group(const MoeArgs& a, hipStream_t stream, bool down) {
+  using S = Slot<BITS, GS>;
+  constexpr bool kMayNarrow = S::kGroups > 1;
+  const int pairs = a.tokens * a.top_k, by_pair = pairs < a.experts;
+  const dim3 grid((unsigned)(down ? a.down_blocks : a.blocks), (unsigned)(by_pair ? pairs : a.experts),
+                  (unsigned)(down ? a.splits : 1));
   if (down) {
-    const dim3 grid((unsigned)((a.hidden + 15) / 16), (unsigned)a.splits);
-    if (a.tokens <= 16)
-      hipLaunchKernelGGL((down_kernel<T, BITS, GS, 1>), grid, dim3(kThreads), 0, stream, a);
+    if (sb_wide<S>(a.down, a.inter))
+      hipLaunchKernelGGL((down_kernel<T, BITS, GS, false>), grid, dim3(kThreads), 0, stream, a, by_pair);
     else
-      hipLaunchKernelGGL((down_kernel<T, BITS, GS, 2>), grid, dim3(kThreads), 0, stream, a);
+      hipLaunchKernelGGL((down_kernel<T, BITS, GS, kMayNarrow>), grid, dim3(kThreads), 0, stream, a, by_pair);
   } else {
-    const int tiles = (a.inter + 15) / 16, per = kWaves / a.parts;
-    const int experts = a.tokens * a.top_k < a.experts ? a.tokens * a.top_k : a.experts;
-    const dim3 grid((unsigned)((tiles + per - 1) / per), (unsigned)experts);
-    if (a.tokens <= 16)
-      hipLaunchKernelGGL((gate_up_kernel<T, BITS, GS, 1>), grid, dim3(kThreads), 0, stream, a);
+    if (sb_wide<S>(a.gate, a.hidden) && sb_wide<S>(a.up, a.hidden))
+      hipLaunchKernelGGL((gate_up_kernel<T, BITS, GS, false>), grid, dim3(kThreads), 0, stream, a, by_pair);
     else
-      hipLaunchKernelGGL((gate_up_kernel<T, BITS, GS, 2>), grid, dim3(kThreads), 0, stream, a);
+      hipLaunchKernelGGL((gate_up_kernel<T, BITS, GS, kMayNarrow>), grid, dim3(kThreads), 0, stream, a, by_pair);
   }
   return hipGetLastError();
 }

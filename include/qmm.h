@@ -389,12 +389,10 @@ typedef struct {
 #define QMM_MOE_MAX_EXPERTS 512
 #define QMM_MOE_MAX_TOP_K 32
 
-/* The layer: y DEVICE [tokens, y_stride] of dtype, 2-byte aligned.  Products and sums in
- * float32; p * silu(g) * u is rounded once to dtype before the product with Wd.  workspace:
- * DEVICE, 16-byte aligned, qmm_moe_workspace_bytes(...) bytes of any content; one serves any
+/* The layer: y DEVICE [tokens, y_stride] of dtype, 2-byte aligned.  Sums in float32;
+ * silu(g) * u enters the second product with twice the bits of dtype.  workspace: DEVICE, 16-byte aligned, qmm_moe_workspace_bytes(...) bytes of any content; one serves any
  * number of calls in stream order, calls that may overlap need their own.  The result depends
- * only on the inputs (no atomics).  tokens == 0 is a no-op.  Two kernels are enqueued, or
- * three when the second product is split over workgroups. */
+ * only on the inputs (no atomics).  tokens == 0 is a no-op.  Three kernels are enqueued. */
 int32_t qmm_moe(const qmm_moe_t* args, void* y, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Host-only: workspace bytes of qmm_moe for these sizes, or a negative error code.  Grows with
