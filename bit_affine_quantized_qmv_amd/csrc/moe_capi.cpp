@@ -47,6 +47,9 @@ int32_t check_stack(const char* name, const qmm_expert_stack_t* k, int64_t n, in
     return report(QMM_ERR_SHAPE, who + "row strides smaller than a row");
   if (k->w_expert_stride < n * w.w_row_stride || k->sb_expert_stride < n * w.sb_row_stride)
     return report(QMM_ERR_SHAPE, who + "expert strides smaller than one expert");
+  // rows of one expert, and as many past the last, are addressed with 32-bit byte offsets
+  if ((n + 128) * w.w_row_stride * 4 >= (1ll << 30) || (n + 128) * w.sb_row_stride * 2 >= (1ll << 30))
+    return report(QMM_ERR_SHAPE, who + "one expert's codes must be smaller than 1 GiB");
   const bool wide = w.bits == 4 || w.bits == 8;   // codes loaded 16 bytes at a time, else word by word
   if (wide && (w.w_row_stride % 4 || k->w_expert_stride % 4))
     return report(QMM_ERR_ALIGN, who + "w_row_stride and w_expert_stride must be multiples of 4 words");

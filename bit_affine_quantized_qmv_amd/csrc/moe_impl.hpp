@@ -163,9 +163,12 @@ __device__ inline u32x4 even_odd(u32x4 u) {
                __builtin_amdgcn_perm(u.y, u.x, 0x07060302u), __builtin_amdgcn_perm(u.w, u.z, 0x07060302u)};
 }
 
-// One wave's weight stream of two 16-row tiles.  NARROW: a slot's scales and biases are read
-// one halfword at a time (rows, experts or arrays that do not start on a slot's groups, or a K
-// that is no multiple of the slot).
+// One wave's weight stream of two 16-row tiles, through buffer descriptors over one expert: a
+// slot's offset is a scalar, the lane's row a register, rows past the last read as zeros, and
+// what a slot reads past its row's end is multiplied by zero.  The scales and biases of a
+// round of kDepth slots are one load per tile, a round ahead: one load per slot asked for
+// twice as many cache lines as the codes (16 rows of two bytes each).  NARROW: they are read
+// one halfword at a time (rows, experts or arrays that are not whole words).
 template <class T, int BITS, int GS, bool NARROW>
 struct Stream {
   using S = Slot<BITS, GS>;
@@ -173,72 +176,76 @@ struct Stream {
   static constexpr int kBits = BITS;
   static constexpr int kSteps = S::kSteps;
   static constexpr int KG = S::kGroups;
-  static constexpr int kDepth = S::kWords <= 4 ? 4 : 2;      // slots in flight: 8 KB of 4- and 8-bit codes
-  static constexpr int kSlotX = kSteps * 4;                  // 16-byte operand entries of a slot per row
+  static constexpr int kDepth = S::kWords <= 4 && KG < 4 ? 4 : 2;   // slots in flight
+  static constexpr int NH = kDepth * KG;                            // groups of a round
+  static constexpr int kSlotX = kSteps * 4;                         // 16-byte operand entries of a slot per row
 
-  const uint32_t* w[TN];          // the lane's weight row of each tile
-  const uint16_t* s[TN];
-  const uint16_t* b[TN];
-  int K, row_words, groups, lg, col, gword;
+  __amdgpu_buffer_rsrc_t w_rs[TN], s_rs[TN], b_rs[TN];
+  int w_voff[TN], sb_voff[TN];    // the lane's row of each tile, bytes
+  int w_row_bytes, sb_row_bytes;
+  int K, lg, col;
   uint32_t gshift;
   SlotData<BITS, GS> ring[kDepth][TN];
+  struct Sb {
+    SbRegs<NH> s[TN], b[TN];
+  };
 
-  __device__ inline void setup(int k) {
-    K = k;
+  // Tile t's weights: expert e of a stack with n rows.
+  __device__ inline void setup(int t, const Stack& k, int e, int64_t n, int cols) {
+    K = cols;
     lg = (threadIdx.x & 63) >> 4;
     col = threadIdx.x & 15;
-    row_words = (K * BITS) >> 5;
-    groups = K / GS;
-    gword = 0;
+    w_row_bytes = (int)(k.w_row_stride * 4);
+    sb_row_bytes = (int)(k.sb_row_stride * 2);
     gshift = 0u;
+    int gword = 0;
     if constexpr (BITS != 4 && BITS != 8) generic_lane_offsets<BITS>(lg, gword, gshift);
+    const uint32_t w_bytes = (uint32_t)(n - 1) * (uint32_t)w_row_bytes + (uint32_t)(K / 32 * BITS * 4);
+    const uint32_t sb_bytes = (uint32_t)(n - 1) * (uint32_t)sb_row_bytes + (uint32_t)(K / GS * 2);
+    w_rs[t] = decode::make_rsrc(k.w + e * k.w_expert_stride, w_bytes);
+    s_rs[t] = decode::make_rsrc(k.s + e * k.sb_expert_stride, sb_bytes);
+    b_rs[t] = decode::make_rsrc(k.b + e * k.sb_expert_stride, sb_bytes);
+    lane_word = BITS == 4 || BITS == 8 ? 16 * lg : 4 * gword;
   }
-  // tile t of the loads to come: the lane's row `row` of expert e of a stack with n rows (rows past the last repeat it)
-  __device__ inline void tile(int t, const Stack& k, int e, int64_t row, int64_t n) {
-    const int64_t rr = row < n ? row : n - 1;
-    w[t] = k.w + e * k.w_expert_stride + rr * k.w_row_stride;
-    s[t] = k.s + e * k.sb_expert_stride + rr * k.sb_row_stride;
-    b[t] = k.b + e * k.sb_expert_stride + rr * k.sb_row_stride;
-  }
-  __device__ inline void load_sb(SbRegs<KG>& r, const uint16_t* p, int slot) const {
-    if constexpr (KG == 1) {
-      r.v[0] = p[slot];
-    } else if constexpr (NARROW) {
-#pragma unroll
-      for (int i = 0; i < KG / 2; ++i)
-        r.v[i] = p[min(slot * KG + 2 * i, groups - 1)] | ((uint32_t)p[min(slot * KG + 2 * i + 1, groups - 1)] << 16);
-    } else if constexpr (KG == 2) {
-      r.v[0] = *(const uint32_t*)(p + slot * KG);
-    } else {
-      const uint2 u = *(const uint2*)(p + slot * KG);
-      r.v[0] = u.x;
-      r.v[1] = u.y;
-    }
+  int lane_word;                  // byte of the lane's words in a slot
+  // Tile t starts at row `row`.
+  __device__ inline void tile(int t, int row) {
+    w_voff[t] = (row + col) * w_row_bytes + lane_word;
+    sb_voff[t] = (row + col) * sb_row_bytes;
   }
   __device__ inline void load(SlotData<BITS, GS> (&d)[TN], int slot) const {
+    const int soff = slot * S::kRowWordsPerSlot * 4;
 #pragma unroll
     for (int t = 0; t < TN; ++t) {
       if constexpr (BITS == 4 || BITS == 8) {
-#pragma unroll
-        for (int v = 0; v < S::kVec; ++v)
-          d[t].v[v] = *(const u32x4*)(w[t] + min(slot * S::kRowWordsPerSlot + 16 * v + 4 * lg, row_words - 4));
+        decode::load_slot_buf<BITS, GS, false>(d[t], w_rs[t], s_rs[t], b_rs[t], w_voff[t], soff, 0, 0);
       } else {
 #pragma unroll
         for (int c = 0; c < kSteps; ++c) {
-          const int at = slot * S::kRowWordsPerSlot + c * BITS + gword;
-          d[t].w[2 * c] = w[t][min(at, row_words - 1)];
-          d[t].w[2 * c + 1] = w[t][min(at + 1, row_words - 1)];
+          d[t].w[2 * c] = __builtin_amdgcn_raw_buffer_load_b32(w_rs[t], w_voff[t] + 4 * c * BITS, soff, 0);
+          d[t].w[2 * c + 1] = __builtin_amdgcn_raw_buffer_load_b32(w_rs[t], w_voff[t] + 4 * c * BITS + 4, soff, 0);
         }
       }
-      load_sb(d[t].s, s[t], slot);
-      load_sb(d[t].b, b[t], slot);
+    }
+  }
+  __device__ inline void load_sb(Sb& r, int slot) const {
+    const int soff = slot * KG * 2;
+#pragma unroll
+    for (int t = 0; t < TN; ++t) {
+      if constexpr (NARROW) {
+        decode::load_sb_buf_narrow<NH>(r.s[t], s_rs[t], sb_voff[t], soff);
+        decode::load_sb_buf_narrow<NH>(r.b[t], b_rs[t], sb_voff[t], soff);
+      } else {
+        decode::load_sb_buf<NH>(r.s[t], s_rs[t], sb_voff[t], soff);
+        decode::load_sb_buf<NH>(r.b[t], b_rs[t], sb_voff[t], soff);
+      }
     }
   }
   // x: the chunk's staged operands, entry (((slot - x0) * kSteps + step) * 4 + lane group) << xrl,
-  // plus `plane` entries for the rest; 2^xrl rows.
+  // plus `plane` entries for the rest; 2^xrl rows.  The slot is the nth of its round.
   template <int PLANES>
-  __device__ inline void consume(const SlotData<BITS, GS> (&d)[TN], int slot, const u32x4* x, int plane, int xrl,
-                                 f32x4 (&acc)[TN]) const {
+  __device__ inline void consume(const SlotData<BITS, GS> (&d)[TN], const Sb& sb, int nth, int slot, const u32x4* x,
+                                 int plane, int xrl, f32x4 (&acc)[TN]) const {
     constexpr int SPG = GS / 32;
     const uint32_t one2 = T::pack2(1.0f, 1.0f);
     const u32x4 ones = {one2, one2, one2, one2};
@@ -267,7 +274,8 @@ struct Stream {
         const bool ok = whole || slot * S::kSpan + g * GS < K;   // groups past K scale by zero
 #pragma unroll
         for (int t = 0; t < TN; ++t) {
-          const float sv = ok ? T::to_f32(d[t].s.get(g)) : 0.f, bv = ok ? T::to_f32(d[t].b.get(g)) : 0.f;
+          const float sv = ok ? T::to_f32(sb.s[t].get(nth * KG + g)) : 0.f;
+          const float bv = ok ? T::to_f32(sb.b[t].get(nth * KG + g)) : 0.f;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             acc[t][i] = __builtin_fmaf(sv, part[t][i], __builtin_fmaf(bv, sum[i], acc[t][i]));
@@ -277,14 +285,12 @@ struct Stream {
   }
 };
 
-// Whether a slot's scales (and biases) can be read as one load: every row, expert and array
-// start aligned to the slot's groups, and K whole slots.
-template <class S>
+// Whether a stack's scales and biases can be read in whole words: every row, expert and array
+// starts on one, and a row ends on one.
+template <int GS>
 inline bool sb_wide(const Stack& k, int64_t K) {
-  constexpr int w = 2 * S::kGroups;
-  if (S::kGroups == 1) return true;
-  return K % S::kSpan == 0 && (((uintptr_t)k.s | (uintptr_t)k.b) % w) == 0 && (k.sb_row_stride * 2) % w == 0 &&
-         (k.sb_expert_stride * 2) % w == 0;
+  return K / GS % 2 == 0 && (((uintptr_t)k.s | (uintptr_t)k.b) % 4) == 0 && k.sb_row_stride % 2 == 0 &&
+         k.sb_expert_stride % 2 == 0;
 }
 
 // How a workgroup walks its tiles: tile units first, first + step, .. below units; a unit is
@@ -299,7 +305,7 @@ struct Walk {
 // The products of the walk's tiles with up to 16 rows of activations, PLANES operand planes
 // each.  row(m): address of row m < rows (plane p at + p * plane_stride).  set_tiles(st, unit)
 // points the stream's loads at a unit; finish(unit, acc) gets its sums, in the waves of part 0.
-// The ring of loads runs on over chunks and tiles.  With `started` its first loads are out.
+// The ring of loads runs on over chunks and tiles.
 template <int PLANES, class St, class Row, class Tiles, class Finish>
 struct Products {
   static constexpr int kDepth = St::kDepth, kSlotX = St::kSlotX;
@@ -308,31 +314,28 @@ struct Products {
   // the next slot to load
   int unit, c0, at;
 
-  // slots of a wave's stretch of a chunk, a whole number of ring rounds
+  // slots of a wave's stretch of a chunk: even, so that its scales start on a word; the loop
+  // goes over whole rounds of the ring, whose last slots may be the next wave's (loaded, and
+  // not used)
   __device__ inline int stretch(int c) const {
     const int n = min(w.chunk, w.k1 - c), per = (n + w.parts - 1) / w.parts;
-    return (per + kDepth - 1) / kDepth * kDepth;
+    return (per + 1) & ~1;
   }
+  __device__ static inline int whole_rounds(int n) { return (n + kDepth - 1) / kDepth * kDepth; }
+  __device__ inline int next_slot() const { return c0 + w.part * stretch(c0) + at; }
   __device__ inline void load_next(int i, Tiles& set_tiles) {
-    const int c1 = min(w.k1, c0 + w.chunk), per = (c1 - c0 + w.parts - 1) / w.parts;
-    st.load(st.ring[i], min(min(c0 + w.part * per + at, c0 + (w.part + 1) * per - 1), c1 - 1));
-    if (++at == stretch(c0)) {
+    st.load(st.ring[i], next_slot() + i);
+    if (i + 1 < kDepth) return;
+    at += kDepth;
+    if (at >= stretch(c0)) {
       at = 0;
       c0 += w.chunk;
       if (c0 >= w.k1) {
         c0 = w.k0;
-        if (unit + w.step < w.units) unit += w.step;   // past the last unit its loads repeat
+        unit += w.step;                  // rows past the last unit read as zeros
         set_tiles(st, unit);
       }
     }
-  }
-  __device__ inline void start(Tiles& set_tiles) {
-    unit = w.first;
-    c0 = w.k0;
-    at = 0;
-    set_tiles(st, unit);
-#pragma unroll
-    for (int i = 0; i < kDepth; ++i) load_next(i, set_tiles);
   }
   __device__ inline void stage(int rows, Row& row, int64_t plane_stride, u32x4* xs, int k, int n, int xrl) {
     const int plane = (n * kSlotX) << xrl, entries = plane * PLANES;
@@ -359,9 +362,16 @@ struct Products {
     }
   }
   __device__ inline void run(int rows, Row row, int64_t plane_stride, Tiles set_tiles, Finish finish, int xrl,
-                             u32x4* xs, f32x4* hand, bool started) {
+                             u32x4* xs, f32x4* hand) {
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    if (!started) start(set_tiles);
+    unit = w.first;
+    c0 = w.k0;
+    at = 0;
+    set_tiles(st, unit);
+    typename St::Sb sb, sb_next;
+    st.load_sb(sb, next_slot());
+#pragma unroll
+    for (int i = 0; i < kDepth; ++i) load_next(i, set_tiles);
     const bool resident = w.k1 - w.k0 <= w.chunk;     // one chunk: staged once for all tiles
     if (resident) {
       stage(rows, row, plane_stride, xs, w.k0, w.k1 - w.k0, xrl);
@@ -370,22 +380,24 @@ struct Products {
     for (int u = w.first; u < w.units; u += w.step) {
       f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
       for (int c = w.k0; c < w.k1; c += w.chunk) {
-        const int c1 = min(w.k1, c + w.chunk), per = (c1 - c + w.parts - 1) / w.parts;
-        const int s0 = c + w.part * per, s1 = min(c1, s0 + per), pad = stretch(c);
+        const int c1 = min(w.k1, c + w.chunk), per = stretch(c);
+        const int s0 = c + w.part * per, s1 = min(c1, s0 + per);
         const int plane = ((c1 - c) * kSlotX) << xrl;
         if (!resident) {
           lds_barrier();
           stage(rows, row, plane_stride, xs, c, c1 - c, xrl);
           lds_barrier();
         }
-        for (int base = s0; base < s0 + pad; base += kDepth) {
+        for (int base = s0; base < s0 + whole_rounds(per); base += kDepth) {
+          st.load_sb(sb_next, next_slot());
 #pragma unroll
           for (int i = 0; i < kDepth; ++i) {
             if (base + i < s1)
-              st.template consume<PLANES>(st.ring[i], base + i, xs + (((base + i - c) * kSlotX) << xrl), plane, xrl,
-                                          acc);
+              st.template consume<PLANES>(st.ring[i], sb, i, base + i, xs + (((base + i - c) * kSlotX) << xrl), plane,
+                                          xrl, acc);
             load_next(i, set_tiles);
           }
+          sb = sb_next;
         }
       }
       if (w.parts > 1) {
@@ -441,11 +453,12 @@ __global__ __launch_bounds__(kThreads, kWorkgroups) void gate_up_kernel(const Mo
   // the same in the whole workgroup: nobody uses the expert, or an earlier pair's workgroup does it
   if (u.count == 0 || (by_pair && u.token[0] != pair_token)) return;
   St st;
-  st.setup(a.hidden);
-  const auto column = [&](int unit) { return ((int64_t)unit * per + group) * 16 + col; };
+  st.setup(0, a.gate, e, a.inter, a.hidden);
+  st.setup(1, a.up, e, a.inter, a.hidden);
+  const auto first_row = [&](int unit) { return (unit * per + group) * 16; };
   const auto set_tiles = [&](St& t, int unit) {
-    t.tile(0, a.gate, e, column(unit), a.inter);
-    t.tile(1, a.up, e, column(unit), a.inter);
+    t.tile(0, first_row(unit));
+    t.tile(1, first_row(unit));
   };
   if (blockIdx.x == 0 && (int)threadIdx.x < u.count) {
     a.pair_expert[u.pair[threadIdx.x]] = e;
@@ -459,7 +472,7 @@ __global__ __launch_bounds__(kThreads, kWorkgroups) void gate_up_kernel(const Mo
                  wave - group * a.parts, 0, (a.hidden + St::S::kSpan - 1) / St::S::kSpan, chunk};
     const auto row = [&](int m) { return a.x + (int64_t)u.token[r0 + m] * a.x_stride; };
     const auto finish = [&](int unit, const f32x4 (&acc)[2]) {
-      const int64_t n = column(unit);
+      const int n = first_row(unit) + col;
       if (n >= a.inter) return;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -474,7 +487,7 @@ __global__ __launch_bounds__(kThreads, kWorkgroups) void gate_up_kernel(const Mo
       }
     };
     Products<1, St, decltype(row), decltype(set_tiles), decltype(finish)> p{st, w};
-    p.run(rows, row, 0, set_tiles, finish, xrl, xs, hand, false);
+    p.run(rows, row, 0, set_tiles, finish, xrl, xs, hand);
   }
 }
 
@@ -492,23 +505,24 @@ __global__ __launch_bounds__(kThreads, kWorkgroups) void down_kernel(const MoeAr
   read_users(a, e, u);
   if (u.count == 0 || (by_pair && u.pair[0] != (int)blockIdx.y)) return;
   St st;
-  st.setup(a.inter);
-  const auto column = [&](int unit) { return ((int64_t)unit * per + group) * 32 + col; };
+  st.setup(0, a.down, e, a.hidden, a.inter);
+  st.setup(1, a.down, e, a.hidden, a.inter);
+  const auto first_row = [&](int unit) { return (unit * per + group) * 32; };
   const auto set_tiles = [&](St& t, int unit) {
-    t.tile(0, a.down, e, column(unit), a.hidden);
-    t.tile(1, a.down, e, column(unit) + 16, a.hidden);
+    t.tile(0, first_row(unit));
+    t.tile(1, first_row(unit) + 16);
   };
-  const int slots = (a.inter + St::S::kSpan - 1) / St::S::kSpan, share = (slots + a.splits - 1) / a.splits;
+  const int slots = (a.inter + St::S::kSpan - 1) / St::S::kSpan, share = ((slots + a.splits - 1) / a.splits + 1) & ~1;
   const int z = blockIdx.z;
   for (int r0 = 0; r0 < u.count; r0 += 16) {
     const int rows = min(16, u.count - r0);
     int xrl;
     const int chunk = fit_chunk<2, St>(rows, a.down_parts, &xrl);
     const Walk w{(int)blockIdx.x, (int)gridDim.x, (int)((a.hidden + 32 * per - 1) / (32 * per)), a.down_parts,
-                 wave - group * a.down_parts, z * share, min(slots, (z + 1) * share), chunk};
+                 wave - group * a.down_parts, min(slots, z * share), min(slots, (z + 1) * share), chunk};
     const auto row = [&](int m) { return a.h + (int64_t)u.pair[r0 + m] * 2 * a.inter; };
     const auto finish = [&](int unit, const f32x4 (&acc)[2]) {
-      const int64_t n = column(unit);
+      const int n = first_row(unit) + col;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = r0 + 4 * lg + i;
@@ -519,27 +533,25 @@ __global__ __launch_bounds__(kThreads, kWorkgroups) void down_kernel(const MoeAr
       }
     };
     Products<2, St, decltype(row), decltype(set_tiles), decltype(finish)> p{st, w};
-    p.run(rows, row, a.inter, set_tiles, finish, xrl, xs, hand, false);
+    p.run(rows, row, a.inter, set_tiles, finish, xrl, xs, hand);
   }
 }
 
 template <class T, int BITS, int GS>
 hipError_t launch_group(const MoeArgs& a, hipStream_t stream, bool down) {
-  using S = Slot<BITS, GS>;
-  constexpr bool kMayNarrow = S::kGroups > 1;
   const int pairs = a.tokens * a.top_k, by_pair = pairs < a.experts;
   const dim3 grid((unsigned)(down ? a.down_blocks : a.blocks), (unsigned)(by_pair ? pairs : a.experts),
                   (unsigned)(down ? a.splits : 1));
   if (down) {
-    if (sb_wide<S>(a.down, a.inter))
+    if (sb_wide<GS>(a.down, a.inter))
       hipLaunchKernelGGL((down_kernel<T, BITS, GS, false>), grid, dim3(kThreads), 0, stream, a, by_pair);
     else
-      hipLaunchKernelGGL((down_kernel<T, BITS, GS, kMayNarrow>), grid, dim3(kThreads), 0, stream, a, by_pair);
+      hipLaunchKernelGGL((down_kernel<T, BITS, GS, true>), grid, dim3(kThreads), 0, stream, a, by_pair);
   } else {
-    if (sb_wide<S>(a.gate, a.hidden) && sb_wide<S>(a.up, a.hidden))
+    if (sb_wide<GS>(a.gate, a.hidden) && sb_wide<GS>(a.up, a.hidden))
       hipLaunchKernelGGL((gate_up_kernel<T, BITS, GS, false>), grid, dim3(kThreads), 0, stream, a, by_pair);
     else
-      hipLaunchKernelGGL((gate_up_kernel<T, BITS, GS, kMayNarrow>), grid, dim3(kThreads), 0, stream, a, by_pair);
+      hipLaunchKernelGGL((gate_up_kernel<T, BITS, GS, true>), grid, dim3(kThreads), 0, stream, a, by_pair);
   }
   return hipGetLastError();
 }
