@@ -83,8 +83,13 @@ struct Side {
   uint32_t sb[2][D / GS][4];
 };
 
+// Workgroups per compute unit that the registers allow: the single-token form (one row tile) is
+// bound by the latency of its loads and takes four.
+template <int D, int GS, int RT>
+constexpr int workgroups() { return RT > 1 || D > 128 ? 1 : (D / GS == 1 ? 4 : (D / GS == 2 ? 3 : 2)); }
+
 template <class T, int D, int GS, int RT, bool BY_ROWS>
-__global__ __launch_bounds__(kThreads) void attend_kernel(const AttendArgs a) {
+__global__ __launch_bounds__(kThreads, (workgroups<D, GS, RT>())) void attend_kernel(const AttendArgs a) {
   constexpr int KC = D / 32;          // 32-element steps of a score; code words per lane and tile
   constexpr int NT = D / 16;          // 16-element output tiles
   constexpr int NG = D / GS;
@@ -115,6 +120,89 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendArgs a) {
   const int c1 = min(c0 + a.chunk, hi_max);
   const int stride = BY_ROWS ? kStep : kStep * kWaves;
 
+  float m[RT], l[RT], bsum[RT][NG];
+  f32x4 acc[RT][NT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    m[t] = kNone;
+    l[t] = 0.f;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) bsum[t][g] = 0.f;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  // The page of a 16-token tile that starts at token t0, and the token's place in it.  Tiles
+  // that no row sees read page 0 (their tokens are masked); a tile that is needed and has no
+  // page of the pool poisons the wave's outputs.
+  const int32_t* table = a.table + b * a.table_stride;
+  const int64_t page_words = 2 * a.c.side;
+  struct Place {
+    int page, token;
+  };
+  const auto place = [&](int t0) {
+    Place p{0, 0};
+    if (t0 < hi_max && t0 + 16 > lo_min) {
+      // t0 / page_size by a rounded-up reciprocal: exact below 2^27 tiles of 16
+      const uint32_t tile = (uint32_t)t0 >> 4;
+      const int blk = (int)(((uint64_t)tile * a.page_recip) >> 40);
+      p.token = t0 - blk * a.c.page_size;
+      p.page = __builtin_amdgcn_readfirstlane(table[blk]);
+    }
+    return p;
+  };
+  const auto base_of = [&](const Place& p) -> const uint32_t* {
+    int page = p.page;
+    if (page < 0 || page >= a.c.pages) {
+      bad = true;
+      page = 0;
+    }
+    return a.c.data + ((int64_t)page * a.c.heads + head) * page_words;
+  };
+  const int code_at = h * KC;
+  Side<D, GS> ks, vs;
+  auto load_side = [&](Side<D, GS>& s, int tile, const uint32_t* p, int token, bool value) {
+    if (value)
+      load_words<KC>(s.code[tile], p + (token / 4 + h) * (16 * KC) + col * KC);
+    else
+      load_words<KC>(s.code[tile], p + (token + col) * (D / 8) + code_at);
+    const uint32_t* sb = p + (int64_t)a.c.page_size * (D / 8) + token + 4 * h;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) load_words<4>(s.sb[tile][g], sb + g * a.c.page_size);
+  };
+  // the next step's tiles, and the pages of the step after it
+  const uint32_t* base_next[2] = {nullptr, nullptr};
+  int token_next[2] = {0, 0};
+  Place place_next[2];
+  auto find = [&](int t0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) place_next[i] = place(t0 + 16 * i);
+  };
+  auto take = [&]() {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      base_next[i] = base_of(place_next[i]);
+      token_next[i] = place_next[i].token;
+    }
+  };
+  auto load_k = [&]() {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) load_side(ks, i, base_next[i], token_next[i], false);
+  };
+  auto load_v = [&]() {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) load_side(vs, i, base_next[i] + a.c.side, token_next[i], true);
+  };
+
+  const int first = BY_ROWS ? c0 : c0 + kStep * wave;
+  if (first < c1) {
+    find(first);
+    take();
+    load_k();
+    load_v();
+    if (first + stride < c1) find(first + stride);
+  }
+
   // query operands: column col of row tile t is query row base + 16 t + col
   typename T::v8 q[RT][KC];
   float qsum[RT][NG];
@@ -140,70 +228,6 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendArgs a) {
     row_lo[t] = a.window ? off + i - a.window + 1 : 0;
   }
 
-  float m[RT], l[RT], bsum[RT][NG];
-  f32x4 acc[RT][NT];
-#pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    m[t] = kNone;
-    l[t] = 0.f;
-#pragma unroll
-    for (int g = 0; g < NG; ++g) bsum[t][g] = 0.f;
-#pragma unroll
-    for (int i = 0; i < NT; ++i) acc[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
-
-  // Word offset of the 16-token tile that starts at token t0, and whether its page is real.
-  // Tiles that no row sees read page 0 (their tokens are masked); a tile that is needed and
-  // has no page of the pool poisons the wave's outputs.
-  const int32_t* table = a.table + b * a.table_stride;
-  const int64_t page_words = 2 * a.c.side;
-  auto tile_base = [&](int t0, int* token) -> const uint32_t* {
-    const bool needed = t0 < hi_max && t0 + 16 > lo_min;
-    int page = 0, in_page = 0;
-    if (needed) {
-      const int blk = t0 / a.c.page_size;
-      in_page = t0 - blk * a.c.page_size;
-      page = __builtin_amdgcn_readfirstlane(table[blk]);
-      if (page < 0 || page >= a.c.pages) {
-        bad = true;
-        page = 0;
-      }
-    }
-    *token = in_page;
-    return a.c.data + ((int64_t)page * a.c.heads + head) * page_words;
-  };
-  const int code_at = h * KC;
-  Side<D, GS> ks, vs;
-  auto load_side = [&](Side<D, GS>& s, int tile, const uint32_t* p, int token, bool value) {
-    if (value)
-      load_words<KC>(s.code[tile], p + (token / 4 + h) * (16 * KC) + col * KC);
-    else
-      load_words<KC>(s.code[tile], p + (token + col) * (D / 8) + code_at);
-    const uint32_t* sb = p + (int64_t)a.c.page_size * (D / 8) + token + 4 * h;
-#pragma unroll
-    for (int g = 0; g < NG; ++g) load_words<4>(s.sb[tile][g], sb + g * a.c.page_size);
-  };
-  const uint32_t* base_next[2] = {nullptr, nullptr};
-  int token_next[2] = {0, 0};
-  auto find = [&](int t0) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) base_next[i] = tile_base(t0 + 16 * i, &token_next[i]);
-  };
-  auto load_k = [&]() {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) load_side(ks, i, base_next[i], token_next[i], false);
-  };
-  auto load_v = [&]() {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) load_side(vs, i, base_next[i] + a.c.side, token_next[i], true);
-  };
-
-  const int first = BY_ROWS ? c0 : c0 + kStep * wave;
-  if (first < c1) {
-    find(first);
-    load_k();
-    load_v();
-  }
   for (int t0 = first; t0 < c1; t0 += stride) {
     const bool more = t0 + stride < c1;
     // ---- scores: sc[t][i][r] of token t0 + 16 i + 4 h + r
@@ -239,8 +263,9 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(const AttendArgs a) {
       }
     }
     if (more) {
-      find(t0 + stride);
+      take();
       load_k();
+      if (t0 + 2 * stride < c1) find(t0 + 2 * stride);
     }
     // ---- rows that do not see every token of the step
     const bool masked = t0 < lo_max || t0 + kStep > hi_min;
@@ -437,12 +462,24 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(const AttendArgs 
   top = fmaxf(fmaxf(top_s[0], top_s[1]), fmaxf(top_s[2], top_s[3]));
   float sum = 0.f;
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
-  for (int s = grp; s < a.splits; s += kGroups) {
-    const float m = ml[2 * s];
-    if (m == kNone) continue;                            // no token of the split was seen
-    const float f = __builtin_amdgcn_exp2f(m - top);
-    sum = __builtin_fmaf(f, ml[2 * s + 1], sum);
-    o += f * *(const f32x4*)(o_part + (int64_t)s * D + 4 * lane);
+  constexpr int kAhead = 8;                              // splits loaded before the first is used
+  for (int s0 = grp; s0 < a.splits; s0 += kAhead * kGroups) {
+    float m[kAhead], l[kAhead];
+    f32x4 v[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int s = min(s0 + i * kGroups, a.splits - 1);
+      m[i] = ml[2 * s];
+      l[i] = ml[2 * s + 1];
+      v[i] = *(const f32x4*)(o_part + (int64_t)s * D + 4 * lane);
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (s0 + i * kGroups >= a.splits || m[i] == kNone) continue;   // no token of the split was seen
+      const float f = __builtin_amdgcn_exp2f(m[i] - top);
+      sum = __builtin_fmaf(f, l[i], sum);
+      o += f * v[i];
+    }
   }
   o_s[grp][lane] = o;
   if (lane == 0) sum_s[grp] = sum;

@@ -96,6 +96,7 @@ struct AttendArgs {
   int32_t chunk;          // tokens per split, a multiple of the tokens of one workgroup step
   int32_t splits;
   void* out;              // dense [batch, q_len, q_heads, head_dim]
+  uint64_t page_recip;    // 2^40 / (page_size / 16), rounded up
   float* part;            // splits > 1: [batch * heads * rows][splits][head_dim] sums, then their (max, sum) pairs
 };
 

@@ -97,7 +97,7 @@ int64_t part_floats(const AttendArgs& a, int64_t splits) {
 // Splits: enough workgroups for kTarget in all, each of at least one step of every wave (128
 // tokens), or 512 tokens where each wave has its own rows and a split's sums are large.
 AttendPlan plan_attend(int64_t batch, int heads, int head_dim, int64_t rows, int64_t range) {
-  constexpr int64_t kTarget = 2048;
+  constexpr int64_t kTarget = 1024;
   AttendPlan p{};
   p.by_rows = rows > 128;
   p.tile_rows = p.by_rows ? (head_dim == 256 ? 32 : 64) : (rows <= 16 ? 16 : 32);
@@ -119,7 +119,7 @@ static int64_t most_splits(const AttendArgs& a) {
   const AttendPlan one = plan_attend(a.batch, a.c.heads, a.c.head_dim, a.rows, 1);
   const int64_t wgs = std::max<int64_t>(1, a.batch * a.c.heads * one.row_tiles);
   const int64_t step = one.by_rows ? 512 : 128;
-  const int64_t want = std::max<int64_t>(1, (one.by_rows ? 512 : 2048) / wgs);
+  const int64_t want = std::max<int64_t>(1, (one.by_rows ? 512 : 1024) / wgs);
   return std::min<int64_t>(want, std::max<int64_t>(1, (a.max_length + step - 1) / step));
 }
 
@@ -210,6 +210,7 @@ int32_t qmm_kv_attend(const qmm_kv_cache_t* cache, const qmm_kv_attend_t* args, 
     if (workspace_bytes < need)
       return report(QMM_ERR_SHAPE, "kv_attend: workspace of " + std::to_string(workspace_bytes) + " bytes, needs " +
                                        std::to_string(need));
+    a.page_recip = ((1ull << 40) + a.c.page_size / 16 - 1) / (a.c.page_size / 16);
     a.chunk = p.chunk;
     a.splits = p.splits;
     a.out = out;

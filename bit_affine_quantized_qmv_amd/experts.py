@@ -7,15 +7,22 @@ import ctypes
 import torch
 
 from . import _lib
-from .api import ExpertWeights, _dtype_code, _stream
+from .api import _DTYPE_CODE, ExpertWeights
+from .kv import raw_stream
 
 
 def _stack(w: ExpertWeights) -> _lib.ExpertStack:
-    return _lib.ExpertStack(w.expert(0).desc(), w.num_experts, w.w_packed.stride(0), w.scales.stride(0))
+    codes, scales, biases = w.w_packed, w.scales, w.biases
+    ce, cr, cl = codes.stride()
+    se, sr, sl = scales.stride()
+    assert cl == 1 and sl == 1 and (se, sr, sl) == biases.stride() and codes.dtype == torch.int32
+    return _lib.ExpertStack(_lib.WeightDesc(codes.data_ptr(), cr, scales.data_ptr(), biases.data_ptr(), sr, w.N, w.K,
+                                            w.group_size, w.bits, _DTYPE_CODE[scales.dtype]),
+                            codes.size(0), ce, se)
 
 
-def _bytes(tokens: int, gate: ExpertWeights, top_k: int) -> int:
-    n = _lib.load().qmm_moe_workspace_bytes(tokens, gate.num_experts, top_k, gate.K, gate.N)
+def _bytes(lib, tokens: int, gate: ExpertWeights, top_k: int) -> int:
+    n = lib.qmm_moe_workspace_bytes(tokens, gate.num_experts, top_k, gate.K, gate.N)
     if n < 0:
         _lib.check(int(n))
     return n
@@ -24,7 +31,7 @@ def _bytes(tokens: int, gate: ExpertWeights, top_k: int) -> int:
 def moe_workspace(x: torch.Tensor, gate: ExpertWeights, top_k: int) -> torch.Tensor:
     """A workspace for moe calls of up to x.shape[0] tokens through experts like `gate`
     (reusable in stream order; its content does not matter)."""
-    return torch.empty((_bytes(x.shape[0], gate, top_k) + 3) // 4, dtype=torch.float32, device=x.device)
+    return torch.empty((_bytes(_lib.load(), x.shape[0], gate, top_k) + 3) // 4, dtype=torch.float32, device=x.device)
 
 
 def moe(x: torch.Tensor, router_logits: torch.Tensor, gate: ExpertWeights, up: ExpertWeights, down: ExpertWeights,
@@ -34,29 +41,34 @@ def moe(x: torch.Tensor, router_logits: torch.Tensor, gate: ExpertWeights, up: E
     top_k experts, softmax over them (renormalize) or over all, SwiGLU through gate, up and
     down."""
     lib = _lib.load()
-    if x.dim() != 2 or router_logits.dim() != 2 or router_logits.shape != (x.shape[0], gate.num_experts):
+    experts = gate.w_packed.size(0)
+    if x.dim() != 2 or router_logits.shape != (x.size(0), experts):
         raise ValueError("moe: x %s must be [tokens, hidden], router_logits %s [tokens, %d]"
-                         % (tuple(x.shape), tuple(router_logits.shape), gate.num_experts))
-    if x.shape[1] != gate.K:
-        raise _lib.QmmError(-3, "moe: x has %d columns, the experts take %d" % (x.shape[1], gate.K))
+                         % (tuple(x.shape), tuple(router_logits.shape), experts))
+    tokens, hidden = x.shape
+    if hidden != gate.K:
+        raise _lib.QmmError(-3, "moe: x has %d columns, the experts take %d" % (hidden, gate.K))
+    code = _DTYPE_CODE.get(x.dtype, 0)
     if router_logits.dtype != x.dtype:
         raise _lib.QmmError(-2, "x and router_logits must share one dtype")
-    if x.numel() and (x.stride(1) != 1 or router_logits.stride(1) != 1):
+    xs, xl = x.stride()
+    rs, rl = router_logits.stride()
+    if tokens and ((xl != 1 and hidden > 1) or (rl != 1 and experts > 1)):
         raise _lib.QmmError(-4, "moe: the last stride of x and router_logits must be 1")
-    y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    assert y.dtype == x.dtype and y.shape == x.shape and (y.numel() == 0 or y.stride(1) == 1)
-    stacks = [_stack(w) for w in (gate, up, down)]
-    d = _lib.MoeDesc()
-    d.x, d.x_stride = x.data_ptr(), x.stride(0) if x.shape[0] > 1 else x.shape[1]
-    d.router_logits = router_logits.data_ptr()
-    d.router_stride = router_logits.stride(0) if x.shape[0] > 1 else gate.num_experts
-    d.tokens, d.top_k, d.renormalize, d.dtype = x.shape[0], top_k, int(renormalize), _dtype_code(x.dtype)
-    d.gate, d.up, d.down = (ctypes.pointer(s) for s in stacks)
-    d.y_stride = y.stride(0) if x.shape[0] > 1 else x.shape[1]
-    ws = workspace
-    if ws is None:
-        ws = moe_workspace(x, gate, top_k)
-    assert ws.is_contiguous()
-    _lib.check(lib.qmm_moe(ctypes.byref(d), y.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
-                           _stream(x.device)))
-    return y
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    else:
+        assert out.dtype == x.dtype and out.shape == x.shape and (out.stride(1) == 1 or tokens == 0)
+    if workspace is None:
+        workspace = moe_workspace(x, gate, top_k)
+    assert workspace.is_contiguous()
+    g, u, d = _stack(gate), _stack(up), _stack(down)
+    pointer = ctypes.pointer
+    if tokens <= 1:                      # one row's strides may be anything
+        xs, rs, ys = hidden, experts, hidden
+    else:
+        ys = out.stride(0)
+    args = _lib.MoeDesc(x.data_ptr(), xs, router_logits.data_ptr(), rs, tokens, top_k, int(renormalize), code,
+                        pointer(g), pointer(u), pointer(d), ys)
+    _lib.check(lib.qmm_moe(ctypes.byref(args), out.data_ptr(), workspace.data_ptr(), workspace.nbytes, raw_stream(x)))
+    return out

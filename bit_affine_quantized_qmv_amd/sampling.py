@@ -6,7 +6,8 @@ import ctypes
 import torch
 
 from . import _lib
-from .api import _dtype_code, _stream
+from .api import _dtype_code
+from .kv import raw_stream
 
 _WORKSPACE_BYTES = 190520    # per row
 
@@ -24,24 +25,33 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
     and min_p are numbers or device tensors [rows] (float32; top_k int32).  temperature 0 takes
     the largest logit; a row of nothing but NaN and -inf gives index -1 and probability 0."""
     lib = _lib.load()
-    assert logits.dim() == 2 and (logits.numel() == 0 or logits.stride(1) == 1)
     rows, n = logits.shape
+    stride, last = logits.stride()
+    assert last == 1 or rows == 0 or n == 1
     assert u.dtype == torch.float32 and u.is_cuda and u.is_contiguous() and u.numel() == rows
-    p = _lib.SampleParams()
+    arrays, numbers = [], []
     for name, value, dtype in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
                                ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
         if isinstance(value, torch.Tensor):
             assert value.dtype == dtype and value.is_cuda and value.is_contiguous() and value.numel() == rows, name
-            setattr(p, name, value.data_ptr())
+            arrays.append(value.data_ptr())
+            numbers.append(0)
         else:
-            setattr(p, name + "_all", value)
-    idx = out_index if out_index is not None else torch.empty(rows, dtype=torch.int32, device=logits.device)
-    prob = out_prob if out_prob is not None else torch.empty(rows, dtype=torch.float32, device=logits.device)
-    assert idx.dtype == torch.int32 and idx.is_contiguous() and idx.numel() >= rows
-    assert prob.dtype == torch.float32 and prob.is_contiguous() and prob.numel() >= rows
-    ws = workspace if workspace is not None else sample_workspace(rows, logits.device)
-    assert ws.is_contiguous() and ws.numel() * ws.element_size() >= _WORKSPACE_BYTES * rows
-    _lib.check(lib.qmm_sample(logits.data_ptr(), _dtype_code(logits.dtype), rows, n,
-                              logits.stride(0) if rows > 1 else n, ctypes.byref(p), u.data_ptr(), idx.data_ptr(),
-                              prob.data_ptr(), ws.data_ptr(), _stream(logits.device)))
-    return idx, prob
+            arrays.append(None)
+            numbers.append(value)
+    p = _lib.SampleParams(*arrays, *numbers)
+    if out_index is None:
+        out_index = u.new_empty(rows, dtype=torch.int32)
+    else:
+        assert out_index.dtype == torch.int32 and out_index.is_contiguous() and out_index.numel() >= rows
+    if out_prob is None:
+        out_prob = u.new_empty(rows)
+    else:
+        assert out_prob.dtype == torch.float32 and out_prob.is_contiguous() and out_prob.numel() >= rows
+    if workspace is None:
+        workspace = sample_workspace(rows, logits.device)
+    assert workspace.is_contiguous() and workspace.nbytes >= _WORKSPACE_BYTES * rows
+    _lib.check(lib.qmm_sample(logits.data_ptr(), _dtype_code(logits.dtype), rows, n, stride if rows > 1 else n,
+                              ctypes.byref(p), u.data_ptr(), out_index.data_ptr(), out_prob.data_ptr(),
+                              workspace.data_ptr(), raw_stream(u)))
+    return out_index, out_prob
