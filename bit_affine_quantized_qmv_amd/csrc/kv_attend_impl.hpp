@@ -83,12 +83,28 @@ struct Side {
   uint32_t sb[2][D / GS][4];
 };
 
+// Four elements of one query row: its sums of this split, or the finished output.
+template <class T, int D>
+__device__ inline void store4(const AttendArgs& a, int64_t b, int head, int split, int64_t row0, int r, int d, f32x4 o,
+                              float sum) {
+  if (a.splits > 1) {
+    *(f32x4*)(a.part + ((row0 + r) * a.splits + split) * D + d) = o;
+  } else {
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;    // a row that sees nothing is zero
+    const int i = r / a.rep, g = r - i * a.rep;
+    uint2 u;
+    u.x = T::pack2(o[0] * inv, o[1] * inv);
+    u.y = T::pack2(o[2] * inv, o[3] * inv);
+    *(uint2*)((uint16_t*)a.out + ((b * a.q_len + i) * (int64_t)a.q_heads + head * a.rep + g) * D + d) = u;
+  }
+}
+
 // Workgroups per compute unit that the registers allow: the single-token form (one row tile) is
 // bound by the latency of its loads and takes four.
 template <int D, int GS, int RT>
 constexpr int workgroups() { return RT > 1 || D > 128 ? 1 : (D / GS == 1 ? 4 : (D / GS == 2 ? 3 : 2)); }
 
-template <class T, int D, int GS, int RT, bool BY_ROWS>
+template <class T, int D, int GS, int RT>
 __global__ __launch_bounds__(kThreads, (workgroups<D, GS, RT>())) void attend_kernel(const AttendArgs a) {
   constexpr int KC = D / 32;          // 32-element steps of a score; code words per lane and tile
   constexpr int NT = D / 16;          // 16-element output tiles
@@ -103,11 +119,10 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS, RT>())) void attend_ke
   const int split = blockIdx.x;
   const int head = blockIdx.y % a.c.heads, row_tile = blockIdx.y / a.c.heads;
   const int64_t b = blockIdx.z;
-  const int base = BY_ROWS ? (row_tile * kWaves + wave) * kRows : row_tile * kRows;
-  if (BY_ROWS && base >= a.rows) return;   // no barrier follows in this form
+  const int base = row_tile * kRows;
 
   int len = a.lengths[b];
-  bool bad = len < 0 || len > a.max_length;
+  const bool bad = len < 0 || len > a.max_length;
   if (bad) len = 0;
   // token ranges: [lo_min, hi_max) is seen by some row of the wave, [lo_max, hi_min) by all
   const int off = len - a.q_len;
@@ -118,7 +133,7 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS, RT>())) void attend_ke
   const int lo_max = a.window ? max(0, off + i_last - a.window + 1) : 0;
   const int c0 = (lo_min & ~(kStep - 1)) + split * a.chunk;
   const int c1 = min(c0 + a.chunk, hi_max);
-  const int stride = BY_ROWS ? kStep : kStep * kWaves;
+  const int stride = kStep * kWaves;
 
   float m[RT], l[RT], bsum[RT][NG];
   f32x4 acc[RT][NT];
@@ -134,7 +149,7 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS, RT>())) void attend_ke
 
   // The page of a 16-token tile that starts at token t0, and the token's place in it.  Tiles
   // that no row sees read page 0 (their tokens are masked); a tile that is needed and has no
-  // page of the pool poisons the wave's outputs.
+  // page of the pool gets NaN scales, and with them the rows that see it.
   const int32_t* table = a.table + b * a.table_stride;
   const int64_t page_words = 2 * a.c.side;
   struct Place {
@@ -151,13 +166,9 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS, RT>())) void attend_ke
     }
     return p;
   };
+  const auto outside = [&](const Place& p) { return p.page < 0 || p.page >= a.c.pages; };
   const auto base_of = [&](const Place& p) -> const uint32_t* {
-    int page = p.page;
-    if (page < 0 || page >= a.c.pages) {
-      bad = true;
-      page = 0;
-    }
-    return a.c.data + ((int64_t)page * a.c.heads + head) * page_words;
+    return a.c.data + ((int64_t)(outside(p) ? 0 : p.page) * a.c.heads + head) * page_words;
   };
   const int code_at = h * KC;
   Side<D, GS> ks, vs;
@@ -173,6 +184,7 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS, RT>())) void attend_ke
   // the next step's tiles, and the pages of the step after it
   const uint32_t* base_next[2] = {nullptr, nullptr};
   int token_next[2] = {0, 0};
+  bool bad_next[2] = {false, false};
   Place place_next[2];
   auto find = [&](int t0) {
 #pragma unroll
@@ -182,19 +194,28 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS, RT>())) void attend_ke
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       base_next[i] = base_of(place_next[i]);
+      bad_next[i] = outside(place_next[i]);
       token_next[i] = place_next[i].token;
     }
   };
   auto load_k = [&]() {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) load_side(ks, i, base_next[i], token_next[i], false);
+    for (int i = 0; i < 2; ++i) {
+      load_side(ks, i, base_next[i], token_next[i], false);
+      if (bad_next[i]) {
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) ks.sb[i][g][r] = 0x7FFF7FFFu;
+      }
+    }
   };
   auto load_v = [&]() {
 #pragma unroll
     for (int i = 0; i < 2; ++i) load_side(vs, i, base_next[i] + a.c.side, token_next[i], true);
   };
 
-  const int first = BY_ROWS ? c0 : c0 + kStep * wave;
+  const int first = c0 + kStep * wave;
   if (first < c1) {
     find(first);
     take();
@@ -377,32 +398,7 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS, RT>())) void attend_ke
 
   const int64_t row0 = (b * a.c.heads + head) * a.rows;
   float* part_ml = a.part + (int64_t)gridDim.z * a.c.heads * a.rows * a.splits * D;
-  auto store4 = [&](int r, int d, f32x4 o, float sum) {   // four elements of one row
-    if (a.splits > 1) {
-      *(f32x4*)(a.part + ((row0 + r) * a.splits + split) * D + d) = o;
-    } else {
-      const float inv = sum == 0.f ? 0.f : 1.0f / sum;    // a row that sees nothing is zero
-      const int i = r / a.rep, g = r - i * a.rep;
-      uint2 u;
-      u.x = T::pack2(o[0] * inv, o[1] * inv);
-      u.y = T::pack2(o[2] * inv, o[3] * inv);
-      *(uint2*)((uint16_t*)a.out + ((b * a.q_len + i) * (int64_t)a.q_heads + head * a.rep + g) * D + d) = u;
-    }
-  };
-  if constexpr (BY_ROWS) {
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      const int r = base + 16 * t + col;
-      if (r >= a.rows) continue;
-#pragma unroll
-      for (int i = 0; i < NT; ++i) store4(r, 16 * i + 4 * h, acc[t][i], l[t]);
-      if (a.splits > 1 && h == 0) {
-        float* ml = part_ml + ((row0 + r) * a.splits + split) * 2;
-        ml[0] = m[t];
-        ml[1] = l[t];
-      }
-    }
-  } else {
+  {
     // the four waves' sums meet in LDS: [wave][row][D], then [wave][row] maxima and sums
     float* ml_s = lds + kWaves * kRows * kPitch;
 #pragma unroll
@@ -431,12 +427,373 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS, RT>())) void attend_ke
         sum = __builtin_fmaf(f, ml_s[2 * (w * kRows + rr) + 1], sum);
         o += f * *(const f32x4*)(lds + (w * kRows + rr) * kPitch + d);
       }
-      store4(r, d, o, sum);
+      store4<T, D>(a, b, head, split, row0, r, d, o, sum);
       if (a.splits > 1 && d == 0) {
         float* ml = part_ml + ((row0 + r) * a.splits + split) * 2;
         ml[0] = top;
         ml[1] = sum;
       }
+    }
+  }
+}
+
+
+// ---- prompts: many query rows per cached head.
+//
+// Here the work per score decides, not the memory: the workgroup's eight waves take 16 * RT
+// query rows each and share what a step's 32 tokens cost to unpack, in LDS, in operand order
+// (double-buffered, one barrier per step; the next step's words are in registers meanwhile):
+//   K  its codes as exact integers, and its scales and biases as float32: a score costs one
+//      matrix-core pass and two multiply-adds per group;
+//   V  the values s c + b themselves, as two operands (leading bits, rest), so that the
+//      probabilities need no scale per token and group: they are split once, and
+//      p v = p_hi v_lo + p_lo v_hi + p_hi v_hi.
+// (Codes and scales for V, as in the single-token form, cost 11 vector operations per score
+// more, two of them per group, against a third matrix-core pass here.)
+// Tokens outside every row's range are zero in LDS.  A token that only some rows see can still
+// hold anything: where a step that is masked for the wave has values that are not finite,
+// which the unpacking notes, the wave multiplies without them and then adds their products
+// one by one to the rows that see them.
+constexpr int kRowWaves = 8;
+constexpr int kRowThreads = 64 * kRowWaves;
+
+// Largest finite value of the element type.
+template <class T>
+constexpr float largest() { return T::kDtype == QMM_BF16 ? 3.38953139e38f : 65504.0f; }
+
+// Whether the element of 16 bits b is infinite or NaN.
+template <class T>
+__device__ inline bool not_finite(uint32_t b) {
+  constexpr uint32_t kExp = T::kDtype == QMM_BF16 ? 0x7F80u : 0x7C00u;
+  return (b & kExp) == kExp;
+}
+
+template <class T, int D, int GS, int RT>
+__global__ __launch_bounds__(kRowThreads, 1) void attend_rows_kernel(const AttendArgs a) {
+  constexpr int KC = D / 32, NT = D / 16, NG = D / GS, CPG = GS / 32;
+  constexpr int kRows = 16 * RT;
+  constexpr int kKUnits = (2 * KC + kRowWaves - 1) / kRowWaves, kVUnits = (NT + kRowWaves - 1) / kRowWaves;
+  static_assert(NG * kStep <= kRowThreads, "one thread per scale word of a step");
+  struct Buffer {
+    u32x4 k[2 * KC][64];          // [tile, 32-element step][lane]
+    u32x4 v[2][NT][64];           // [leading bits, rest][16-element tile][lane]
+    float s[NG][kStep], b[NG][kStep];
+    uint32_t odd;                 // a value of v is not finite
+  };
+  __shared__ Buffer bufs[2];
+
+  const int lane = threadIdx.x & 63, col = lane & 15, h = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int split = blockIdx.x;
+  const int head = blockIdx.y % a.c.heads, row_tile = blockIdx.y / a.c.heads;
+  const int64_t b = blockIdx.z;
+  const int wg_base = row_tile * kRowWaves * kRows, base = wg_base + wave * kRows;
+
+  int len = a.lengths[b];
+  const bool bad = len < 0 || len > a.max_length;
+  if (bad) len = 0;
+  const int off = len - a.q_len;
+  const auto row_end = [&](int r) { return a.causal ? max(0, off + r / a.rep + 1) : len; };
+  const auto row_begin = [&](int r) { return a.window ? max(0, off + r / a.rep - a.window + 1) : 0; };
+  // ranges of the workgroup, and of this wave (empty for a wave without rows)
+  const int wg_last = min(a.rows, wg_base + kRowWaves * kRows) - 1;
+  const int wg_lo = row_begin(wg_base), wg_hi = row_end(wg_last);
+  const bool live = base < a.rows;
+  const int last = min(a.rows, base + kRows) - 1;
+  const int lo_min = live ? row_begin(base) : 0, hi_max = live ? row_end(last) : 0;
+  const int lo_max = live ? row_begin(last) : 0, hi_min = live ? row_end(base) : 0;
+  const int c0 = (wg_lo & ~(kStep - 1)) + split * a.chunk;
+  const int c1 = min(c0 + a.chunk, wg_hi);
+
+  // ---- a step's words, from global memory
+  const int32_t* table = a.table + b * a.table_stride;
+  const int64_t page_words = 2 * a.c.side;
+  const uint32_t* tile_at[2];      // K words of the tile's page; its token
+  int tile_token[2];
+  bool tile_bad[2], loaded_bad[2] = {false, false};
+  int page_next[2] = {0, 0}, token_next[2] = {0, 0};
+  const auto find = [&](int t0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = t0 + 16 * i;
+      page_next[i] = 0;
+      token_next[i] = 0;
+      if (t < wg_hi && t + 16 > wg_lo) {
+        const int blk = (int)(((uint64_t)((uint32_t)t >> 4) * a.page_recip) >> 40);
+        token_next[i] = t - blk * a.c.page_size;
+        page_next[i] = __builtin_amdgcn_readfirstlane(table[blk]);
+      }
+    }
+  };
+  uint32_t kw[kKUnits], vw[kVUnits][2], ksb = 0;
+  u32x4 vsb[kVUnits][2];
+  const int sb_token = threadIdx.x & (kStep - 1), sb_group = threadIdx.x / kStep;
+  const auto load = [&]() {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      tile_bad[i] = page_next[i] < 0 || page_next[i] >= a.c.pages;
+      tile_at[i] = a.c.data + ((int64_t)(tile_bad[i] ? 0 : page_next[i]) * a.c.heads + head) * page_words;
+      tile_token[i] = token_next[i];
+      loaded_bad[i] = tile_bad[i];
+    }
+#pragma unroll
+    for (int n = 0; n < kKUnits; ++n) {
+      const int u = wave + n * kRowWaves, i = u / KC, c = u - i * KC;
+      if (u < 2 * KC) kw[n] = tile_at[i][(tile_token[i] + col) * (D / 8) + h * KC + c];
+    }
+    if (sb_group < NG) {
+      const int i = sb_token >> 4;
+      ksb = (i ? tile_at[1] : tile_at[0])[(int64_t)a.c.page_size * (D / 8) + sb_group * a.c.page_size +
+                                         (i ? tile_token[1] : tile_token[0]) + (sb_token & 15)];
+    }
+#pragma unroll
+    for (int n = 0; n < kVUnits; ++n) {
+      const int u = wave + n * kRowWaves;
+      if (u < NT) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t* p = tile_at[i] + a.c.side;
+          vw[n][i] = p[((tile_token[i] / 4 + h) * 16 + col) * KC + u / 2];
+          vsb[n][i] = *(const u32x4*)(p + (int64_t)a.c.page_size * (D / 8) + (u * 16 / GS) * a.c.page_size +
+                                      tile_token[i] + 4 * h);
+        }
+      }
+    }
+  };
+  // ---- unpack them into a buffer, for the step at t0
+  const auto unpack = [&](Buffer& buf, int t0) {
+#pragma unroll
+    for (int n = 0; n < kKUnits; ++n) {
+      const int u = wave + n * kRowWaves;
+      if (u < 2 * KC) buf.k[u][lane] = codes4_to_v8<T>(kw[n]);
+    }
+    if (sb_group < NG) {
+      // a needed tile without a page of the pool makes the scores of those who see it NaN
+      const bool nan = (sb_token >> 4) ? loaded_bad[1] : loaded_bad[0];
+      buf.s[sb_group][sb_token] = nan ? __builtin_nanf("") : T::to_f32(ksb & 0xFFFFu);
+      buf.b[sb_group][sb_token] = T::to_f32(ksb >> 16);
+    }
+    bool odd = false;
+#pragma unroll
+    for (int n = 0; n < kVUnits; ++n) {
+      const int u = wave + n * kRowWaves;
+      if (u >= NT) continue;
+      u32x4 hi, lo;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t e = (u & 1 ? vw[n][i] >> 4 : vw[n][i]) & 0x0F0F0F0Fu;
+        float v[4], lead[4];   // lead: v, kept from rounding to an infinity
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int token = t0 + 16 * i + 4 * h + r;
+          v[r] = __builtin_fmaf(T::to_f32(vsb[n][i][r] & 0xFFFFu), (float)((e >> (8 * r)) & 0xFFu),
+                                T::to_f32(vsb[n][i][r] >> 16));
+          if (token < wg_lo || token >= wg_hi || loaded_bad[i]) v[r] = 0.f;
+          const bool finite = __builtin_fabsf(v[r]) <= FLT_MAX;
+          odd = odd || !finite;
+          lead[r] = finite ? __builtin_amdgcn_fmed3f(v[r], -largest<T>(), largest<T>()) : v[r];
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t u2 = T::pack2(lead[2 * r], lead[2 * r + 1]);
+          hi[2 * i + r] = u2;
+          lo[2 * i + r] = T::pack2(v[2 * r] - T::to_f32(u2 & 0xFFFFu), v[2 * r + 1] - T::to_f32(u2 >> 16));
+        }
+      }
+      buf.v[0][u][lane] = hi;
+      buf.v[1][u][lane] = lo;
+    }
+    if (odd) buf.odd = 1u;           // the same word from every lane that finds one
+  };
+  if (threadIdx.x < 2) bufs[threadIdx.x].odd = 0u;
+  if (c0 < c1) {
+    find(c0);
+    load();
+    if (c0 + kStep < c1) find(c0 + kStep);
+  }
+
+  typename T::v8 q[RT][KC];
+  float qsum[RT][NG], m[RT], l[RT];
+  int row_lo[RT], row_hi[RT];
+  f32x4 acc[RT][NT];
+  const uint32_t one2 = T::pack2(1.0f, 1.0f);
+  const u32x4 ones = {one2, one2, one2, one2};
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    const int r = min(base + 16 * t + col, a.rows - 1);
+    const int i = r / a.rep, g = r - i * a.rep;
+    const uint16_t* qp = (const uint16_t*)a.q + b * a.q_batch_stride + (int64_t)i * a.q_token_stride +
+                         (int64_t)(head * a.rep + g) * a.q_head_stride + 8 * h;
+#pragma unroll
+    for (int c = 0; c < KC; ++c) q[t][c] = as_v8<T>(interleave_even_odd(*(const u32x4*)(qp + 32 * c)));
+#pragma unroll
+    for (int gi = 0; gi < NG; ++gi) {
+      f32x4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < CPG; ++c) d = T::mfma(as_v8<T>(ones), q[t][gi * CPG + c], d);
+      qsum[t][gi] = d[0];
+    }
+    row_hi[t] = a.causal ? off + i + 1 : len;
+    row_lo[t] = a.window ? off + i - a.window + 1 : 0;
+    m[t] = kNone;
+    l[t] = 0.f;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  __syncthreads();                   // the flags are clear
+  if (c0 < c1) {
+    unpack(bufs[0], c0);
+    if (c0 + kStep < c1) {
+      load();
+      if (c0 + 2 * kStep < c1) find(c0 + 2 * kStep);
+    }
+  }
+  lds_barrier();
+
+  int at = 0;
+  for (int t0 = c0; t0 < c1; t0 += kStep, at ^= 1) {
+    const Buffer& buf = bufs[at];
+    if (t0 + kStep < c1) {
+      unpack(bufs[at ^ 1], t0 + kStep);
+      if (t0 + 2 * kStep < c1) {
+        load();
+        if (t0 + 3 * kStep < c1) find(t0 + 3 * kStep);
+      }
+    }
+    if (t0 < hi_max && t0 + kStep > lo_min) {
+      // ---- scores
+      float sc[RT][2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const f32x4 s = *(const f32x4*)&buf.s[g][16 * i + 4 * h], bb = *(const f32x4*)&buf.b[g][16 * i + 4 * h];
+          f32x4 d[RT];
+#pragma unroll
+          for (int t = 0; t < RT; ++t) d[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < CPG; ++c) {
+            const typename T::v8 kc = as_v8<T>(buf.k[i * KC + g * CPG + c][lane]);
+#pragma unroll
+            for (int t = 0; t < RT; ++t) d[t] = T::mfma(kc, q[t][g * CPG + c], d[t]);
+          }
+#pragma unroll
+          for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float x = g == 0 ? bb[r] * qsum[t][0] : __builtin_fmaf(bb[r], qsum[t][g], sc[t][i][r]);
+              sc[t][i][r] = __builtin_fmaf(s[r], d[t][r], x);
+            }
+        }
+      const bool masked = t0 < lo_max || t0 + kStep > hi_min;
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            sc[t][i][r] *= a.scale_log2;
+            if (masked) {
+              const int token = t0 + 16 * i + 4 * h + r;
+              sc[t][i][r] = token >= row_lo[t] && token < row_hi[t] ? sc[t][i][r] : -__builtin_inff();
+            }
+          }
+      // ---- probabilities
+      u32x4 ph[RT], pl[RT];
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        float top = fmaxf(fmaxf(sc[t][0][0], sc[t][0][1]), fmaxf(sc[t][0][2], sc[t][0][3]));
+        top = fmaxf(top, fmaxf(fmaxf(sc[t][1][0], sc[t][1][1]), fmaxf(sc[t][1][2], sc[t][1][3])));
+        if (__builtin_amdgcn_ballot_w64(top > m[t] + slack<T>()) != 0ull) {
+          top = fmaxf(top, __shfl_xor(top, 16));
+          top = fmaxf(top, __shfl_xor(top, 32));
+          const float raised = fmaxf(m[t], top);
+          const float f = __builtin_amdgcn_exp2f(m[t] - raised);
+          m[t] = raised;
+          l[t] *= f;
+#pragma unroll
+          for (int i = 0; i < NT; ++i) acc[t][i] *= f;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            sc[t][i][r] = __builtin_amdgcn_exp2f(sc[t][i][r] - m[t]);
+            l[t] += sc[t][i][r];
+          }
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          uint32_t uh, ul;
+          split2<T>(sc[t][n >> 1][2 * (n & 1)], sc[t][n >> 1][2 * (n & 1) + 1], &uh, &ul);
+          ph[t][n] = uh;
+          pl[t][n] = ul;
+        }
+      }
+      // ---- second product
+      const bool odd = masked && __builtin_amdgcn_readfirstlane(buf.odd) != 0u;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        u32x4 uh = buf.v[0][i][lane], ul = buf.v[1][i][lane];
+        if (odd) {
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            const uint32_t keep = (not_finite<T>(uh[n]) ? 0u : 0xFFFFu) | (not_finite<T>(uh[n] >> 16) ? 0u : 0xFFFF0000u);
+            uh[n] &= keep;
+            ul[n] &= keep;
+          }
+        }
+        const typename T::v8 vh = as_v8<T>(uh), vl = as_v8<T>(ul);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) acc[t][i] = T::mfma(vl, as_v8<T>(ph[t]), acc[t][i]);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) acc[t][i] = T::mfma(vh, as_v8<T>(pl[t]), acc[t][i]);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) acc[t][i] = T::mfma(vh, as_v8<T>(ph[t]), acc[t][i]);
+      }
+      if (odd) {
+#pragma unroll 1
+        for (int j = 0; j < kStep; ++j) {           // token j: tile j / 16, lane group j / 4 % 4, register j % 4
+          const int from = ((j >> 2) & 3) * 16, e = (j >> 4) * 4 + (j & 3);
+#pragma unroll
+          for (int t = 0; t < RT; ++t) {
+            float p = 0.f;
+#pragma unroll
+            for (int n = 0; n < 8; ++n) p = n == e ? sc[t][n >> 2][n & 3] : p;
+            p = __shfl(p, from + col);
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const uint32_t v = ((const uint16_t*)buf.v[0][i])[(from + 4 * h + r) * 8 + e];
+                if (p != 0.f && not_finite<T>(v)) acc[t][i][r] = __builtin_fmaf(p, T::to_f32(v), acc[t][i][r]);
+              }
+          }
+        }
+      }
+    }
+    lds_barrier();
+    // (a flag stays set: later steps of the buffer are then slow where masked, never wrong)
+  }
+
+  if (!live) return;
+  const int64_t row0 = (b * a.c.heads + head) * a.rows;
+  float* part_ml = a.part + (int64_t)gridDim.z * a.c.heads * a.rows * a.splits * D;
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    l[t] += __shfl_xor(l[t], 16);
+    l[t] += __shfl_xor(l[t], 32);
+    if (bad) {
+      l[t] = __builtin_nanf("");
+      m[t] = 0.f;
+    }
+    const int r = base + 16 * t + col;
+    if (r >= a.rows) continue;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) store4<T, D>(a, b, head, split, row0, r, 16 * i + 4 * h, acc[t][i], l[t]);
+    if (a.splits > 1 && h == 0) {
+      float* ml = part_ml + ((row0 + r) * a.splits + split) * 2;
+      ml[0] = m[t];
+      ml[1] = l[t];
     }
   }
 }
@@ -500,26 +857,28 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(const AttendArgs 
   *(uint2*)((uint16_t*)a.out + ((b * a.q_len + i) * (int64_t)a.q_heads + head * a.rep + g) * D + 4 * lane) = u;
 }
 
-template <class T, int D, int GS, int RT, bool BY_ROWS>
-hipError_t launch_form(const AttendArgs& a, const AttendPlan& p, hipStream_t stream) {
-  const int lds = BY_ROWS ? 0 : (kWaves * 16 * RT * (D + 4) + kWaves * 16 * RT * 2) * 4;
+template <class T, int D, int GS, int RT>
+hipError_t launch_tokens(const AttendArgs& a, const AttendPlan& p, dim3 grid, hipStream_t stream) {
+  const int lds = (kWaves * 16 * RT * (D + 4) + kWaves * 16 * RT * 2) * 4;
   if (lds > 64 * 1024) {
-    const hipError_t e = hipFuncSetAttribute((const void*)attend_kernel<T, D, GS, RT, BY_ROWS>,
+    const hipError_t e = hipFuncSetAttribute((const void*)attend_kernel<T, D, GS, RT>,
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
-  const dim3 grid((unsigned)p.splits, (unsigned)(a.c.heads * p.row_tiles), (unsigned)a.batch);
-  hipLaunchKernelGGL((attend_kernel<T, D, GS, RT, BY_ROWS>), grid, dim3(kThreads), lds, stream, a);
+  hipLaunchKernelGGL((attend_kernel<T, D, GS, RT>), grid, dim3(kThreads), lds, stream, a);
   return hipGetLastError();
 }
 
 template <class T, int D, int GS>
 hipError_t launch_shape(const AttendArgs& a, const AttendPlan& p, hipStream_t stream) {
+  const dim3 grid((unsigned)p.splits, (unsigned)(a.c.heads * p.row_tiles), (unsigned)a.batch);
   hipError_t e;
-  if (p.by_rows)
-    e = launch_form<T, D, GS, (D == 256 ? 2 : 4), true>(a, p, stream);
-  else
-    e = p.tile_rows == 16 ? launch_form<T, D, GS, 1, false>(a, p, stream) : launch_form<T, D, GS, 2, false>(a, p, stream);
+  if (p.by_rows) {
+    hipLaunchKernelGGL((attend_rows_kernel<T, D, GS, (D == 256 ? 1 : 2)>), grid, dim3(kRowThreads), 0, stream, a);
+    e = hipGetLastError();
+  } else {
+    e = p.tile_rows == 16 ? launch_tokens<T, D, GS, 1>(a, p, grid, stream) : launch_tokens<T, D, GS, 2>(a, p, grid, stream);
+  }
   if (e != hipSuccess || p.splits == 1) return e;
   hipLaunchKernelGGL((attend_join_kernel<T, D>), dim3((unsigned)(a.batch * a.c.heads * a.rows)), dim3(kThreads), 0,
                      stream, a);

@@ -49,8 +49,8 @@ int32_t check_attend(const qmm_kv_cache_t* cache, const qmm_kv_attend_t* q, bool
     return report(QMM_ERR_UNSUPPORTED, "kv_attend: window must be >= 0 and needs causal");
   if (q->max_blocks < 0 || q->table_stride < q->max_blocks || q->max_blocks > kMaxInt / cache->page_size)
     return report(QMM_ERR_SHAPE, "kv_attend: need 0 <= max_blocks <= table_stride, max_blocks * page_size < 2^31");
-  if (q->max_length < 0 || q->max_length > q->max_blocks * cache->page_size)
-    return report(QMM_ERR_SHAPE, "kv_attend: max_length must be in [0, max_blocks * page_size]");
+  if (q->max_length < 0 || q->max_length > q->max_blocks * cache->page_size || q->max_length > (1 << 30))
+    return report(QMM_ERR_SHAPE, "kv_attend: max_length must be in [0, max_blocks * page_size] and at most 2^30");
   if (q->q_batch_stride < 0 || q->q_token_stride < 0 || q->q_head_stride < 0)
     return report(QMM_ERR_LAYOUT, "kv_attend: negative q stride");
   if (q->q_batch_stride % 8 || q->q_token_stride % 8 || q->q_head_stride % 8)
@@ -91,36 +91,42 @@ int64_t part_floats(const AttendArgs& a, int64_t splits) {
 }  // namespace
 
 // Rows: up to 16 query rows per kv head (single tokens) take one 16-row tile per wave, the
-// workgroup's waves sharing out the tokens; up to 128 rows two tiles; more rows (prompts) four
-// tiles per wave (two at head_dim 256, whose accumulators are twice as large) and different
-// rows in each wave, so a code is unpacked once per 64 rows.
-// Splits: enough workgroups for kTarget in all, each of at least one step of every wave (128
-// tokens), or 512 tokens where each wave has its own rows and a split's sums are large.
-AttendPlan plan_attend(int64_t batch, int heads, int head_dim, int64_t rows, int64_t range) {
-  constexpr int64_t kTarget = 1024;
-  AttendPlan p{};
-  p.by_rows = rows > 128;
-  p.tile_rows = p.by_rows ? (head_dim == 256 ? 32 : 64) : (rows <= 16 ? 16 : 32);
-  const int64_t wg_rows = p.by_rows ? 4 * p.tile_rows : p.tile_rows;
-  p.row_tiles = (int32_t)((rows + wg_rows - 1) / wg_rows);
-  const int64_t wgs = std::max<int64_t>(1, batch * heads * p.row_tiles);
-  const int64_t step = p.by_rows ? 512 : 128;
-  const int64_t want = std::max<int64_t>(1, (p.by_rows ? 512 : kTarget) / wgs);
-  const int64_t steps = std::max<int64_t>(1, (range + step - 1) / step);
-  const int64_t per = std::max<int64_t>(1, (steps + want - 1) / want);
-  p.chunk = (int32_t)(per * step);
-  p.splits = (int32_t)((steps + per - 1) / per);
-  return p;
+// workgroup's waves sharing out the tokens; up to 128 rows two tiles; more rows (prompts) take
+// the form whose eight waves have two tiles of their own each (one at head_dim 256, whose
+// accumulators are twice as large) and share the unpacked tokens.
+// Splits: as many as make `want` workgroups, each of at least one step of every wave (128
+// tokens), or 512 tokens in the prompt form, where a split's sums are large.
+namespace {
+
+struct Shape {
+  int32_t by_rows, tile_rows, row_tiles;
+  int64_t step, want;
+};
+
+Shape shape_of(int64_t batch, int heads, int head_dim, int64_t rows) {
+  Shape s{};
+  s.by_rows = rows > 128;
+  s.tile_rows = s.by_rows ? (head_dim == 256 ? 16 : 32) : (rows <= 16 ? 16 : 32);
+  const int64_t wg_rows = s.by_rows ? 8 * s.tile_rows : s.tile_rows;
+  s.row_tiles = (int32_t)((rows + wg_rows - 1) / wg_rows);
+  s.step = s.by_rows ? 512 : 128;
+  s.want = std::max<int64_t>(1, (s.by_rows ? 256 : 1024) / std::max<int64_t>(1, batch * heads * s.row_tiles));
+  return s;
 }
 
-// Splits that no shorter range of the same call exceeds: min(steps, the wanted count) bounds
-// the plan's splits and grows with the range.
+}  // namespace
+
+AttendPlan plan_attend(int64_t batch, int heads, int head_dim, int64_t rows, int64_t range) {
+  const Shape s = shape_of(batch, heads, head_dim, rows);
+  const int64_t steps = std::max<int64_t>(1, (range + s.step - 1) / s.step);
+  const int64_t per = std::max<int64_t>(1, (steps + s.want - 1) / s.want);
+  return AttendPlan{s.tile_rows, s.by_rows, s.row_tiles, (int32_t)(per * s.step), (int32_t)((steps + per - 1) / per)};
+}
+
+// Splits that no shorter range of the same call exceeds.
 static int64_t most_splits(const AttendArgs& a) {
-  const AttendPlan one = plan_attend(a.batch, a.c.heads, a.c.head_dim, a.rows, 1);
-  const int64_t wgs = std::max<int64_t>(1, a.batch * a.c.heads * one.row_tiles);
-  const int64_t step = one.by_rows ? 512 : 128;
-  const int64_t want = std::max<int64_t>(1, (one.by_rows ? 512 : 1024) / wgs);
-  return std::min<int64_t>(want, std::max<int64_t>(1, (a.max_length + step - 1) / step));
+  const Shape s = shape_of(a.batch, a.c.heads, a.c.head_dim, a.rows);
+  return std::min<int64_t>(s.want, std::max<int64_t>(1, (a.max_length + s.step - 1) / s.step));
 }
 
 }  // namespace kv

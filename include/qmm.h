@@ -336,7 +336,7 @@ typedef struct {
   const int32_t* lengths;  /* DEVICE int32 [batch]; a length outside [0, max_length] makes
                             * the sequence's outputs NaN                                     */
   int64_t max_length;      /* the most tokens any sequence has, known to the host: sizes the
-                            * launch; <= max_blocks * page_size                              */
+                            * launch; <= max_blocks * page_size, <= 2^30                      */
 } qmm_kv_attend_t;
 
 /* Attention over the cache: out, DEVICE, dense [batch, q_len, q_heads, head_dim] of dtype,
