@@ -450,22 +450,18 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS, RT>())) void attend_ke
 //      p v = p_hi v_lo + p_lo v_hi + p_hi v_hi.
 // (Codes and scales for V, as in the single-token form, cost 11 vector operations per score
 // more, two of them per group, against a third matrix-core pass here.)
-// Tokens outside every row's range are zero in LDS.  A token that only some rows see can still
-// hold anything: where a step that is masked for the wave has values that are not finite,
-// which the unpacking notes, the wave multiplies without them and then adds their products
-// one by one to the rows that see them.
+// Tokens outside every row's range are zero in LDS, and so are values that are not finite,
+// which a token that only some rows see may hold: the unpacking notes the token, and a row
+// that gives it weight becomes NaN.
+// Scores leave the multiply-adds relative to the running maximum: -m is where they start.
 constexpr int kRowWaves = 8;
 constexpr int kRowThreads = 64 * kRowWaves;
 
-// Largest finite value of the element type.
+// split2 with hi rounded to nearest: for values below half the type's largest.
 template <class T>
-constexpr float largest() { return T::kDtype == QMM_BF16 ? 3.38953139e38f : 65504.0f; }
-
-// Whether the element of 16 bits b is infinite or NaN.
-template <class T>
-__device__ inline bool not_finite(uint32_t b) {
-  constexpr uint32_t kExp = T::kDtype == QMM_BF16 ? 0x7F80u : 0x7C00u;
-  return (b & kExp) == kExp;
+__device__ inline void split2_near(float x, float y, uint32_t* hi, uint32_t* lo) {
+  *hi = T::pack2(x, y);
+  *lo = T::pack2(x - T::to_f32(*hi & 0xFFFFu), y - T::to_f32(*hi >> 16));
 }
 
 template <class T, int D, int GS, int RT>
@@ -477,10 +473,10 @@ __global__ __launch_bounds__(kRowThreads, 1) void attend_rows_kernel(const Atten
   struct Buffer {
     u32x4 k[2 * KC][64];          // [tile, 32-element step][lane]
     u32x4 v[2][NT][64];           // [leading bits, rest][16-element tile][lane]
-    float s[NG][kStep], b[NG][kStep];
-    uint32_t odd;                 // a value of v is not finite
+    float s[NG][kStep], b[NG][kStep];   // times the score's scale
   };
   __shared__ Buffer bufs[2];
+  __shared__ uint32_t odd_tokens[4];    // by step % 4: tokens of the step with values that are not finite
 
   const int lane = threadIdx.x & 63, col = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -570,10 +566,10 @@ __global__ __launch_bounds__(kRowThreads, 1) void attend_rows_kernel(const Atten
     if (sb_group < NG) {
       // a needed tile without a page of the pool makes the scores of those who see it NaN
       const bool nan = (sb_token >> 4) ? loaded_bad[1] : loaded_bad[0];
-      buf.s[sb_group][sb_token] = nan ? __builtin_nanf("") : T::to_f32(ksb & 0xFFFFu);
-      buf.b[sb_group][sb_token] = T::to_f32(ksb >> 16);
+      buf.s[sb_group][sb_token] = nan ? __builtin_nanf("") : T::to_f32(ksb & 0xFFFFu) * a.scale_log2;
+      buf.b[sb_group][sb_token] = T::to_f32(ksb >> 16) * a.scale_log2;
     }
-    bool odd = false;
+    const bool edge = t0 < wg_lo || t0 + kStep > wg_hi || loaded_bad[0] || loaded_bad[1];
 #pragma unroll
     for (int n = 0; n < kVUnits; ++n) {
       const int u = wave + n * kRowWaves;
@@ -582,30 +578,38 @@ __global__ __launch_bounds__(kRowThreads, 1) void attend_rows_kernel(const Atten
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint32_t e = (u & 1 ? vw[n][i] >> 4 : vw[n][i]) & 0x0F0F0F0Fu;
-        float v[4], lead[4];   // lead: v, kept from rounding to an infinity
+        float v[4], zero = 0.f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int token = t0 + 16 * i + 4 * h + r;
           v[r] = __builtin_fmaf(T::to_f32(vsb[n][i][r] & 0xFFFFu), (float)((e >> (8 * r)) & 0xFFu),
                                 T::to_f32(vsb[n][i][r] >> 16));
-          if (token < wg_lo || token >= wg_hi || loaded_bad[i]) v[r] = 0.f;
-          const bool finite = __builtin_fabsf(v[r]) <= FLT_MAX;
-          odd = odd || !finite;
-          lead[r] = finite ? __builtin_amdgcn_fmed3f(v[r], -largest<T>(), largest<T>()) : v[r];
+          if (edge) {
+            const int token = t0 + 16 * i + 4 * h + r;
+            if (token < wg_lo || token >= wg_hi || loaded_bad[i]) v[r] = 0.f;
+          }
+          zero = __builtin_fmaf(v[r], 0.f, zero);      // NaN for an infinity or a NaN
+        }
+        if (__builtin_amdgcn_ballot_w64(zero != 0.f) != 0ull) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (!(__builtin_fabsf(v[r]) <= FLT_MAX)) {
+              v[r] = 0.f;
+              atomicOr(&odd_tokens[(t0 / kStep) & 3], 1u << (16 * i + 4 * h + r));
+            }
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const uint32_t u2 = T::pack2(lead[2 * r], lead[2 * r + 1]);
-          hi[2 * i + r] = u2;
-          lo[2 * i + r] = T::pack2(v[2 * r] - T::to_f32(u2 & 0xFFFFu), v[2 * r + 1] - T::to_f32(u2 >> 16));
+          uint32_t uh, ul;
+          split2<T>(v[2 * r], v[2 * r + 1], &uh, &ul);
+          hi[2 * i + r] = uh;
+          lo[2 * i + r] = ul;
         }
       }
       buf.v[0][u][lane] = hi;
       buf.v[1][u][lane] = lo;
     }
-    if (odd) buf.odd = 1u;           // the same word from every lane that finds one
   };
-  if (threadIdx.x < 2) bufs[threadIdx.x].odd = 0u;
+  if (threadIdx.x < 4) odd_tokens[threadIdx.x] = 0u;
   if (c0 < c1) {
     find(c0);
     load();
@@ -614,6 +618,7 @@ __global__ __launch_bounds__(kRowThreads, 1) void attend_rows_kernel(const Atten
 
   typename T::v8 q[RT][KC];
   float qsum[RT][NG], m[RT], l[RT];
+  float over[RT];                    // scores above m + over raise m: any score at first, then slack
   int row_lo[RT], row_hi[RT];
   f32x4 acc[RT][NT];
   const uint32_t one2 = T::pack2(1.0f, 1.0f);
@@ -635,7 +640,8 @@ __global__ __launch_bounds__(kRowThreads, 1) void attend_rows_kernel(const Atten
     }
     row_hi[t] = a.causal ? off + i + 1 : len;
     row_lo[t] = a.window ? off + i - a.window + 1 : 0;
-    m[t] = kNone;
+    m[t] = 0.f;
+    over[t] = -__builtin_inff();
     l[t] = 0.f;
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -650,16 +656,22 @@ __global__ __launch_bounds__(kRowThreads, 1) void attend_rows_kernel(const Atten
   }
   lds_barrier();
 
+  // The next step's unpacking: half of the waves do it before the step's products and half
+  // after them, so that the two waves of a SIMD do not need the matrix core at the same time.
+  const auto prepare = [&](int t0, int to) {
+    if (t0 + kStep >= c1) return;
+    unpack(bufs[to], t0 + kStep);
+    if (t0 + 2 * kStep < c1) {
+      load();
+      if (t0 + 3 * kStep < c1) find(t0 + 3 * kStep);
+    }
+  };
   int at = 0;
   for (int t0 = c0; t0 < c1; t0 += kStep, at ^= 1) {
     const Buffer& buf = bufs[at];
-    if (t0 + kStep < c1) {
-      unpack(bufs[at ^ 1], t0 + kStep);
-      if (t0 + 2 * kStep < c1) {
-        load();
-        if (t0 + 3 * kStep < c1) find(t0 + 3 * kStep);
-      }
-    }
+    const int step = t0 / kStep;
+    if (threadIdx.x == 0) odd_tokens[(step + 2) & 3] = 0u;   // last read two steps ago, next set in the next one
+    if (wave < kRowWaves / 2) prepare(t0, at ^ 1);
     if (t0 < hi_max && t0 + kStep > lo_min) {
       // ---- scores
       float sc[RT][2][4];
@@ -681,68 +693,64 @@ __global__ __launch_bounds__(kRowThreads, 1) void attend_rows_kernel(const Atten
           for (int t = 0; t < RT; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              const float x = g == 0 ? bb[r] * qsum[t][0] : __builtin_fmaf(bb[r], qsum[t][g], sc[t][i][r]);
+              const float x = __builtin_fmaf(bb[r], qsum[t][g], g == 0 ? -m[t] : sc[t][i][r]);
               sc[t][i][r] = __builtin_fmaf(s[r], d[t][r], x);
             }
         }
-      const bool masked = t0 < lo_max || t0 + kStep > hi_min;
+      if (t0 < lo_max || t0 + kStep > hi_min) {   // rows that do not see every token of the step
 #pragma unroll
-      for (int t = 0; t < RT; ++t)
+        for (int t = 0; t < RT; ++t)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            sc[t][i][r] *= a.scale_log2;
-            if (masked) {
+            for (int r = 0; r < 4; ++r) {
               const int token = t0 + 16 * i + 4 * h + r;
               sc[t][i][r] = token >= row_lo[t] && token < row_hi[t] ? sc[t][i][r] : -__builtin_inff();
             }
-          }
+      }
       // ---- probabilities
       u32x4 ph[RT], pl[RT];
+      const uint32_t odd = __builtin_amdgcn_readfirstlane(odd_tokens[step & 3]);
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
         float top = fmaxf(fmaxf(sc[t][0][0], sc[t][0][1]), fmaxf(sc[t][0][2], sc[t][0][3]));
         top = fmaxf(top, fmaxf(fmaxf(sc[t][1][0], sc[t][1][1]), fmaxf(sc[t][1][2], sc[t][1][3])));
-        if (__builtin_amdgcn_ballot_w64(top > m[t] + slack<T>()) != 0ull) {
+        if (__builtin_amdgcn_ballot_w64(top > over[t]) != 0ull) {
           top = fmaxf(top, __shfl_xor(top, 16));
           top = fmaxf(top, __shfl_xor(top, 32));
-          const float raised = fmaxf(m[t], top);
-          const float f = __builtin_amdgcn_exp2f(m[t] - raised);
-          m[t] = raised;
+          const bool some = top > -__builtin_inff();             // false: nothing seen yet, m stays
+          const float up = over[t] < 0.f ? (some ? top : 0.f) : fmaxf(top, 0.f);
+          over[t] = over[t] < 0.f && !some ? over[t] : slack<T>();
+          const float f = __builtin_amdgcn_exp2f(-up);
+          m[t] += up;
           l[t] *= f;
 #pragma unroll
           for (int i = 0; i < NT; ++i) acc[t][i] *= f;
+#pragma unroll
+          for (int n = 0; n < 8; ++n) sc[t][n >> 2][n & 3] -= up;
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int n = 0; n < 8; ++n) {
+          sc[t][n >> 2][n & 3] = __builtin_amdgcn_exp2f(sc[t][n >> 2][n & 3]);
+          l[t] += sc[t][n >> 2][n & 3];
+        }
+        if (odd) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            sc[t][i][r] = __builtin_amdgcn_exp2f(sc[t][i][r] - m[t]);
-            l[t] += sc[t][i][r];
-          }
+          for (int n = 0; n < 8; ++n)
+            if (((odd >> (16 * (n >> 2) + 4 * h + (n & 3))) & 1u) && sc[t][n >> 2][n & 3] != 0.f) l[t] = __builtin_nanf("");
+        }
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
           uint32_t uh, ul;
-          split2<T>(sc[t][n >> 1][2 * (n & 1)], sc[t][n >> 1][2 * (n & 1) + 1], &uh, &ul);
+          split2_near<T>(sc[t][n >> 1][2 * (n & 1)], sc[t][n >> 1][2 * (n & 1) + 1], &uh, &ul);
           ph[t][n] = uh;
           pl[t][n] = ul;
         }
       }
       // ---- second product
-      const bool odd = masked && __builtin_amdgcn_readfirstlane(buf.odd) != 0u;
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        u32x4 uh = buf.v[0][i][lane], ul = buf.v[1][i][lane];
-        if (odd) {
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const uint32_t keep = (not_finite<T>(uh[n]) ? 0u : 0xFFFFu) | (not_finite<T>(uh[n] >> 16) ? 0u : 0xFFFF0000u);
-            uh[n] &= keep;
-            ul[n] &= keep;
-          }
-        }
-        const typename T::v8 vh = as_v8<T>(uh), vl = as_v8<T>(ul);
+        const typename T::v8 vh = as_v8<T>(buf.v[0][i][lane]), vl = as_v8<T>(buf.v[1][i][lane]);
 #pragma unroll
         for (int t = 0; t < RT; ++t) acc[t][i] = T::mfma(vl, as_v8<T>(ph[t]), acc[t][i]);
 #pragma unroll
@@ -750,29 +758,9 @@ __global__ __launch_bounds__(kRowThreads, 1) void attend_rows_kernel(const Atten
 #pragma unroll
         for (int t = 0; t < RT; ++t) acc[t][i] = T::mfma(vh, as_v8<T>(ph[t]), acc[t][i]);
       }
-      if (odd) {
-#pragma unroll 1
-        for (int j = 0; j < kStep; ++j) {           // token j: tile j / 16, lane group j / 4 % 4, register j % 4
-          const int from = ((j >> 2) & 3) * 16, e = (j >> 4) * 4 + (j & 3);
-#pragma unroll
-          for (int t = 0; t < RT; ++t) {
-            float p = 0.f;
-#pragma unroll
-            for (int n = 0; n < 8; ++n) p = n == e ? sc[t][n >> 2][n & 3] : p;
-            p = __shfl(p, from + col);
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const uint32_t v = ((const uint16_t*)buf.v[0][i])[(from + 4 * h + r) * 8 + e];
-                if (p != 0.f && not_finite<T>(v)) acc[t][i][r] = __builtin_fmaf(p, T::to_f32(v), acc[t][i][r]);
-              }
-          }
-        }
-      }
     }
+    if (wave >= kRowWaves / 2) prepare(t0, at ^ 1);
     lds_barrier();
-    // (a flag stays set: later steps of the buffer are then slow where masked, never wrong)
   }
 
   if (!live) return;
@@ -792,7 +780,7 @@ __global__ __launch_bounds__(kRowThreads, 1) void attend_rows_kernel(const Atten
     for (int i = 0; i < NT; ++i) store4<T, D>(a, b, head, split, row0, r, 16 * i + 4 * h, acc[t][i], l[t]);
     if (a.splits > 1 && h == 0) {
       float* ml = part_ml + ((row0 + r) * a.splits + split) * 2;
-      ml[0] = m[t];
+      ml[0] = over[t] < 0.f && !bad ? kNone : m[t];   // kNone: no token of the split was seen
       ml[1] = l[t];
     }
   }
@@ -832,7 +820,7 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(const AttendArgs 
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      if (s0 + i * kGroups >= a.splits || m[i] == kNone) continue;   // no token of the split was seen
+      if (s0 + i * kGroups >= a.splits || l[i] == 0.f) continue;   // no token of the split was seen
       const float f = __builtin_amdgcn_exp2f(m[i] - top);
       sum = __builtin_fmaf(f, l[i], sum);
       o += f * v[i];

@@ -246,6 +246,24 @@ def test_attend_bad_lengths_and_pages_give_nan():
         s.check(y, queries, 64 ** -0.5, skip=(1, 2))
 
 
+@pytest.mark.parametrize("q_len", [1, 140])
+def test_attend_a_missing_page_reaches_the_output_through_the_splits(q_len):
+    """One page of a long sequence is not in the pool: the queries that need it are NaN, the
+    ones before it (and other sequences) are not."""
+    import bit_affine_quantized_qmv_amd as q
+    s = Setup([3000, 2900], 1, 64, 32, 16, "bf16", seed=21)
+    dev = s.len_dev.device
+    queries = _rows((2, q_len, 2, 64), "bf16", 22, loud=False)
+    for block in (1000 // 16, (3000 - q_len // 2 - 1) // 16):
+        table = s.table.clone()
+        table[0, block] = 10 ** 6
+        y = q.kv_attend(queries.to(dev), s.cache, table, s.len_dev)
+        torch.cuda.synchronize()
+        nan = torch.isnan(y.float())
+        needs = torch.tensor([3000 - q_len + i >= 16 * block for i in range(q_len)])
+        assert nan[0][needs].all() and not nan[0][~needs].any() and not nan[1].any()
+
+
 def test_attend_same_bits_again_on_another_stream_and_in_a_graph():
     import bit_affine_quantized_qmv_amd as q
     s = Setup([900, 17, 300], 2, 128, 64, 16, "bf16", seed=17)
