@@ -17,8 +17,8 @@
 // e < 4, 4h + e - 4 of the second one otherwise.
 //
 // Softmax: m, the sum of p, the bias sums and both accumulators are float32.  m is raised only
-// when a score exceeds it by more than kSlack (in powers of two), so most steps rescale
-// nothing; p is then at most 2^kSlack.  p_j s_jg goes to the matrix cores as two operands of
+// when a score exceeds it by more than slack() (in powers of two), so most steps rescale
+// nothing; p is then at most 2^slack.  p_j s_jg goes to the matrix cores as two operands of
 // the element type, its leading bits and the rest (split2), so that the product carries 16
 // (bf16) or 22 (fp16) bits of it: with one operand, a row that attends to one token would
 // return that token's codes with an error of up to 2^-8 (bf16) of their span.
@@ -99,26 +99,38 @@ __device__ inline void store4(const AttendArgs& a, int64_t b, int head, int spli
   }
 }
 
-// Workgroups per compute unit that the registers allow: the single-token form (one row tile) is
-// bound by the latency of its loads and takes four.
-template <int D, int GS, int RT>
-constexpr int workgroups() { return RT > 1 || D > 128 ? 1 : (D / GS == 1 ? 4 : (D / GS == 2 ? 3 : 2)); }
+// ---- up to 512 query rows per cached head: single tokens, drafted tokens.
+//
+// A workgroup takes 16 query rows of one cached head and one split of the tokens; its four waves
+// take the split's 32-token steps in turn, each with its own softmax, and meet in LDS once at
+// the end.  K and V of the next step are in flight while a step is computed, the pages of the
+// step after it are looked up already.  Two tiles of 16 rows per wave would unpack each code
+// once for 32 rows, but their registers leave one or two waves per SIMD: slower at every size
+// measured (20 rows: 63 us against 42; 128 rows: 66 against 43; 8192 tokens, 8 heads of 128).
+// What bounds it: a step is 384 vector instructions, about 1600 cycles, for 4.6 KB of codes and
+// scales, so at 5 TB/s the vector units are as busy as the memory; with lengths that differ,
+// what is left is the longest sequences' share.  Measured: 131071 tokens, 8 cached heads of
+// 128 elements 35 us (4.1 TB/s); 32 sequences of 0 to 8192 tokens 53 us (2.9 TB/s).
 
-template <class T, int D, int GS, int RT>
-__global__ __launch_bounds__(kThreads, (workgroups<D, GS, RT>())) void attend_kernel(const AttendArgs a) {
+// Workgroups per compute unit that the registers allow: the loads' latency decides, so as many
+// as possible without spills.
+template <int D, int GS>
+constexpr int workgroups() { return D > 128 ? 1 : (D / GS == 1 ? 4 : (D / GS == 2 ? 3 : 2)); }
+
+template <class T, int D, int GS>
+__global__ __launch_bounds__(kThreads, (workgroups<D, GS>())) void attend_kernel(const AttendArgs a) {
   constexpr int KC = D / 32;          // 32-element steps of a score; code words per lane and tile
   constexpr int NT = D / 16;          // 16-element output tiles
   constexpr int NG = D / GS;
   constexpr int CPG = GS / 32;
-  constexpr int kRows = 16 * RT;      // query rows per wave
+  constexpr int kRows = 16;           // query rows per workgroup
   constexpr int kPitch = D + 4;       // LDS row of the merge, padded against bank conflicts
-  extern __shared__ float lds[];
 
   const int lane = threadIdx.x & 63, col = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int split = blockIdx.x;
-  const int head = blockIdx.y % a.c.heads, row_tile = blockIdx.y / a.c.heads;
-  const int64_t b = blockIdx.z;
+  const int split = blockIdx.z;
+  const int head = blockIdx.x % a.c.heads, row_tile = blockIdx.x / a.c.heads;
+  const int64_t b = blockIdx.y;
   const int base = row_tile * kRows;
 
   int len = a.lengths[b];
@@ -134,22 +146,19 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS, RT>())) void attend_ke
   const int c0 = (lo_min & ~(kStep - 1)) + split * a.chunk;
   const int c1 = min(c0 + a.chunk, hi_max);
   const int stride = kStep * kWaves;
+  // scores stay unscaled until their exponential, so that one multiply-add scales and subtracts
+  // m: the scale's sign goes to q, and zero becomes the least number (masked scores are -inf)
+  const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+  const float magnitude = __builtin_fabsf(a.scale_log2), scale = magnitude < FLT_MIN ? FLT_MIN : magnitude;
 
-  float m[RT], l[RT], bsum[RT][NG];
-  f32x4 acc[RT][NT];
+  float m = kNone, l = 0.f, bsum[NG] = {};
+  f32x4 acc[NT];
 #pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    m[t] = kNone;
-    l[t] = 0.f;
-#pragma unroll
-    for (int g = 0; g < NG; ++g) bsum[t][g] = 0.f;
-#pragma unroll
-    for (int i = 0; i < NT; ++i) acc[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
+  for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   // The page of a 16-token tile that starts at token t0, and the token's place in it.  Tiles
-  // that no row sees read page 0 (their tokens are masked); a tile that is needed and has no
-  // page of the pool gets NaN scales, and with them the rows that see it.
+  // that no row sees read page 0 (their tokens are masked), and so do needed ones that have no
+  // page of the pool: rows that see those get NaN scores.
   const int32_t* table = a.table + b * a.table_stride;
   const int64_t page_words = 2 * a.c.side;
   struct Place {
@@ -200,15 +209,7 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS, RT>())) void attend_ke
   };
   auto load_k = [&]() {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      load_side(ks, i, base_next[i], token_next[i], false);
-      if (bad_next[i]) {
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) ks.sb[i][g][r] = 0x7FFF7FFFu;
-      }
-    }
+    for (int i = 0; i < 2; ++i) load_side(ks, i, base_next[i], token_next[i], false);
   };
   auto load_v = [&]() {
 #pragma unroll
@@ -221,144 +222,102 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS, RT>())) void attend_ke
     take();
     load_k();
     load_v();
-    if (first + stride < c1) find(first + stride);
+    find(first + stride);
   }
 
-  // query operands: column col of row tile t is query row base + 16 t + col
-  typename T::v8 q[RT][KC];
-  float qsum[RT][NG];
-  int row_lo[RT], row_hi[RT];
+  // query operands: column col is query row base + col (rows past the last repeat it and are not stored)
+  typename T::v8 q[KC];
+  float qsum[NG];
   const uint32_t one2 = T::pack2(1.0f, 1.0f);
   const u32x4 ones = {one2, one2, one2, one2};
+  const int row = min(base + col, a.rows - 1);
+  const int query = row / a.rep;
+  const uint16_t* qp = (const uint16_t*)a.q + b * a.q_batch_stride + (int64_t)query * a.q_token_stride +
+                       (int64_t)(head * a.rep + row - query * a.rep) * a.q_head_stride + 8 * h;
 #pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    const int r = min(base + 16 * t + col, a.rows - 1);   // rows past the last repeat it and are not stored
-    const int i = r / a.rep, g = r - i * a.rep;
-    const uint16_t* qp = (const uint16_t*)a.q + b * a.q_batch_stride + (int64_t)i * a.q_token_stride +
-                         (int64_t)(head * a.rep + g) * a.q_head_stride + 8 * h;
+  for (int c = 0; c < KC; ++c) q[c] = as_v8<T>(interleave_even_odd(*(const u32x4*)(qp + 32 * c) ^ flip));
 #pragma unroll
-    for (int c = 0; c < KC; ++c) q[t][c] = as_v8<T>(interleave_even_odd(*(const u32x4*)(qp + 32 * c)));
+  for (int g = 0; g < NG; ++g) {
+    f32x4 d = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int gi = 0; gi < NG; ++gi) {
-      f32x4 d = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < CPG; ++c) d = T::mfma(as_v8<T>(ones), q[t][gi * CPG + c], d);
-      qsum[t][gi] = d[0];
-    }
-    row_hi[t] = a.causal ? off + i + 1 : len;
-    row_lo[t] = a.window ? off + i - a.window + 1 : 0;
+    for (int c = 0; c < CPG; ++c) d = T::mfma(as_v8<T>(ones), q[g * CPG + c], d);
+    qsum[g] = d[0];
   }
+  const int row_hi = a.causal ? off + query + 1 : len;
+  const int row_lo = a.window ? off + query - a.window + 1 : 0;
 
   for (int t0 = first; t0 < c1; t0 += stride) {
-    const bool more = t0 + stride < c1;
-    // ---- scores: sc[t][i][r] of token t0 + 16 i + 4 h + r
-    float sc[RT][2][4];
+    const bool bad_now[2] = {bad_next[0], bad_next[1]};
+    // ---- scores: sc[i][r] of token t0 + 16 i + 4 h + r
+    float sc[2][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      u32x4 kc[KC];
 #pragma unroll
-      for (int c = 0; c < KC; ++c) kc[c] = codes4_to_v8<T>(ks.code[i][c]);
-      float s[NG][4], bb[NG][4];
+      for (int g = 0; g < NG; ++g) {
+        f32x4 d = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int g = 0; g < NG; ++g)
+        for (int c = g * CPG; c < (g + 1) * CPG; ++c) d = T::mfma(as_v8<T>(codes4_to_v8<T>(ks.code[i][c])), q[c], d);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          s[g][r] = T::to_f32(ks.sb[i][g][r] & 0xFFFFu);
-          bb[g][r] = T::to_f32(ks.sb[i][g][r] >> 16);
+          const float s = T::to_f32(ks.sb[i][g][r] & 0xFFFFu), kb = T::to_f32(ks.sb[i][g][r] >> 16);
+          sc[i][r] = __builtin_fmaf(s, d[r], g == 0 ? kb * qsum[0] : __builtin_fmaf(kb, qsum[g], sc[i][r]));
         }
-#pragma unroll
-      for (int t = 0; t < RT; ++t) {
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          f32x4 d = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int c = 0; c < CPG; ++c) d = T::mfma(as_v8<T>(kc[g * CPG + c]), q[t][g * CPG + c], d);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float x = g == 0 ? bb[0][r] * qsum[t][0] : __builtin_fmaf(bb[g][r], qsum[t][g], sc[t][i][r]);
-            sc[t][i][r] = __builtin_fmaf(s[g][r], d[r], x);
-          }
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) sc[t][i][r] *= a.scale_log2;
       }
     }
-    if (more) {
-      take();
-      load_k();
-      if (t0 + 2 * stride < c1) find(t0 + 2 * stride);
-    }
-    // ---- rows that do not see every token of the step
-    const bool masked = t0 < lo_max || t0 + kStep > hi_min;
-    uint32_t seen[RT];
-    if (masked) {
-#pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        seen[t] = 0u;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int token = t0 + 16 * i + 4 * h + r;
-            const bool ok = token >= row_lo[t] && token < row_hi[t];
-            seen[t] |= ok ? 1u << (4 * i + r) : 0u;
-            sc[t][i][r] = ok ? sc[t][i][r] : -__builtin_inff();
-          }
-      }
-    }
-    // ---- probabilities
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      float top = fmaxf(fmaxf(sc[t][0][0], sc[t][0][1]), fmaxf(sc[t][0][2], sc[t][0][3]));
-      top = fmaxf(top, fmaxf(fmaxf(sc[t][1][0], sc[t][1][1]), fmaxf(sc[t][1][2], sc[t][1][3])));
-      if (__builtin_amdgcn_ballot_w64(top > m[t] + slack<T>()) != 0ull) {
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float raised = fmaxf(m[t], top);
-        const float f = __builtin_amdgcn_exp2f(m[t] - raised);
-        m[t] = raised;
-        l[t] *= f;
-#pragma unroll
-        for (int g = 0; g < NG; ++g) bsum[t][g] *= f;
-#pragma unroll
-        for (int i = 0; i < NT; ++i) acc[t][i] *= f;
-      }
+    take();                          // past the last step: words of page 0, not used
+    load_k();
+    find(t0 + 2 * stride);
+    // ---- rows that do not see every token of the step, and tiles without a page of the pool
+    if (t0 < lo_max || t0 + kStep > hi_min || bad_now[0] || bad_now[1]) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          sc[t][i][r] = __builtin_amdgcn_exp2f(sc[t][i][r] - m[t]);
-          l[t] += sc[t][i][r];
+          const int token = t0 + 16 * i + 4 * h + r;
+          const bool seen = token >= row_lo && token < row_hi;
+          sc[i][r] = seen ? (bad_now[i] ? __builtin_nanf("") : sc[i][r]) : -__builtin_inff();
+#pragma unroll
+          for (int g = 0; g < NG; ++g) vs.sb[i][g][r] = seen ? vs.sb[i][g][r] : 0u;   // whatever it holds, it adds nothing
         }
+    }
+    // ---- probabilities
+    float top = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3]));
+    top = fmaxf(top, fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3]))) * scale;
+    if (__builtin_amdgcn_ballot_w64(top > m + slack<T>()) != 0ull) {
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float raised = fmaxf(m, top);
+      const float f = __builtin_amdgcn_exp2f(m - raised);
+      m = raised;
+      l *= f;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) bsum[g] *= f;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) acc[i] *= f;
+    }
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      float& p = sc[n >> 2][n & 3];
+      p = __builtin_amdgcn_exp2f(__builtin_fmaf(p, scale, -m));
+      l += p;
     }
     // ---- second product, group by group
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      u32x4 hi[RT], lo[RT];
+      float x[8];
 #pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        float x[2][4];
+      for (int n = 0; n < 8; ++n) {
+        const uint32_t sb = vs.sb[n >> 2][g][n & 3];
+        x[n] = sc[n >> 2][n & 3] * T::to_f32(sb & 0xFFFFu);
+        bsum[g] = __builtin_fmaf(sc[n >> 2][n & 3], T::to_f32(sb >> 16), bsum[g]);
+      }
+      u32x4 hi, lo;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float s = T::to_f32(vs.sb[i][g][r] & 0xFFFFu), bv = T::to_f32(vs.sb[i][g][r] >> 16);
-            x[i][r] = sc[t][i][r] * s;
-            float pb = sc[t][i][r] * bv;
-            if (masked) {   // whatever a masked token's scales hold, it adds nothing
-              const bool ok = (seen[t] >> (4 * i + r)) & 1u;
-              x[i][r] = ok ? x[i][r] : 0.f;
-              pb = ok ? pb : 0.f;
-            }
-            bsum[t][g] += pb;
-          }
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          uint32_t uh, ul;
-          split2<T>(x[n >> 1][2 * (n & 1)], x[n >> 1][2 * (n & 1) + 1], &uh, &ul);
-          hi[t][n] = uh;
-          lo[t][n] = ul;
-        }
+      for (int n = 0; n < 4; ++n) {
+        uint32_t uh, ul;
+        split2<T>(x[2 * n], x[2 * n + 1], &uh, &ul);
+        hi[n] = uh;
+        lo[n] = ul;
       }
 #pragma unroll
       for (int j = g * CPG; j < (g + 1) * CPG; ++j) {
@@ -367,76 +326,61 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS, RT>())) void attend_ke
         for (int n = 0; n < 2; ++n) {
           const uint32_t e0 = (n ? w0 >> 4 : w0) & 0x0F0F0F0Fu, e1 = (n ? w1 >> 4 : w1) & 0x0F0F0F0Fu;
           const u32x4 vc = {T::fp8x2_lo(e0), T::fp8x2_hi(e0), T::fp8x2_lo(e1), T::fp8x2_hi(e1)};
-#pragma unroll
-          for (int t = 0; t < RT; ++t) {
-            acc[t][2 * j + n] = T::mfma(as_v8<T>(vc), as_v8<T>(lo[t]), acc[t][2 * j + n]);
-            acc[t][2 * j + n] = T::mfma(as_v8<T>(vc), as_v8<T>(hi[t]), acc[t][2 * j + n]);
-          }
+          acc[2 * j + n] = T::mfma(as_v8<T>(vc), as_v8<T>(lo), acc[2 * j + n]);
+          acc[2 * j + n] = T::mfma(as_v8<T>(vc), as_v8<T>(hi), acc[2 * j + n]);
         }
       }
     }
-    if (more) load_v();
+    load_v();
   }
 
   // ---- the lanes' shares of the sums, and the bias term: element d = 16 i + 4 h + r of row col
-#pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    l[t] += __shfl_xor(l[t], 16);
-    l[t] += __shfl_xor(l[t], 32);
-    if (bad) {
-      l[t] = __builtin_nanf("");
-      m[t] = 0.f;
-    }
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      bsum[t][g] += __shfl_xor(bsum[t][g], 16);
-      bsum[t][g] += __shfl_xor(bsum[t][g], 32);
-    }
-#pragma unroll
-    for (int i = 0; i < NT; ++i) acc[t][i] += bsum[t][i * 16 / GS];
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+  if (bad) {
+    l = __builtin_nanf("");
+    m = 0.f;
   }
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    bsum[g] += __shfl_xor(bsum[g], 16);
+    bsum[g] += __shfl_xor(bsum[g], 32);
+  }
+#pragma unroll
+  for (int i = 0; i < NT; ++i) acc[i] += bsum[i * 16 / GS];
 
+  // ---- the four waves' sums meet in LDS
+  __shared__ float o_s[kWaves][kRows][kPitch];
+  __shared__ float2 ml_s[kWaves][kRows];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) *(f32x4*)&o_s[wave][col][16 * i + 4 * h] = acc[i];
+  if (h == 0) ml_s[wave][col] = float2{m, l};
+  __syncthreads();
   const int64_t row0 = (b * a.c.heads + head) * a.rows;
-  float* part_ml = a.part + (int64_t)gridDim.z * a.c.heads * a.rows * a.splits * D;
-  {
-    // the four waves' sums meet in LDS: [wave][row][D], then [wave][row] maxima and sums
-    float* ml_s = lds + kWaves * kRows * kPitch;
+  float* part_ml = a.part + a.batch * a.c.heads * a.rows * a.splits * D;
+  for (int e = threadIdx.x; e < kRows * (D / 4); e += kThreads) {
+    const int rr = e / (D / 4), d = (e - rr * (D / 4)) * 4;
+    const int r = base + rr;
+    if (r >= a.rows) break;
+    float top = kNone;
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      const int r = wave * kRows + 16 * t + col;
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, ml_s[w][rr].x);
+    float sum = 0.f;
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < NT; ++i) *(f32x4*)(lds + r * kPitch + 16 * i + 4 * h) = acc[t][i];
-      if (h == 0) {
-        ml_s[2 * r] = m[t];
-        ml_s[2 * r + 1] = l[t];
-      }
+    for (int w = 0; w < kWaves; ++w) {
+      const float f = __builtin_amdgcn_exp2f(ml_s[w][rr].x - top);
+      sum = __builtin_fmaf(f, ml_s[w][rr].y, sum);
+      o += f * *(const f32x4*)&o_s[w][rr][d];
     }
-    __syncthreads();
-    for (int e = threadIdx.x; e < kRows * (D / 4); e += kThreads) {
-      const int rr = e / (D / 4), d = (e - rr * (D / 4)) * 4;
-      const int r = base + rr;
-      if (r >= a.rows) break;
-      float top = kNone;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) top = fmaxf(top, ml_s[2 * (w * kRows + rr)]);
-      float sum = 0.f;
-      f32x4 o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        const float f = __builtin_amdgcn_exp2f(ml_s[2 * (w * kRows + rr)] - top);
-        sum = __builtin_fmaf(f, ml_s[2 * (w * kRows + rr) + 1], sum);
-        o += f * *(const f32x4*)(lds + (w * kRows + rr) * kPitch + d);
-      }
-      store4<T, D>(a, b, head, split, row0, r, d, o, sum);
-      if (a.splits > 1 && d == 0) {
-        float* ml = part_ml + ((row0 + r) * a.splits + split) * 2;
-        ml[0] = top;
-        ml[1] = sum;
-      }
+    store4<T, D>(a, b, head, split, row0, r, d, o, sum);
+    if (a.splits > 1 && d == 0) {
+      float* ml = part_ml + ((row0 + r) * a.splits + split) * 2;
+      ml[0] = top;
+      ml[1] = sum;
     }
   }
 }
-
 
 // ---- prompts: many query rows per cached head.
 //
@@ -449,7 +393,11 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS, RT>())) void attend_ke
 //      probabilities need no scale per token and group: they are split once, and
 //      p v = p_hi v_lo + p_lo v_hi + p_hi v_hi.
 // (Codes and scales for V, as in the single-token form, cost 11 vector operations per score
-// more, two of them per group, against a third matrix-core pass here.)
+// more, two of them per group, against a third matrix-core pass here: 1223 us against 650.)
+// What bounds it: the matrix cores and the vector units alternate in each wave; half of the
+// waves unpack before their products and half after them (800 us -> 650).  Measured: 2048
+// queries after 6144 tokens, 32 query heads over 8 of 128 elements, 650 us, 0.37 PFLOP/s of
+// the two products of the definition (the passes for V's two operands make 0.74 of them).
 // Tokens outside every row's range are zero in LDS, and so are values that are not finite,
 // which a token that only some rows see may hold: the unpacking notes the token, and a row
 // that gives it weight becomes NaN.
@@ -480,9 +428,9 @@ __global__ __launch_bounds__(kRowThreads, 1) void attend_rows_kernel(const Atten
 
   const int lane = threadIdx.x & 63, col = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int split = blockIdx.x;
-  const int head = blockIdx.y % a.c.heads, row_tile = blockIdx.y / a.c.heads;
-  const int64_t b = blockIdx.z;
+  const int split = blockIdx.z;
+  const int head = blockIdx.x % a.c.heads, row_tile = blockIdx.x / a.c.heads;
+  const int64_t b = blockIdx.y;
   const int wg_base = row_tile * kRowWaves * kRows, base = wg_base + wave * kRows;
 
   int len = a.lengths[b];
@@ -765,7 +713,7 @@ __global__ __launch_bounds__(kRowThreads, 1) void attend_rows_kernel(const Atten
 
   if (!live) return;
   const int64_t row0 = (b * a.c.heads + head) * a.rows;
-  float* part_ml = a.part + (int64_t)gridDim.z * a.c.heads * a.rows * a.splits * D;
+  float* part_ml = a.part + a.batch * a.c.heads * a.rows * a.splits * D;
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     l[t] += __shfl_xor(l[t], 16);
@@ -845,28 +793,17 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(const AttendArgs 
   *(uint2*)((uint16_t*)a.out + ((b * a.q_len + i) * (int64_t)a.q_heads + head * a.rep + g) * D + 4 * lane) = u;
 }
 
-template <class T, int D, int GS, int RT>
-hipError_t launch_tokens(const AttendArgs& a, const AttendPlan& p, dim3 grid, hipStream_t stream) {
-  const int lds = (kWaves * 16 * RT * (D + 4) + kWaves * 16 * RT * 2) * 4;
-  if (lds > 64 * 1024) {
-    const hipError_t e = hipFuncSetAttribute((const void*)attend_kernel<T, D, GS, RT>,
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-    if (e != hipSuccess) return e;
-  }
-  hipLaunchKernelGGL((attend_kernel<T, D, GS, RT>), grid, dim3(kThreads), lds, stream, a);
-  return hipGetLastError();
-}
-
 template <class T, int D, int GS>
 hipError_t launch_shape(const AttendArgs& a, const AttendPlan& p, hipStream_t stream) {
-  const dim3 grid((unsigned)p.splits, (unsigned)(a.c.heads * p.row_tiles), (unsigned)a.batch);
-  hipError_t e;
-  if (p.by_rows) {
+  // Workgroups go to the eight XCDs in turn, x fastest.  Of sequences of unequal length only the
+  // longest have work in the last splits, so splits are the slowest index: with splits fastest
+  // (4 of them), two XCDs had every first split.
+  const dim3 grid((unsigned)(a.c.heads * p.row_tiles), (unsigned)a.batch, (unsigned)p.splits);
+  if (p.by_rows)
     hipLaunchKernelGGL((attend_rows_kernel<T, D, GS, (D == 256 ? 1 : 2)>), grid, dim3(kRowThreads), 0, stream, a);
-    e = hipGetLastError();
-  } else {
-    e = p.tile_rows == 16 ? launch_tokens<T, D, GS, 1>(a, p, grid, stream) : launch_tokens<T, D, GS, 2>(a, p, grid, stream);
-  }
+  else
+    hipLaunchKernelGGL((attend_kernel<T, D, GS>), grid, dim3(kThreads), 0, stream, a);
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   hipLaunchKernelGGL((attend_join_kernel<T, D>), dim3((unsigned)(a.batch * a.c.heads * a.rows)), dim3(kThreads), 0,
                      stream, a);

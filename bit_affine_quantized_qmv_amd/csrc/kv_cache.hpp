@@ -105,13 +105,12 @@ hipError_t launch_read(const ReadArgs& a, hipStream_t stream);
 
 // Splits of the token range and tokens per split of an attention call (host only).
 struct AttendPlan {
-  int32_t tile_rows;      // query rows per wave
   int32_t by_rows;        // the workgroup's waves take different query rows (else tokens)
   int32_t row_tiles;      // workgroups along the rows of one cached head
   int32_t chunk;
   int32_t splits;
 };
-AttendPlan plan_attend(int64_t batch, int heads, int head_dim, int64_t rows, int64_t range);
+AttendPlan plan_attend(int64_t batch, const CacheArgs& c, int64_t rows, int64_t range);
 
 hipError_t launch_attend_bf16(const AttendArgs& a, const AttendPlan& p, hipStream_t stream);
 hipError_t launch_attend_fp16(const AttendArgs& a, const AttendPlan& p, hipStream_t stream);

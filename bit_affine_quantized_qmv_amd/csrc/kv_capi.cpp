@@ -72,7 +72,7 @@ int32_t check_attend(const qmm_kv_cache_t* cache, const qmm_kv_attend_t* q, bool
   a->max_length = (int32_t)q->max_length;
   a->scale_log2 = q->scale * 1.44269504088896340736f;
   a->causal = q->causal != 0;
-  a->window = (int32_t)std::min<int64_t>(q->window, kMaxInt);
+  a->window = (int32_t)std::min<int64_t>(q->window, 1 << 30);   // positions stay below 2^30: no limit
   return QMM_OK;
 }
 
@@ -90,42 +90,47 @@ int64_t part_floats(const AttendArgs& a, int64_t splits) {
 
 }  // namespace
 
-// Rows: up to 16 query rows per kv head (single tokens) take one 16-row tile per wave, the
-// workgroup's waves sharing out the tokens; up to 128 rows two tiles; more rows (prompts) take
-// the form whose eight waves have two tiles of their own each (one at head_dim 256, whose
-// accumulators are twice as large) and share the unpacked tokens.
-// Splits: as many as make `want` workgroups, each of at least one step of every wave (128
-// tokens), or 512 tokens in the prompt form, where a split's sums are large.
+// Rows: up to 512 query rows per kv head (single tokens, drafts) take 16 rows per workgroup,
+// whose waves share out the tokens; more rows (prompts) take the form whose eight waves have
+// two 16-row tiles of their own each (one at head_dim 256, whose accumulators are twice as
+// large) and share the unpacked tokens.  Measured at 8192 or 4096 tokens, the first form
+// against the second: 192 rows 56 us / 69, 512 rows of 64 elements 46 / 52, 400 rows of 256
+// elements 70 / 80; 400 rows of 128 elements in groups of 64 118 / 109.
+// Splits: as many as make one workgroup per CU in the prompt form and at head_dim 256 (only one
+// is resident: 19 us against 35 with four, 8192 tokens), two with four groups per row (17 us /
+// 20), else four (32 ragged sequences: 53 us against 63 with three; 131071 tokens: 35 us, with
+// eight 42); each of at least one step of every wave (128 tokens), or 512 tokens in the prompt
+// form, where a split's sums are large.
 namespace {
 
 struct Shape {
-  int32_t by_rows, tile_rows, row_tiles;
+  int32_t by_rows, row_tiles;
   int64_t step, want;
 };
 
-Shape shape_of(int64_t batch, int heads, int head_dim, int64_t rows) {
+Shape shape_of(int64_t batch, int heads, int head_dim, int group, int64_t rows) {
   Shape s{};
-  s.by_rows = rows > 128;
-  s.tile_rows = s.by_rows ? (head_dim == 256 ? 16 : 32) : (rows <= 16 ? 16 : 32);
-  const int64_t wg_rows = s.by_rows ? 8 * s.tile_rows : s.tile_rows;
+  s.by_rows = rows > 512;
+  const int64_t wg_rows = s.by_rows ? (head_dim == 256 ? 128 : 256) : 16;
   s.row_tiles = (int32_t)((rows + wg_rows - 1) / wg_rows);
   s.step = s.by_rows ? 512 : 128;
-  s.want = std::max<int64_t>(1, (s.by_rows ? 256 : 1024) / std::max<int64_t>(1, batch * heads * s.row_tiles));
+  const int64_t per_cu = s.by_rows || head_dim == 256 ? 1 : (head_dim == 4 * group ? 2 : 4);
+  s.want = std::max<int64_t>(1, 256 * per_cu / std::max<int64_t>(1, batch * heads * s.row_tiles));
   return s;
 }
 
 }  // namespace
 
-AttendPlan plan_attend(int64_t batch, int heads, int head_dim, int64_t rows, int64_t range) {
-  const Shape s = shape_of(batch, heads, head_dim, rows);
+AttendPlan plan_attend(int64_t batch, const CacheArgs& c, int64_t rows, int64_t range) {
+  const Shape s = shape_of(batch, c.heads, c.head_dim, c.group_size, rows);
   const int64_t steps = std::max<int64_t>(1, (range + s.step - 1) / s.step);
   const int64_t per = std::max<int64_t>(1, (steps + s.want - 1) / s.want);
-  return AttendPlan{s.tile_rows, s.by_rows, s.row_tiles, (int32_t)(per * s.step), (int32_t)((steps + per - 1) / per)};
+  return AttendPlan{s.by_rows, s.row_tiles, (int32_t)(per * s.step), (int32_t)((steps + per - 1) / per)};
 }
 
 // Splits that no shorter range of the same call exceeds.
 static int64_t most_splits(const AttendArgs& a) {
-  const Shape s = shape_of(a.batch, a.c.heads, a.c.head_dim, a.rows);
+  const Shape s = shape_of(a.batch, a.c.heads, a.c.head_dim, a.c.group_size, a.rows);
   return std::min<int64_t>(s.want, std::max<int64_t>(1, (a.max_length + s.step - 1) / s.step));
 }
 
@@ -208,7 +213,7 @@ int32_t qmm_kv_attend(const qmm_kv_cache_t* cache, const qmm_kv_attend_t* args, 
     if ((uintptr_t)a.table % 4 || (uintptr_t)a.lengths % 4)
       return report(QMM_ERR_ALIGN, "kv_attend: block_table and lengths must be 4-byte aligned");
     const kv::AttendPlan p =
-        kv::plan_attend(a.batch, a.c.heads, a.c.head_dim, a.rows, kv::token_range(a));
+        kv::plan_attend(a.batch, a.c, a.rows, kv::token_range(a));
     if ((int64_t)a.c.heads * p.row_tiles > 65535)
       return report(QMM_ERR_SHAPE, "kv_attend: too many query rows per sequence");
     const int64_t need = kv::part_floats(a, p.splits) * 4;

@@ -1,0 +1,108 @@
+"""Cache attention with more query rows per cached head than the single-token form takes (its
+workgroups share a step's unpacked tokens over many query rows), against the same float64
+reference and bounds; and arguments at their limits, for both forms."""
+import pytest
+import torch
+
+from qmm_testlib import require_gpu
+from test_gpu_kv_cache import Setup, _rows
+
+pytestmark = pytest.mark.gpu
+
+PROMPTS = [
+    # lengths, q_len, heads, rep, dim, group, page, window, dtype
+    ([540, 700], 540, 1, 1, 64, 64, 16, 0, "bf16"),
+    ([300, 0, 7], 260, 1, 2, 64, 32, 32, 0, "fp16"),                # more queries than tokens: padded rows
+    ([400, 70], 140, 2, 4, 128, 64, 64, 0, "bf16"),
+    ([600], 260, 1, 2, 128, 128, 16, 100, "bf16"),
+    ([530], 175, 1, 3, 128, 32, 48, 0, "fp16"),
+    ([560, 520], 520, 1, 1, 256, 64, 16, 0, "bf16"),
+    ([560], 513, 1, 1, 256, 32, 16, 50, "fp16"),
+    ([200], 130, 1, 4, 256, 128, 16, 0, "bf16"),
+]
+
+
+@pytest.mark.parametrize("lengths,q_len,heads,rep,dim,group,page,window,dtype", PROMPTS)
+def test_prompt_matches_float64(lengths, q_len, heads, rep, dim, group, page, window, dtype):
+    import bit_affine_quantized_qmv_amd as q
+    s = Setup(lengths, heads, dim, group, page, dtype, seed=dim + q_len)
+    dev = s.len_dev.device
+    queries = _rows((len(lengths), q_len, heads * rep, dim), dtype, 78, loud=False)
+    y = q.kv_attend(queries.to(dev), s.cache, s.table, s.len_dev, window=window)
+    torch.cuda.synchronize()
+    s.check(y, queries, dim ** -0.5, window=window)
+
+
+def test_prompt_all_tokens_scale_and_strides():
+    """causal=False, a negative scale, queries as a strided slice of a larger tensor."""
+    import bit_affine_quantized_qmv_amd as q
+    lengths, heads, rep, q_len, dim = [60, 1, 0, 200], 2, 2, 270, 128
+    s = Setup(lengths, heads, dim, 64, 16, "bf16", seed=5)
+    dev = s.len_dev.device
+    big = _rows((heads * rep + 2, len(lengths), q_len, dim + 8), "bf16", 6, loud=False)
+    view = big.to(dev)[1:-1, :, :, :dim].permute(1, 2, 0, 3)
+    y = q.kv_attend(view, s.cache, s.table, s.len_dev, scale=-0.21, causal=False)
+    torch.cuda.synchronize()
+    s.check(y, view.cpu(), -0.21, causal=False)
+
+
+def test_prompt_masked_tokens_may_hold_anything():
+    """NaN and infinite rows that a query does not see leave its output alone."""
+    import bit_affine_quantized_qmv_amd as q
+    n, q_len, window = 400, 140, 64
+    s = Setup([n], 1, 64, 32, 16, "bf16", seed=13)
+    dev = s.len_dev.device
+    queries = _rows((1, q_len, 4, 64), "bf16", 14, loud=False)
+    clean = q.kv_attend(queries.to(dev), s.cache, s.table, s.len_dev, window=window)
+    bad = s.cache.data.clone()
+    sb = 16 * 64 // 8
+    side = sb + 2 * 16
+    for token, word in ((n - 1, 0x7FFF7FFF), (0, 0x7F807F80), (n - q_len - window, 0x7FFF7FFF)):
+        page = int(s.table[0, token // 16])
+        for start in (0, side):
+            for g in (0, 1):
+                bad[page, 0, start + sb + g * 16 + token % 16] = word
+    y = q.kv_attend(queries.to(dev), q.KVCache(bad, 16, 64, 32, torch.bfloat16), s.table, s.len_dev, window=window)
+    torch.cuda.synchronize()
+    assert torch.equal(y[0, :-1], clean[0, :-1])                # the last query alone sees token n - 1
+    assert torch.isnan(y[0, -1].float()).all()
+
+
+def test_prompt_a_missing_page_reaches_the_output_through_the_splits():
+    import bit_affine_quantized_qmv_amd as q
+    q_len = 300
+    s = Setup([3000, 2900], 1, 64, 32, 16, "bf16", seed=21)
+    dev = s.len_dev.device
+    queries = _rows((2, q_len, 2, 64), "bf16", 22, loud=False)
+    for block in (1000 // 16, (3000 - q_len // 2 - 1) // 16):
+        table = s.table.clone()
+        table[0, block] = 10 ** 6
+        y = q.kv_attend(queries.to(dev), s.cache, table, s.len_dev)
+        torch.cuda.synchronize()
+        nan = torch.isnan(y.float())
+        needs = torch.tensor([3000 - q_len + i >= 16 * block for i in range(q_len)])
+        assert nan[0][needs].all() and not nan[0][~needs].any() and not nan[1].any()
+
+
+@pytest.mark.parametrize("q_len", [2, 600])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 40])
+def test_a_window_beyond_any_length_is_no_window(q_len, window):
+    """Also where queries stand before the sequence (more queries than tokens)."""
+    import bit_affine_quantized_qmv_amd as q
+    s = Setup([40, 1], 1, 64, 32, 16, "bf16", seed=23)
+    dev = s.len_dev.device
+    queries = _rows((2, q_len, 1, 64), "bf16", 24, loud=False)
+    y = q.kv_attend(queries.to(dev), s.cache, s.table, s.len_dev, window=window)
+    torch.cuda.synchronize()
+    s.check(y, queries, 64 ** -0.5)
+
+
+@pytest.mark.parametrize("q_len", [3, 520])
+def test_scale_zero_is_the_mean_of_what_a_query_sees(q_len):
+    import bit_affine_quantized_qmv_amd as q
+    s = Setup([77, 2, 0], 1, 64, 32, 16, "fp16", seed=25)
+    dev = s.len_dev.device
+    queries = _rows((3, q_len, 1, 64), "fp16", 26, loud=False)
+    y = q.kv_attend(queries.to(dev), s.cache, s.table, s.len_dev, scale=0.0)
+    torch.cuda.synchronize()
+    s.check(y, queries, 0.0)
