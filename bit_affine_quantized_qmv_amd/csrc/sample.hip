@@ -21,7 +21,15 @@
 // there are more candidates than LDS holds, (3) has left each chunk's weight above the bin and
 // its columns of each key in the bin, from which (4) finds the threshold and the chunk to draw
 // from.  What touches every column is spread over the chunks' workgroups: one workgroup takes
-// about 10 us for 10 instructions on each of 150000 columns.
+// about 10 us for 10 instructions on each of 150000 columns.  (Two kernels with one workgroup
+// per row for all that follows the maximum: 74 us for a row, 132 us for 32.)
+//
+// What bounds it: for one row the chain of four launches (2.3 us each at least) and, inside
+// them, of loads, scans and barriers; a row's columns are loaded before its settings, maximum
+// and threshold arrive.  For many rows (2) is bound by its vector instructions, about 70 per
+// column, most of them the exponential, the division by T (a product with 1/T and a correction
+// changed nothing measurable) and the conversion to an integer.  Measured, 151936 columns: one
+// row with top-k and top-p 25 us; 32 rows with mixed settings 48 us (6 + 14 + 12 + 13 us).
 #include "device_common.hpp"
 #include "sample.hpp"
 
@@ -36,17 +44,19 @@ constexpr int kRowThreads = 1024;
 constexpr int kRowWaves = kRowThreads / 64;
 constexpr int kLow = 32;             // keys per bin
 constexpr int kShift = 5;
+constexpr uint32_t kFew = 256;       // candidates that one wave draws from
 constexpr int kUnitBits = 24;        // u and top_p count in units of 2^-24
 constexpr int kRun = 8;              // consecutive columns per lane and step
 constexpr int kStep = 64 * kRun;     // columns per wave and step
+constexpr int kCols = kRun * kChunkThreads;   // columns per workgroup and step of the chunk kernels
 
 // Order key of a 16-bit logit: larger logits have larger keys, NaN and -inf (never drawn) 0.
 template <bool FP16>
 __device__ inline uint32_t key_of(uint32_t b) {
-  constexpr uint32_t kInf = FP16 ? 0x7C00u : 0x7F80u;
-  if ((b & 0x7FFFu) > kInf || b == (0x8000u | kInf)) return 0u;
-  if (b == 0x8000u) b = 0u;          // -0 draws like +0
-  return (b & 0x8000u) ? (~b & 0xFFFFu) : (b | 0x8000u);
+  constexpr uint32_t kInf = FP16 ? 0x7C00u : 0x7F80u, kLeast = 0xFFFFu - (0x8000u | kInf) + 1u;   // of the lowest finite
+  uint32_t k = b ^ (0x8000u | (uint32_t)-(int32_t)(b >> 15)) & 0xFFFFu;
+  k = k == 0x7FFFu ? 0x8000u : k;    // -0 draws like +0
+  return k - kLeast <= (0x8000u | kInf) - kLeast ? k : 0u;
 }
 
 template <class T>
@@ -109,19 +119,44 @@ __device__ inline void load_keys(const uint16_t* row, int64_t i, int64_t end, bo
   }
 }
 
+// The same columns as they are, four runs `step` apart: what a kernel loads before it knows the
+// row's settings.  Past the end NaN, whose key is 0.
+constexpr int kAhead = 4;
+struct Ahead {
+  u32x4 w[kAhead];
+  template <bool FP16>
+  __device__ uint32_t key(int j, int e) const {
+    return key_of<FP16>((w[j][e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+  }
+};
+__device__ inline void load_ahead(const uint16_t* row, int64_t i, int64_t end, int64_t step, bool vec, Ahead& r) {
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) {
+    const int64_t c = i + j * step;
+    r.w[j] = u32x4{~0u, ~0u, ~0u, ~0u};
+    if (c >= end) continue;
+    if (vec && c + kRun <= end) {
+      r.w[j] = *(const u32x4*)(row + c);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        r.w[j][e] = (c + 2 * e < end ? (uint32_t)row[c + 2 * e] : 0xFFFFu) |
+                    (c + 2 * e + 1 < end ? (uint32_t)row[c + 2 * e + 1] : 0xFFFFu) << 16;
+    }
+  }
+}
+
 // f(key) for the runs of columns at i, i + step, .. below end (key 0 past it); four runs are
 // loaded before the first is used.
 template <bool FP16, class F>
 __device__ inline void each_key(const uint16_t* row, int64_t i, int64_t end, int64_t step, bool vec, F&& f) {
-  constexpr int kAhead = 4;
   for (; i < end; i += kAhead * step) {
-    uint32_t k[kAhead][kRun];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) load_keys<FP16>(row, i + j * step, end, vec, k[j]);
+    Ahead a;
+    load_ahead(row, i, end, step, vec, a);
 #pragma unroll
     for (int j = 0; j < kAhead; ++j)
 #pragma unroll
-      for (int e = 0; e < kRun; ++e) f(k[j][e]);
+      for (int e = 0; e < kRun; ++e) f(a.template key<FP16>(j, e));
   }
 }
 
@@ -167,17 +202,22 @@ __global__ __launch_bounds__(kChunkThreads) void chunk_top_kernel(const SampleAr
   const uint16_t* x = (const uint16_t*)a.logits + row * a.row_stride;
   const bool vec = ((uintptr_t)x & 15u) == 0u;
   const int64_t begin = chunk * a.chunk, end = min(a.n, begin + a.chunk);
-  u64 top = 0;
-  for (int64_t i = begin + kRun * threadIdx.x; i < end; i += kRun * kChunkThreads) {
-    uint32_t k[kRun];
-    load_keys<FP16>(x, i, end, vec, k);
+  uint32_t key = 0u, column = 0u;    // the thread's largest, and its first column (columns ascend)
+  for (int64_t i = begin + kRun * threadIdx.x; i < end; i += kAhead * kCols) {
+    Ahead v;
+    load_ahead(x, i, end, kCols, vec, v);
 #pragma unroll
-    for (int e = 0; e < kRun; ++e) {
-      const u64 w = k[e] ? ((u64)k[e] << 32) | (0xFFFFFFFFu - (uint32_t)(i + e)) : 0ull;
-      top = w > top ? w : top;
+    for (int j = 0; j < kAhead; ++j) {
+      if (i + j * kCols >= end) break;
+#pragma unroll
+      for (int e = 0; e < kRun; ++e) {
+        const uint32_t k = v.template key<FP16>(j, e);
+        column = k > key ? (uint32_t)(i + j * kCols) + e : column;
+        key = k > key ? k : key;
+      }
     }
   }
-  top = wave_max64(top);
+  u64 top = wave_max64(key ? ((u64)key << 32) | (0xFFFFFFFFu - column) : 0ull);
   if ((threadIdx.x & 63) == 0) wave_top[threadIdx.x >> 6] = top;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -195,6 +235,11 @@ __global__ __launch_bounds__(kChunkThreads) void chunk_weights_kernel(const Samp
   const int64_t row = blockIdx.y;
   const int chunk = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   RowSpace& s = a.space[row];
+  const uint16_t* x = (const uint16_t*)a.logits + row * a.row_stride;
+  const bool vec = ((uintptr_t)x & 15u) == 0u;
+  const int64_t begin = chunk * a.chunk, end = min(a.n, begin + a.chunk);
+  Ahead v;                                    // (in flight while the settings and the maximum arrive)
+  load_ahead(x, begin + kRun * threadIdx.x, end, kCols, vec, v);
   const Row r = row_settings(a, row);
   const u64 top_word = row_top(s, a.chunks, lane);
   const uint32_t top_key = (uint32_t)(top_word >> 32);
@@ -208,24 +253,26 @@ __global__ __launch_bounds__(kChunkThreads) void chunk_weights_kernel(const Samp
     }
     __syncthreads();
   }
-  const uint16_t* x = (const uint16_t*)a.logits + row * a.row_stride;
-  const bool vec = ((uintptr_t)x & 15u) == 0u;
-  const int64_t begin = chunk * a.chunk, end = min(a.n, begin + a.chunk);
   u64 sum = 0;
-  for (int64_t i = begin + kRun * threadIdx.x; i < end; i += kRun * kChunkThreads) {
-    uint32_t k[kRun];
-    load_keys<FP16>(x, i, end, vec, k);
+  for (int64_t i = begin + kRun * threadIdx.x; i < end;) {
 #pragma unroll
-    for (int e = 0; e < kRun; ++e) {
-      if (k[e] == 0u) continue;
-      const float w = weight<T>(k[e], top_key, top, r.t);
-      if (threshold) {
-        atomicAdd(&mass[k[e] >> kShift], weight_int(w));
-        atomicAdd(&count[k[e] >> kShift], 1u);
-      } else if (w >= r.min_p) {
-        sum += weight_int(w);
+    for (int j = 0; j < kAhead; ++j) {
+      if (i + j * kCols >= end) break;
+#pragma unroll
+      for (int e = 0; e < kRun; ++e) {
+        const uint32_t k = v.template key<FP16>(j, e);
+        if (k == 0u) continue;
+        const float w = weight<T>(k, top_key, top, r.t);
+        if (threshold) {
+          atomicAdd(&mass[k >> kShift], weight_int(w));
+          atomicAdd(&count[k >> kShift], 1u);
+        } else if (w >= r.min_p) {
+          sum += weight_int(w);
+        }
       }
     }
+    i += kAhead * kCols;
+    if (i < end) load_ahead(x, i, end, kCols, vec, v);
   }
   if (threshold) {
     __syncthreads();
@@ -348,6 +395,11 @@ __global__ __launch_bounds__(kChunkThreads) void collect_kernel(const SampleArgs
   const int64_t row = blockIdx.y;
   const int chunk = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   RowSpace& s = a.space[row];
+  const uint16_t* x = (const uint16_t*)a.logits + row * a.row_stride;
+  const bool vec = ((uintptr_t)x & 15u) == 0u;
+  const int64_t begin = chunk * a.chunk, end = min(a.n, begin + a.chunk);
+  Ahead v;                                 // (in flight while the threshold's bin is found)
+  load_ahead(x, begin + kRun * threadIdx.x, end, kCols, vec, v);
   const Row r = row_settings(a, row);
   const u64 top_word = row_top(s, a.chunks, lane);
   const uint32_t top_key = (uint32_t)(top_word >> 32);
@@ -398,49 +450,50 @@ __global__ __launch_bounds__(kChunkThreads) void collect_kernel(const SampleArgs
     s.plan = p;
     if (!store) s.found = kCandidates + 1;
   }
-  const uint16_t* x = (const uint16_t*)a.logits + row * a.row_stride;
-  const bool vec = ((uintptr_t)x & 15u) == 0u;
-  const int64_t begin = chunk * a.chunk, end = min(a.n, begin + a.chunk);
   u64 mass = 0;
-  for (int64_t base = begin; base < end; base += kRun * kChunkThreads) {
+  for (int64_t base = begin; base < end; base += kAhead * kCols) {
     const int64_t i = base + kRun * threadIdx.x;
-    uint32_t k[kRun], n = 0;
-    float w[kRun];
-    load_keys<FP16>(x, i, end, vec, k);
+    uint32_t take = 0u;             // the thread's candidates, bit 8 j + e
 #pragma unroll
-    for (int e = 0; e < kRun; ++e) {
-      w[e] = k[e] >= edge ? weight<T>(k[e], top_key, top, r.t) : 0.0f;
-      n += k[e] >= edge ? 1u : 0u;
-      if ((int)(k[e] >> kShift) > low_bin) mass += weight_int(w[e]);
-      if (k[e] && (int)(k[e] >> kShift) == low_bin) atomicAdd(&low[k[e] & (kLow - 1)], 1u);
-    }
-    if (!store) continue;
-    uint32_t at = n;
-    for (int d = 1; d < 64; d <<= 1) {
-      const uint32_t o = __shfl_up(at, d);
-      if (lane >= d) at += o;
-    }
-    if (lane == 63) wave_n[wave] = at;
-    at -= n;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      uint32_t all = 0;
-      for (int v = 0; v < kChunkThreads / 64; ++v) all += wave_n[v];
-      first = all ? atomicAdd(&s.found, all) : 0u;   // n <= 2^22: no wrap
-    }
-    __syncthreads();
-    at += first;
-    for (int v = 0; v < wave; ++v) at += wave_n[v];
+    for (int j = 0; j < kAhead; ++j) {
+      if (base + j * kCols >= end) break;
 #pragma unroll
-    for (int e = 0; e < kRun; ++e)
-      if (k[e] >= edge) {
-        if (at < (uint32_t)kCandidates) {
-          s.candidate[at] = ((u64)k[e] << 32) | (uint32_t)(i + e);
-          s.weight[at] = w[e];
-        }
-        ++at;
+      for (int e = 0; e < kRun; ++e) {
+        const uint32_t k = v.template key<FP16>(j, e);
+        if ((int)(k >> kShift) > low_bin) mass += weight_int(weight<T>(k, top_key, top, r.t));
+        if (k && (int)(k >> kShift) == low_bin) atomicAdd(&low[k & (kLow - 1)], 1u);
+        take |= k >= edge ? 1u << (kRun * j + e) : 0u;
       }
-    __syncthreads();                       // wave_n and first are used again
+    }
+    if (store) {
+      const uint32_t n = __popc(take);
+      uint32_t at = n;
+      for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t o = __shfl_up(at, d);
+        if (lane >= d) at += o;
+      }
+      if (lane == 63) wave_n[wave] = at;
+      at -= n;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        uint32_t all = 0;
+        for (int g = 0; g < kChunkThreads / 64; ++g) all += wave_n[g];
+        first = all ? atomicAdd(&s.found, all) : 0u;   // n <= 2^22: no wrap
+      }
+      __syncthreads();
+      at += first;
+      for (int g = 0; g < wave; ++g) at += wave_n[g];
+      for (; take; take &= take - 1u, ++at) {          // few: their logits are read again
+        const int bit = __ffs(take) - 1;
+        const int64_t c = i + (bit / kRun) * kCols + bit % kRun;
+        if (at >= (uint32_t)kCandidates) break;
+        const uint32_t k = key_of<FP16>(x[c]);
+        s.candidate[at] = ((u64)k << 32) | (uint32_t)c;
+        s.weight[at] = weight<T>(k, top_key, top, r.t);
+      }
+      __syncthreads();                     // wave_n and first are used again
+    }
+    if (base + kAhead * kCols < end) load_ahead(x, i + kAhead * kCols, end, kCols, vec, v);
   }
   mass = wave_sum64(mass);
   if (lane == 0) wave_mass[wave] = mass;
@@ -518,7 +571,7 @@ __global__ __launch_bounds__(kRowThreads) void row_kernel(const SampleArgs a) {
   extern __shared__ u64 cand[];            // [kCandidates], then their weights
   float* const rel = (float*)(cand + kCandidates);
   const int64_t row = blockIdx.x;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const RowSpace& s = a.space[row];
   const Row r = row_settings(a, row);
   const RowPlan plan = s.plan;
@@ -547,9 +600,10 @@ __global__ __launch_bounds__(kRowThreads) void row_kernel(const SampleArgs a) {
       rel[i] = s.weight[i];
     }
   }
-  // f(key, column, relative weight) for this thread's candidates (each reads what it wrote)
+  // f(key, column, relative weight) for this thread's candidates (at first those that it wrote)
+  uint32_t stride = kRowThreads;           // threads that share them
   const auto each_candidate = [&](auto&& f) {
-    for (uint32_t i = threadIdx.x; i < found; i += kRowThreads) {
+    for (uint32_t i = threadIdx.x; i < found; i += stride) {
       const u64 c = cand[i];
       f((uint32_t)(c >> 32), (uint32_t)c, rel[i]);
     }
@@ -616,7 +670,13 @@ __global__ __launch_bounds__(kRowThreads) void row_kernel(const SampleArgs a) {
   const u64 tie_w = cut.c ? int_weight(cut.t) : 0ull;
 
   if (held) {
-    // ---- the draw among the candidates
+    // ---- the draw among the candidates: few of them by one wave, whose barriers wait for
+    // nobody (waves that have ended do not count)
+    if (found <= kFew) {
+      __syncthreads();
+      if (wave != 0) return;
+      stride = 64u;
+    }
     u64 mass = 0;
     uint32_t ties = 0;
     each_candidate([&](uint32_t key, uint32_t, float w) {
@@ -632,8 +692,7 @@ __global__ __launch_bounds__(kRowThreads) void row_kernel(const SampleArgs a) {
     __syncthreads();
     mass = 0;
     ties = 0;
-#pragma unroll
-    for (int w = 0; w < kRowWaves; ++w) {
+    for (uint32_t w = 0; w < stride / 64; ++w) {
       mass += sh.part_mass[w];
       ties += sh.part_ties[w];
     }
@@ -884,7 +943,6 @@ hipError_t launch(const SampleArgs& a, hipStream_t stream) {
 
 hipError_t launch_sample(SampleArgs a, hipStream_t stream) {
   // about 1024 chunks in all, each of whole 2048-column steps of its workgroup
-  constexpr int64_t kCols = kRun * kChunkThreads;
   const int64_t want = a.rows >= 1024 ? 1 : (1024 / a.rows < kMaxChunks ? 1024 / a.rows : kMaxChunks);
   const int64_t steps = (a.n + kCols - 1) / kCols;
   a.chunk = (steps + want - 1) / want * kCols;
