@@ -99,7 +99,7 @@ int64_t part_floats(const AttendArgs& a, int64_t splits) {
 // Splits: as many as make one workgroup per CU in the prompt form and at head_dim 256 (only one
 // is resident: 19 us against 35 with four, 8192 tokens), two with four groups per row (17 us /
 // 20), else four (32 ragged sequences: 53 us against 63 with three; 131071 tokens: 35 us, with
-// eight 42); each of at least one step of every wave (128 tokens), or 512 tokens in the prompt
+// six 39); each of at least one step of every wave (128 tokens), or 512 tokens in the prompt
 // form, where a split's sums are large.
 namespace {
 

@@ -27,12 +27,20 @@ __global__ __launch_bounds__(kSumThreads) void sum_kernel(const MoeArgs a) {
   const float* o = a.out + (int64_t)t * a.top_k * a.splits * a.hidden + n;
   const float* share = a.pair_share + t * a.top_k;
   float v = 0.f, sum = 0.f;
-  for (int i = 0; i < a.top_k; ++i) {
-    float w = 0.f;
-#pragma unroll 4
-    for (int z = 0; z < a.splits; ++z) w += o[(int64_t)(i * a.splits + z) * a.hidden];
-    v = __builtin_fmaf(share[i], w, v);
-    sum += share[i];
+  constexpr int kAhead = 8;          // choices whose loads are in flight together
+  for (int i0 = 0; i0 < a.top_k; i0 += kAhead) {
+    float w[kAhead] = {}, f[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) f[i] = i0 + i < a.top_k ? share[i0 + i] : 0.f;
+    for (int z = 0; z < a.splits; ++z)
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) w[i] += o[(int64_t)(min(i0 + i, a.top_k - 1) * a.splits + z) * a.hidden];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (i0 + i >= a.top_k) break;
+      v = __builtin_fmaf(f[i], w[i], v);
+      sum += f[i];
+    }
   }
   a.y[t * a.y_stride + n] = T::from_f32(a.renormalize ? v / sum : v);
 }

@@ -153,18 +153,27 @@ int32_t qmm_moe(const qmm_moe_t* m, void* y, void* workspace, int64_t workspace_
     a.out = (float*)ws;
 
     a.splits = (int32_t)moe::splits_of(inter);
-    // Waves per tile: each with at least four slots.  Workgroups per expert: three for every
-    // compute unit in all, each with several tiles.
+    // Waves per tile: each with at least four slots, so that a wave's ring of loads is in use (one
+    // token, 8 experts of 1024 x 2048: 24 us with one wave per tile, 20 with two or four); in the
+    // second kernel one where that fills the machine, since its activations pass through LDS in
+    // many chunks, each with a barrier (7 tokens, 4096 x 14336: 179 us against 199 with four).
+    // Workgroups: three for every compute unit in all, which is what is resident, each with
+    // several tiles (that layer: 512 workgroups 220 us, 768 199, 1024 206; 32 tokens over 128
+    // experts of 704 x 1408: 108, 104, 128).
+    constexpr int64_t kResident = 768;
     const int64_t used = std::min<int64_t>(experts, m->tokens * m->top_k);   // experts in use at most
+    const int64_t tiles = (inter + 15) / 16, down_tiles = (hidden + 31) / 32;
     const auto parts = [](int64_t slots) { return slots >= 16 ? 4 : (slots >= 8 ? 2 : 1); };
-    const auto blocks = [&](int64_t tiles, int64_t part, int64_t per_tile) {
-      const int64_t units = (tiles * part + moe::kWaves - 1) / moe::kWaves;
-      return (int32_t)std::min(units, std::max<int64_t>(1, 768 / (used * per_tile)));
+    const auto blocks = [&](int64_t n, int64_t part, int64_t per_tile) {
+      const int64_t units = (n * part + moe::kWaves - 1) / moe::kWaves;
+      return (int32_t)std::min(units, std::max<int64_t>(1, kResident / (used * per_tile)));
     };
     a.parts = parts(moe::slots_of(hidden, a.gate.bits, a.gate.group_size));
-    a.down_parts = parts(moe::slots_of(inter, a.down.bits, a.down.group_size) / a.splits);
-    a.blocks = blocks((inter + 15) / 16, a.parts, 1);
-    a.down_blocks = blocks((hidden + 31) / 32, a.down_parts, a.splits);
+    a.down_parts = down_tiles * used * a.splits >= kResident * moe::kWaves
+                       ? 1
+                       : parts(moe::slots_of(inter, a.down.bits, a.down.group_size) / a.splits);
+    a.blocks = blocks(tiles, a.parts, 1);
+    a.down_blocks = blocks(down_tiles, a.down_parts, a.splits);
     hipStream_t s = (hipStream_t)stream;
     hipError_t e = moe::launch(a, a.gate.bits, false, s);
     if (e == hipSuccess) e = moe::launch(a, a.down.bits, true, s);

@@ -25,6 +25,13 @@
 // h = silu(g) u reaches the second product as two operands of the element type, its leading
 // bits and the rest: the one rounding that a single operand would add is as large as the
 // output's own.
+//
+// What bounds it: the stream, at 3.6 TB/s of the 5.2 of a copy -- each workgroup's first
+// loads wait for its users and its activations, and the last ones leave CUs idle.  Measured:
+// 32 tokens, 128 experts of [704, 1408] in 8 bits, top 8: 104 us, 374 MB (67 + 36 + 5); 7 tokens,
+// 8 experts of [14336, 4096] in 4 bits, top 2: 179 us, 649 MB (106 + 71 + 5); one token, 8 of 64 experts of
+// [1024, 2048] in 4 bits: 20 us for 28 MB, of which three launches take 7 and the chain of
+// logits, expert, weights and sums most of the rest.
 #pragma once
 
 #include "decode_impl.hpp"
@@ -42,7 +49,7 @@ using decode::slot_reorder;
 
 constexpr int kThreads = 64 * kWaves;
 constexpr int kWorkgroups = 3;       // per compute unit: 168 registers per thread
-constexpr int kXBytes = 40 * 1024;   // LDS of the staged activations
+constexpr int kXBytes = 40 * 1024;   // LDS of the staged activations: three workgroups fit (with 48 KB, two)
 
 // Order key of a 16-bit float: larger values have larger keys, NaN the largest.
 template <class T>
@@ -155,6 +162,16 @@ __device__ inline void read_users(const MoeArgs& a, int e, Users& u) {
   for (int i = threadIdx.x; i < a.tokens * a.top_k; i += kThreads)
     if (a.pair_expert[i] == e) u.pair_of[i / a.top_k] = (int16_t)i;
   list_users(a, u);
+}
+
+// The only token's pair, which nobody else has (by_pair with one token): nothing to look up.
+__device__ inline void only_user(int pair, Users& u) {
+  if (threadIdx.x == 0) {
+    u.token[0] = 0;
+    u.pair[0] = (int16_t)pair;
+    u.count = 1;
+  }
+  __syncthreads();
 }
 
 // [x0 .. x7] -> [x0, x2, x4, x6, x1, x3, x5, x7], the order in which 4-bit codes are expanded.
@@ -449,7 +466,11 @@ __global__ __launch_bounds__(kThreads, kWorkgroups) void gate_up_kernel(const Mo
     pair_token = blockIdx.y / a.top_k;
     e = expert_of_rank<T>(a.router + pair_token * a.router_stride, a.experts, blockIdx.y - pair_token * a.top_k, lane);
   }
-  find_users<T>(a, e, u);
+  const bool only = by_pair && a.tokens == 1;
+  if (only)
+    only_user(blockIdx.y, u);
+  else
+    find_users<T>(a, e, u);
   // the same in the whole workgroup: nobody uses the expert, or an earlier pair's workgroup does it
   if (u.count == 0 || (by_pair && u.token[0] != pair_token)) return;
   St st;
@@ -460,10 +481,13 @@ __global__ __launch_bounds__(kThreads, kWorkgroups) void gate_up_kernel(const Mo
     t.tile(0, first_row(unit));
     t.tile(1, first_row(unit));
   };
-  if (blockIdx.x == 0 && (int)threadIdx.x < u.count) {
-    a.pair_expert[u.pair[threadIdx.x]] = e;
-    a.pair_share[u.pair[threadIdx.x]] = u.share[threadIdx.x];
-  }
+  const auto publish = [&]() {
+    if (blockIdx.x == 0 && (int)threadIdx.x < u.count) {
+      a.pair_expert[u.pair[threadIdx.x]] = e;
+      a.pair_share[u.pair[threadIdx.x]] = u.share[threadIdx.x];
+    }
+  };
+  if (!only) publish();
   for (int r0 = 0; r0 < u.count; r0 += 16) {   // a second pass only for more than 16 tokens
     const int rows = min(16, u.count - r0);
     int xrl;
@@ -489,6 +513,10 @@ __global__ __launch_bounds__(kThreads, kWorkgroups) void gate_up_kernel(const Mo
     Products<1, St, decltype(row), decltype(set_tiles), decltype(finish)> p{st, w};
     p.run(rows, row, 0, set_tiles, finish, xrl, xs, hand);
   }
+  if (only && blockIdx.x == 0) {               // the share is not needed before the last kernel
+    find_users<T>(a, e, u);
+    publish();
+  }
 }
 
 // out[pair][z] = h Wd_e^T over the z-th stretch of inter, of expert e's pairs, in float32.
@@ -502,7 +530,10 @@ __global__ __launch_bounds__(kThreads, kWorkgroups) void down_kernel(const MoeAr
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = wave / a.down_parts, per = kWaves / a.down_parts;
   const int e = by_pair ? __builtin_amdgcn_readfirstlane(a.pair_expert[blockIdx.y]) : (int)blockIdx.y;
-  read_users(a, e, u);
+  if (by_pair && a.tokens == 1)
+    only_user(blockIdx.y, u);
+  else
+    read_users(a, e, u);
   if (u.count == 0 || (by_pair && u.pair[0] != (int)blockIdx.y)) return;
   St st;
   st.setup(0, a.down, e, a.hidden, a.inter);
