@@ -8,7 +8,7 @@ import torch
 
 from . import _lib
 from .api import _DTYPE_CODE, ExpertWeights
-from .kv import raw_stream
+from .kv import raw_stream, same_device
 
 
 def _stack(w: ExpertWeights) -> _lib.ExpertStack:
@@ -62,6 +62,8 @@ def moe(x: torch.Tensor, router_logits: torch.Tensor, gate: ExpertWeights, up: E
     if workspace is None:
         workspace = moe_workspace(x, gate, top_k)
     assert workspace.is_contiguous()
+    same_device("moe", x, router_logits, out, workspace, gate.w_packed, gate.scales, gate.biases, up.w_packed, up.scales,
+                up.biases, down.w_packed, down.scales, down.biases)
     g, u, d = _stack(gate), _stack(up), _stack(down)
     pointer = ctypes.pointer
     if tokens <= 1:                      # one row's strides may be anything

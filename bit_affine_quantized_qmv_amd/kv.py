@@ -19,6 +19,15 @@ def raw_stream(t: torch.Tensor) -> int:
     return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
+def same_device(who: str, first: torch.Tensor, *others) -> None:
+    """The tensors of one call are on one GPU (None: not given)."""
+    device = first.get_device()
+    for t in (first,) + others:
+        if t is not None and (device < 0 or t.get_device() != device):
+            raise ValueError("%s: a tensor is on %s, another on %s; all must be on one GPU"
+                             % (who, first.device, t.device))
+
+
 @dataclass(frozen=True)
 class KVCache:
     """`pages` pages of `page_size` token slots with one K and one V row of `head_dim` values
@@ -68,6 +77,7 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Ten
     into slot slots[t] of every head; slots outside the cache are skipped."""
     lib = _lib.load()
     tokens = _check_slots(slots)
+    same_device("kv_append", slots, k, v, cache.data)
     want = (tokens, cache.heads, cache.head_dim)
     if k.shape != want or v.shape != want:
         raise ValueError("kv_append: k %s and v %s must be [tokens, heads, head_dim] = %s"
@@ -95,6 +105,7 @@ def kv_read(cache: KVCache, slots: torch.Tensor, out_k=None, out_v=None):
         else:
             assert t.dtype == cache.dtype and t.is_contiguous() and t.shape == shape
         out.append(t)
+    same_device("kv_read", slots, out[0], out[1], cache.data)
     _lib.check(lib.qmm_kv_read(_byref(cache._desc), slots.data_ptr(), count, out[0].data_ptr(), out[1].data_ptr(),
                                raw_stream(slots)))
     return out[0], out[1]
@@ -155,6 +166,7 @@ def kv_attend(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, length
     if workspace is None:
         n = _workspace_bytes(lib, cache, d)
         workspace = q.new_empty(n // 4, dtype=torch.float32) if n else None
+    same_device("kv_attend", q, cache.data, block_table, lengths, out, workspace)
     ws, size = (workspace.data_ptr(), workspace.nbytes) if workspace is not None else (None, 0)
     _lib.check(lib.qmm_kv_attend(_byref(cache._desc), _byref(d), out.data_ptr(), ws, size, raw_stream(q)))
     return out

@@ -7,7 +7,7 @@ import torch
 
 from . import _lib
 from .api import _dtype_code
-from .kv import raw_stream
+from .kv import raw_stream, same_device
 
 _WORKSPACE_BYTES = 190520    # per row
 
@@ -51,6 +51,7 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
     if workspace is None:
         workspace = sample_workspace(rows, logits.device)
     assert workspace.is_contiguous() and workspace.nbytes >= _WORKSPACE_BYTES * rows
+    same_device("sample", u, logits, out_index, out_prob, workspace)
     _lib.check(lib.qmm_sample(logits.data_ptr(), _dtype_code(logits.dtype), rows, n, stride if rows > 1 else n,
                               ctypes.byref(p), u.data_ptr(), out_index.data_ptr(), out_prob.data_ptr(),
                               workspace.data_ptr(), raw_stream(u)))

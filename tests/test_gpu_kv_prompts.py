@@ -106,3 +106,16 @@ def test_scale_zero_is_the_mean_of_what_a_query_sees(q_len):
     y = q.kv_attend(queries.to(dev), s.cache, s.table, s.len_dev, scale=0.0)
     torch.cuda.synchronize()
     s.check(y, queries, 0.0)
+
+
+def test_tensors_of_one_call_are_on_one_gpu():
+    import bit_affine_quantized_qmv_amd as q
+    s = Setup([20], 1, 64, 32, 16, "bf16", seed=27)
+    queries = _rows((1, 1, 2, 64), "bf16", 28)
+    rows = _rows((20, 1, 64), "bf16", 29)
+    with pytest.raises(ValueError, match="one GPU"):
+        q.kv_append(s.cache, rows, rows, s.slots)
+    with pytest.raises(ValueError, match="one GPU"):
+        q.kv_attend(queries, s.cache, s.table, s.len_dev)
+    with pytest.raises(ValueError, match="one GPU"):
+        q.sample(torch.zeros(2, 8, dtype=torch.bfloat16), torch.zeros(2, device=s.len_dev.device))
