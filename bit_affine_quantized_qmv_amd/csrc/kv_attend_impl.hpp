@@ -99,7 +99,7 @@ __device__ inline void store4(const AttendArgs& a, int64_t b, int head, int spli
   }
 }
 
-// ---- up to 512 query rows per cached head: single tokens, drafted tokens.
+// ---- few query rows per cached head: single tokens, drafted tokens, short chunks.
 //
 // A workgroup takes 16 query rows of one cached head and one split of the tokens; its four waves
 // take the split's 32-token steps in turn, each with its own softmax, and meet in LDS once at
@@ -384,8 +384,8 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS>())) void attend_kernel
 
 // ---- prompts: many query rows per cached head.
 //
-// Here the work per score decides, not the memory: the workgroup's eight waves take 16 * RT
-// query rows each and share what a step's 32 tokens cost to unpack, in LDS, in operand order
+// Here the work per score decides, not the memory: the workgroup's waves take 16 query rows
+// each and share what a step's 32 tokens cost to unpack, in LDS, in operand order
 // (double-buffered, one barrier per step; the next step's words are in registers meanwhile):
 //   K  its codes as exact integers, and its scales and biases as float32: a score costs one
 //      matrix-core pass and two multiply-adds per group;
@@ -393,17 +393,19 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS>())) void attend_kernel
 //      probabilities need no scale per token and group: they are split once, and
 //      p v = p_hi v_lo + p_lo v_hi + p_hi v_hi.
 // (Codes and scales for V, as in the single-token form, cost 11 vector operations per score
-// more, two of them per group, against a third matrix-core pass here: 1223 us against 650.)
-// What bounds it: the matrix cores and the vector units alternate in each wave; half of the
-// waves unpack before their products and half after them (800 us -> 650).  Measured: 2048
-// queries after 6144 tokens, 32 query heads over 8 of 128 elements, 650 us, 0.37 PFLOP/s of
-// the two products of the definition (the passes for V's two operands make 0.74 of them).
+// more, two of them per group, against a third matrix-core pass here: 1223 us against 800 in
+// the case below.)
+// What bounds it: LDS.  A wave reads 32 16-byte operands a lane for 32 products, and the
+// sixteen waves' reads take 4100 of a step's 5400 cycles, the matrix cores 2050 and the vector
+// units about 3000, with four waves per SIMD to overlap them.  Two 16-row tiles per wave halve
+// the reads, but then two waves per SIMD wait for each other (650 us; 680 with the products of
+// half of the waves a step late); two workgroups of eight waves unpack everything twice (656).
+// Measured: 2048 queries after 6144 tokens, 32 query heads over 8 of 128 elements, 550 us, 0.44
+// PFLOP/s of the two products of the definition (0.87 with the passes for V's two operands).
 // Tokens outside every row's range are zero in LDS, and so are values that are not finite,
 // which a token that only some rows see may hold: the unpacking notes the token, and a row
 // that gives it weight becomes NaN.
 // Scores leave the multiply-adds relative to the running maximum: -m is where they start.
-constexpr int kRowWaves = 8;
-constexpr int kRowThreads = 64 * kRowWaves;
 
 // split2 with hi rounded to nearest: for values below half the type's largest.
 template <class T>
@@ -412,12 +414,17 @@ __device__ inline void split2_near(float x, float y, uint32_t* hi, uint32_t* lo)
   *lo = T::pack2(x - T::to_f32(*hi & 0xFFFFu), y - T::to_f32(*hi >> 16));
 }
 
-template <class T, int D, int GS, int RT>
-__global__ __launch_bounds__(kRowThreads, 1) void attend_rows_kernel(const AttendArgs a) {
+// Waves per workgroup: 16 where 128 registers hold a wave, of which the first eight unpack.
+constexpr int row_waves(int head_dim) { return head_dim == 256 ? 8 : 16; }
+constexpr int kUnpackers = 8;
+
+template <class T, int D, int GS>
+__global__ __launch_bounds__(64 * row_waves(D), 1) void attend_rows_kernel(const AttendArgs a) {
+  constexpr int W = row_waves(D);
   constexpr int KC = D / 32, NT = D / 16, NG = D / GS, CPG = GS / 32;
-  constexpr int kRows = 16 * RT;
-  constexpr int kKUnits = (2 * KC + kRowWaves - 1) / kRowWaves, kVUnits = (NT + kRowWaves - 1) / kRowWaves;
-  static_assert(NG * kStep <= kRowThreads, "one thread per scale word of a step");
+  constexpr int kRows = 16;
+  constexpr int kKUnits = (2 * KC + kUnpackers - 1) / kUnpackers, kVUnits = (NT + kUnpackers - 1) / kUnpackers;
+  static_assert(NG * kStep <= 64 * kUnpackers, "one thread per scale word of a step");
   struct Buffer {
     u32x4 k[2 * KC][64];          // [tile, 32-element step][lane]
     u32x4 v[2][NT][64];           // [leading bits, rest][16-element tile][lane]
@@ -431,7 +438,7 @@ __global__ __launch_bounds__(kRowThreads, 1) void attend_rows_kernel(const Atten
   const int split = blockIdx.z;
   const int head = blockIdx.x % a.c.heads, row_tile = blockIdx.x / a.c.heads;
   const int64_t b = blockIdx.y;
-  const int wg_base = row_tile * kRowWaves * kRows, base = wg_base + wave * kRows;
+  const int wg_base = row_tile * W * kRows, base = wg_base + wave * kRows;
 
   int len = a.lengths[b];
   const bool bad = len < 0 || len > a.max_length;
@@ -440,7 +447,7 @@ __global__ __launch_bounds__(kRowThreads, 1) void attend_rows_kernel(const Atten
   const auto row_end = [&](int r) { return a.causal ? max(0, off + r / a.rep + 1) : len; };
   const auto row_begin = [&](int r) { return a.window ? max(0, off + r / a.rep - a.window + 1) : 0; };
   // ranges of the workgroup, and of this wave (empty for a wave without rows)
-  const int wg_last = min(a.rows, wg_base + kRowWaves * kRows) - 1;
+  const int wg_last = min(a.rows, wg_base + W * kRows) - 1;
   const int wg_lo = row_begin(wg_base), wg_hi = row_end(wg_last);
   const bool live = base < a.rows;
   const int last = min(a.rows, base + kRows) - 1;
@@ -482,7 +489,7 @@ __global__ __launch_bounds__(kRowThreads, 1) void attend_rows_kernel(const Atten
     }
 #pragma unroll
     for (int n = 0; n < kKUnits; ++n) {
-      const int u = wave + n * kRowWaves, i = u / KC, c = u - i * KC;
+      const int u = wave + n * kUnpackers, i = u / KC, c = u - i * KC;
       if (u < 2 * KC) kw[n] = tile_at[i][(tile_token[i] + col) * (D / 8) + h * KC + c];
     }
     if (sb_group < NG) {
@@ -492,7 +499,7 @@ __global__ __launch_bounds__(kRowThreads, 1) void attend_rows_kernel(const Atten
     }
 #pragma unroll
     for (int n = 0; n < kVUnits; ++n) {
-      const int u = wave + n * kRowWaves;
+      const int u = wave + n * kUnpackers;
       if (u < NT) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -508,7 +515,7 @@ __global__ __launch_bounds__(kRowThreads, 1) void attend_rows_kernel(const Atten
   const auto unpack = [&](Buffer& buf, int t0) {
 #pragma unroll
     for (int n = 0; n < kKUnits; ++n) {
-      const int u = wave + n * kRowWaves;
+      const int u = wave + n * kUnpackers;
       if (u < 2 * KC) buf.k[u][lane] = codes4_to_v8<T>(kw[n]);
     }
     if (sb_group < NG) {
@@ -520,7 +527,7 @@ __global__ __launch_bounds__(kRowThreads, 1) void attend_rows_kernel(const Atten
     const bool edge = t0 < wg_lo || t0 + kStep > wg_hi || loaded_bad[0] || loaded_bad[1];
 #pragma unroll
     for (int n = 0; n < kVUnits; ++n) {
-      const int u = wave + n * kRowWaves;
+      const int u = wave + n * kUnpackers;
       if (u >= NT) continue;
       u32x4 hi, lo;
 #pragma unroll
@@ -558,44 +565,36 @@ __global__ __launch_bounds__(kRowThreads, 1) void attend_rows_kernel(const Atten
     }
   };
   if (threadIdx.x < 4) odd_tokens[threadIdx.x] = 0u;
-  if (c0 < c1) {
+  if (wave < kUnpackers && c0 < c1) {
     find(c0);
     load();
     if (c0 + kStep < c1) find(c0 + kStep);
   }
 
-  typename T::v8 q[RT][KC];
-  float qsum[RT][NG], m[RT], l[RT];
-  float over[RT];                    // scores above m + over raise m: any score at first, then slack
-  int row_lo[RT], row_hi[RT];
-  f32x4 acc[RT][NT];
+  typename T::v8 q[KC];
+  float qsum[NG], m = 0.f, l = 0.f;
+  float over = -__builtin_inff();    // scores above m + over raise m: any score at first, then slack
+  f32x4 acc[NT];
   const uint32_t one2 = T::pack2(1.0f, 1.0f);
   const u32x4 ones = {one2, one2, one2, one2};
+  const int r = min(base + col, a.rows - 1), query = r / a.rep;
+  const uint16_t* qp = (const uint16_t*)a.q + b * a.q_batch_stride + (int64_t)query * a.q_token_stride +
+                       (int64_t)(head * a.rep + r - query * a.rep) * a.q_head_stride + 8 * h;
 #pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    const int r = min(base + 16 * t + col, a.rows - 1);
-    const int i = r / a.rep, g = r - i * a.rep;
-    const uint16_t* qp = (const uint16_t*)a.q + b * a.q_batch_stride + (int64_t)i * a.q_token_stride +
-                         (int64_t)(head * a.rep + g) * a.q_head_stride + 8 * h;
+  for (int c = 0; c < KC; ++c) q[c] = as_v8<T>(interleave_even_odd(*(const u32x4*)(qp + 32 * c)));
 #pragma unroll
-    for (int c = 0; c < KC; ++c) q[t][c] = as_v8<T>(interleave_even_odd(*(const u32x4*)(qp + 32 * c)));
+  for (int g = 0; g < NG; ++g) {
+    f32x4 d = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int gi = 0; gi < NG; ++gi) {
-      f32x4 d = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < CPG; ++c) d = T::mfma(as_v8<T>(ones), q[t][gi * CPG + c], d);
-      qsum[t][gi] = d[0];
-    }
-    row_hi[t] = a.causal ? off + i + 1 : len;
-    row_lo[t] = a.window ? off + i - a.window + 1 : 0;
-    m[t] = 0.f;
-    over[t] = -__builtin_inff();
-    l[t] = 0.f;
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < CPG; ++c) d = T::mfma(as_v8<T>(ones), q[g * CPG + c], d);
+    qsum[g] = d[0];
   }
+  const int row_hi = a.causal ? off + query + 1 : len;
+  const int row_lo = a.window ? off + query - a.window + 1 : 0;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
   __syncthreads();                   // the flags are clear
-  if (c0 < c1) {
+  if (wave < kUnpackers && c0 < c1) {
     unpack(bufs[0], c0);
     if (c0 + kStep < c1) {
       load();
@@ -604,133 +603,112 @@ __global__ __launch_bounds__(kRowThreads, 1) void attend_rows_kernel(const Atten
   }
   lds_barrier();
 
-  // The next step's unpacking: half of the waves do it before the step's products and half
-  // after them, so that the two waves of a SIMD do not need the matrix core at the same time.
-  const auto prepare = [&](int t0, int to) {
+  const auto prepare = [&](int t0, Buffer& to) {
     if (t0 + kStep >= c1) return;
-    unpack(bufs[to], t0 + kStep);
+    unpack(to, t0 + kStep);
     if (t0 + 2 * kStep < c1) {
       load();
       if (t0 + 3 * kStep < c1) find(t0 + 3 * kStep);
     }
   };
-  int at = 0;
-  for (int t0 = c0; t0 < c1; t0 += kStep, at ^= 1) {
-    const Buffer& buf = bufs[at];
-    const int step = t0 / kStep;
-    if (threadIdx.x == 0) odd_tokens[(step + 2) & 3] = 0u;   // last read two steps ago, next set in the next one
-    if (wave < kRowWaves / 2) prepare(t0, at ^ 1);
-    if (t0 < hi_max && t0 + kStep > lo_min) {
-      // ---- scores
-      float sc[RT][2][4];
+  // ---- scores and probabilities of a step, as operands
+  u32x4 ph, pl;
+  const auto weigh = [&](const Buffer& buf, int t0) {
+    float sc[2][4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          const f32x4 s = *(const f32x4*)&buf.s[g][16 * i + 4 * h], bb = *(const f32x4*)&buf.b[g][16 * i + 4 * h];
-          f32x4 d[RT];
+      for (int g = 0; g < NG; ++g) {
+        const f32x4 s = *(const f32x4*)&buf.s[g][16 * i + 4 * h], bb = *(const f32x4*)&buf.b[g][16 * i + 4 * h];
+        f32x4 d = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int t = 0; t < RT; ++t) d[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int c = g * CPG; c < (g + 1) * CPG; ++c) d = T::mfma(as_v8<T>(buf.k[i * KC + c][lane]), q[c], d);
 #pragma unroll
-          for (int c = 0; c < CPG; ++c) {
-            const typename T::v8 kc = as_v8<T>(buf.k[i * KC + g * CPG + c][lane]);
-#pragma unroll
-            for (int t = 0; t < RT; ++t) d[t] = T::mfma(kc, q[t][g * CPG + c], d[t]);
-          }
-#pragma unroll
-          for (int t = 0; t < RT; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float x = __builtin_fmaf(bb[r], qsum[t][g], g == 0 ? -m[t] : sc[t][i][r]);
-              sc[t][i][r] = __builtin_fmaf(s[r], d[t][r], x);
-            }
-        }
-      if (t0 < lo_max || t0 + kStep > hi_min) {   // rows that do not see every token of the step
-#pragma unroll
-        for (int t = 0; t < RT; ++t)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int token = t0 + 16 * i + 4 * h + r;
-              sc[t][i][r] = token >= row_lo[t] && token < row_hi[t] ? sc[t][i][r] : -__builtin_inff();
-            }
+        for (int n = 0; n < 4; ++n)
+          sc[i][n] = __builtin_fmaf(s[n], d[n], __builtin_fmaf(bb[n], qsum[g], g == 0 ? -m : sc[i][n]));
       }
-      // ---- probabilities
-      u32x4 ph[RT], pl[RT];
-      const uint32_t odd = __builtin_amdgcn_readfirstlane(odd_tokens[step & 3]);
+    if (t0 < lo_max || t0 + kStep > hi_min) {     // rows that do not see every token of the step
 #pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        float top = fmaxf(fmaxf(sc[t][0][0], sc[t][0][1]), fmaxf(sc[t][0][2], sc[t][0][3]));
-        top = fmaxf(top, fmaxf(fmaxf(sc[t][1][0], sc[t][1][1]), fmaxf(sc[t][1][2], sc[t][1][3])));
-        if (__builtin_amdgcn_ballot_w64(top > over[t]) != 0ull) {
-          top = fmaxf(top, __shfl_xor(top, 16));
-          top = fmaxf(top, __shfl_xor(top, 32));
-          const bool some = top > -__builtin_inff();             // false: nothing seen yet, m stays
-          const float up = over[t] < 0.f ? (some ? top : 0.f) : fmaxf(top, 0.f);
-          over[t] = over[t] < 0.f && !some ? over[t] : slack<T>();
-          const float f = __builtin_amdgcn_exp2f(-up);
-          m[t] += up;
-          l[t] *= f;
-#pragma unroll
-          for (int i = 0; i < NT; ++i) acc[t][i] *= f;
-#pragma unroll
-          for (int n = 0; n < 8; ++n) sc[t][n >> 2][n & 3] -= up;
-        }
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          sc[t][n >> 2][n & 3] = __builtin_amdgcn_exp2f(sc[t][n >> 2][n & 3]);
-          l[t] += sc[t][n >> 2][n & 3];
-        }
-        if (odd) {
-#pragma unroll
-          for (int n = 0; n < 8; ++n)
-            if (((odd >> (16 * (n >> 2) + 4 * h + (n & 3))) & 1u) && sc[t][n >> 2][n & 3] != 0.f) l[t] = __builtin_nanf("");
-        }
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          uint32_t uh, ul;
-          split2_near<T>(sc[t][n >> 1][2 * (n & 1)], sc[t][n >> 1][2 * (n & 1) + 1], &uh, &ul);
-          ph[t][n] = uh;
-          pl[t][n] = ul;
-        }
-      }
-      // ---- second product
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const typename T::v8 vh = as_v8<T>(buf.v[0][i][lane]), vl = as_v8<T>(buf.v[1][i][lane]);
-#pragma unroll
-        for (int t = 0; t < RT; ++t) acc[t][i] = T::mfma(vl, as_v8<T>(ph[t]), acc[t][i]);
-#pragma unroll
-        for (int t = 0; t < RT; ++t) acc[t][i] = T::mfma(vh, as_v8<T>(pl[t]), acc[t][i]);
-#pragma unroll
-        for (int t = 0; t < RT; ++t) acc[t][i] = T::mfma(vh, as_v8<T>(ph[t]), acc[t][i]);
+      for (int n = 0; n < 8; ++n) {
+        const int token = t0 + 16 * (n >> 2) + 4 * h + (n & 3);
+        sc[n >> 2][n & 3] = token >= row_lo && token < row_hi ? sc[n >> 2][n & 3] : -__builtin_inff();
       }
     }
-    if (wave >= kRowWaves / 2) prepare(t0, at ^ 1);
+    float top = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3]));
+    top = fmaxf(top, fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3])));
+    if (__builtin_amdgcn_ballot_w64(top > over) != 0ull) {
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const bool some = top > -__builtin_inff();             // false: nothing seen yet, m stays
+      const float up = over < 0.f ? (some ? top : 0.f) : fmaxf(top, 0.f);
+      over = over < 0.f && !some ? over : slack<T>();
+      const float f = __builtin_amdgcn_exp2f(-up);
+      m += up;
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) acc[i] *= f;
+#pragma unroll
+      for (int n = 0; n < 8; ++n) sc[n >> 2][n & 3] -= up;
+    }
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      sc[n >> 2][n & 3] = __builtin_amdgcn_exp2f(sc[n >> 2][n & 3]);
+      l += sc[n >> 2][n & 3];
+    }
+    const uint32_t odd = __builtin_amdgcn_readfirstlane(odd_tokens[(t0 / kStep) & 3]);
+    if (odd) {
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+        if (((odd >> (16 * (n >> 2) + 4 * h + (n & 3))) & 1u) && sc[n >> 2][n & 3] != 0.f) l = __builtin_nanf("");
+    }
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      uint32_t uh, ul;
+      split2_near<T>(sc[n >> 1][2 * (n & 1)], sc[n >> 1][2 * (n & 1) + 1], &uh, &ul);
+      ph[n] = uh;
+      pl[n] = ul;
+    }
+  };
+  const auto add = [&](const Buffer& buf) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const typename T::v8 vh = as_v8<T>(buf.v[0][i][lane]), vl = as_v8<T>(buf.v[1][i][lane]);
+      acc[i] = T::mfma(vl, as_v8<T>(ph), acc[i]);
+      acc[i] = T::mfma(vh, as_v8<T>(pl), acc[i]);
+      acc[i] = T::mfma(vh, as_v8<T>(ph), acc[i]);
+    }
+  };
+  // ---- the steps
+  int at = 0;
+  for (int t0 = c0; t0 < c1; t0 += kStep, at ^= 1) {
+    if (threadIdx.x == 0) odd_tokens[(t0 / kStep + 2) & 3] = 0u;   // last read two steps ago, next set in the next one
+    // of eight waves, half unpack after their products: the two of a SIMD need the matrix core in turn
+    const bool first = W > kUnpackers || wave < W / 2;
+    if (wave < kUnpackers && first) prepare(t0, bufs[at ^ 1]);
+    if (t0 < hi_max && t0 + kStep > lo_min) {
+      weigh(bufs[at], t0);
+      add(bufs[at]);
+    }
+    if (!first) prepare(t0, bufs[at ^ 1]);
     lds_barrier();
   }
 
   if (!live) return;
   const int64_t row0 = (b * a.c.heads + head) * a.rows;
   float* part_ml = a.part + a.batch * a.c.heads * a.rows * a.splits * D;
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+  if (bad) {
+    l = __builtin_nanf("");
+    m = 0.f;
+  }
+  if (base + col >= a.rows) return;
 #pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    l[t] += __shfl_xor(l[t], 16);
-    l[t] += __shfl_xor(l[t], 32);
-    if (bad) {
-      l[t] = __builtin_nanf("");
-      m[t] = 0.f;
-    }
-    const int r = base + 16 * t + col;
-    if (r >= a.rows) continue;
-#pragma unroll
-    for (int i = 0; i < NT; ++i) store4<T, D>(a, b, head, split, row0, r, 16 * i + 4 * h, acc[t][i], l[t]);
-    if (a.splits > 1 && h == 0) {
-      float* ml = part_ml + ((row0 + r) * a.splits + split) * 2;
-      ml[0] = over[t] < 0.f && !bad ? kNone : m[t];   // kNone: no token of the split was seen
-      ml[1] = l[t];
-    }
+  for (int i = 0; i < NT; ++i) store4<T, D>(a, b, head, split, row0, r, 16 * i + 4 * h, acc[i], l);
+  if (a.splits > 1 && h == 0) {
+    float* ml = part_ml + ((row0 + r) * a.splits + split) * 2;
+    ml[0] = over < 0.f && !bad ? kNone : m;             // kNone: no token of the split was seen
+    ml[1] = l;
   }
 }
 
@@ -800,7 +778,7 @@ hipError_t launch_shape(const AttendArgs& a, const AttendPlan& p, hipStream_t st
   // (4 of them), two XCDs had every first split.
   const dim3 grid((unsigned)(a.c.heads * p.row_tiles), (unsigned)a.batch, (unsigned)p.splits);
   if (p.by_rows)
-    hipLaunchKernelGGL((attend_rows_kernel<T, D, GS, (D == 256 ? 1 : 2)>), grid, dim3(kRowThreads), 0, stream, a);
+    hipLaunchKernelGGL((attend_rows_kernel<T, D, GS>), grid, dim3(64 * row_waves(D)), 0, stream, a);
   else
     hipLaunchKernelGGL((attend_kernel<T, D, GS>), grid, dim3(kThreads), 0, stream, a);
   hipError_t e = hipGetLastError();

@@ -90,12 +90,11 @@ int64_t part_floats(const AttendArgs& a, int64_t splits) {
 
 }  // namespace
 
-// Rows: up to 512 query rows per kv head (single tokens, drafts) take 16 rows per workgroup,
-// whose waves share out the tokens; more rows (prompts) take the form whose eight waves have
-// two 16-row tiles of their own each (one at head_dim 256, whose accumulators are twice as
-// large) and share the unpacked tokens.  Measured at 8192 or 4096 tokens, the first form
-// against the second: 192 rows 56 us / 69, 512 rows of 64 elements 46 / 52, 400 rows of 256
-// elements 70 / 80; 400 rows of 128 elements in groups of 64 118 / 109.
+// Rows: single tokens, drafts and short chunks take 16 query rows of one kv head per workgroup,
+// whose waves share out the tokens; long chunks (prompts) take the form whose waves have 16
+// rows of their own each and share the unpacked tokens.  Measured, the first form against the
+// second: head_dim 128, 8192 tokens, 192 rows 60 us / 67, 256 rows 73 / 66; head_dim 64, 512
+// rows 46 / 50, 1024 rows 87 / 79; head_dim 256, 800 rows 107 / 121, 2048 rows 265 / 246.
 // Splits: as many as make one workgroup per CU in the prompt form and at head_dim 256 (only one
 // is resident: 19 us against 35 with four, 8192 tokens), two with four groups per row (17 us /
 // 20), else four (32 ragged sequences: 53 us against 63 with three; 131071 tokens: 35 us, with
@@ -110,7 +109,7 @@ struct Shape {
 
 Shape shape_of(int64_t batch, int heads, int head_dim, int group, int64_t rows) {
   Shape s{};
-  s.by_rows = rows > 512;
+  s.by_rows = rows >= (head_dim == 128 ? 256 : 1024);
   const int64_t wg_rows = s.by_rows ? (head_dim == 256 ? 128 : 256) : 16;
   s.row_tiles = (int32_t)((rows + wg_rows - 1) / wg_rows);
   s.step = s.by_rows ? 512 : 128;

@@ -345,8 +345,8 @@ typedef struct {
  * 0); one workspace serves any number of calls in stream order, calls that may overlap need
  * their own.  The result depends only on the inputs and max_length.  Cached rows that are not
  * finite reach only the queries that see their token: those of K make their outputs NaN, those
- * of V the elements of their group, or the whole outputs with more than 512 query rows per kv
- * head (q_len * q_heads / heads).  batch == 0 or q_len == 0 is a no-op.  One kernel is enqueued, or two when the tokens are split over workgroups. */
+ * of V the elements of their group, or the whole outputs in calls with 256 query rows per kv
+ * head (q_len * q_heads / heads) or more.  batch == 0 or q_len == 0 is a no-op.  One kernel is enqueued, or two when the tokens are split over workgroups. */
 int32_t qmm_kv_attend(const qmm_kv_cache_t* cache, const qmm_kv_attend_t* args, void* out, void* workspace,
                       int64_t workspace_bytes, void* stream);
 

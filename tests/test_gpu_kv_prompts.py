@@ -19,6 +19,11 @@ PROMPTS = [
     ([560, 520], 520, 1, 1, 256, 64, 16, 0, "bf16"),
     ([560], 513, 1, 1, 256, 32, 16, 50, "fp16"),
     ([200], 130, 1, 4, 256, 128, 16, 0, "bf16"),
+    ([540, 90], 520, 1, 2, 64, 64, 16, 0, "bf16"),                  # as above with twice the rows and more
+    ([300, 0, 7], 260, 1, 4, 64, 32, 32, 77, "fp16"),
+    ([330], 300, 2, 4, 256, 64, 16, 0, "bf16"),
+    ([560], 513, 1, 2, 256, 32, 16, 50, "fp16"),
+    ([200], 260, 1, 4, 256, 128, 16, 0, "bf16"),
 ]
 
 
@@ -33,10 +38,11 @@ def test_prompt_matches_float64(lengths, q_len, heads, rep, dim, group, page, wi
     s.check(y, queries, dim ** -0.5, window=window)
 
 
-def test_prompt_all_tokens_scale_and_strides():
+@pytest.mark.parametrize("q_len", [270, 520])
+def test_prompt_all_tokens_scale_and_strides(q_len):
     """causal=False, a negative scale, queries as a strided slice of a larger tensor."""
     import bit_affine_quantized_qmv_amd as q
-    lengths, heads, rep, q_len, dim = [60, 1, 0, 200], 2, 2, 270, 128
+    lengths, heads, rep, dim = [60, 1, 0, 200], 2, 2, 128
     s = Setup(lengths, heads, dim, 64, 16, "bf16", seed=5)
     dev = s.len_dev.device
     big = _rows((heads * rep + 2, len(lengths), q_len, dim + 8), "bf16", 6, loud=False)
@@ -46,10 +52,11 @@ def test_prompt_all_tokens_scale_and_strides():
     s.check(y, view.cpu(), -0.21, causal=False)
 
 
-def test_prompt_masked_tokens_may_hold_anything():
+@pytest.mark.parametrize("q_len", [140, 260])
+def test_prompt_masked_tokens_may_hold_anything(q_len):
     """NaN and infinite rows that a query does not see leave its output alone."""
     import bit_affine_quantized_qmv_amd as q
-    n, q_len, window = 400, 140, 64
+    n, window = 400, 64
     s = Setup([n], 1, 64, 32, 16, "bf16", seed=13)
     dev = s.len_dev.device
     queries = _rows((1, q_len, 4, 64), "bf16", 14, loud=False)
@@ -68,9 +75,9 @@ def test_prompt_masked_tokens_may_hold_anything():
     assert torch.isnan(y[0, -1].float()).all()
 
 
-def test_prompt_a_missing_page_reaches_the_output_through_the_splits():
+@pytest.mark.parametrize("q_len", [300, 520])
+def test_prompt_a_missing_page_reaches_the_output_through_the_splits(q_len):
     import bit_affine_quantized_qmv_amd as q
-    q_len = 300
     s = Setup([3000, 2900], 1, 64, 32, 16, "bf16", seed=21)
     dev = s.len_dev.device
     queries = _rows((2, q_len, 2, 64), "bf16", 22, loud=False)
@@ -84,7 +91,7 @@ def test_prompt_a_missing_page_reaches_the_output_through_the_splits():
         assert nan[0][needs].all() and not nan[0][~needs].any() and not nan[1].any()
 
 
-@pytest.mark.parametrize("q_len", [2, 600])
+@pytest.mark.parametrize("q_len", [2, 600, 1100])
 @pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 40])
 def test_a_window_beyond_any_length_is_no_window(q_len, window):
     """Also where queries stand before the sequence (more queries than tokens)."""
@@ -97,7 +104,7 @@ def test_a_window_beyond_any_length_is_no_window(q_len, window):
     s.check(y, queries, 64 ** -0.5)
 
 
-@pytest.mark.parametrize("q_len", [3, 520])
+@pytest.mark.parametrize("q_len", [3, 520, 1050])
 def test_scale_zero_is_the_mean_of_what_a_query_sees(q_len):
     import bit_affine_quantized_qmv_amd as q
     s = Setup([77, 2, 0], 1, 64, 32, 16, "fp16", seed=25)
