@@ -29,7 +29,7 @@
 // and threshold arrive.  For many rows (2) is bound by its vector instructions, about 70 per
 // column, most of them the exponential, the division by T (a product with 1/T and a correction
 // changed nothing measurable) and the conversion to an integer.  Measured, 151936 columns: one
-// row with top-k and top-p 25 us; 32 rows with mixed settings 48 us (6 + 14 + 12 + 13 us).
+// row with top-k and top-p 25 us; 32 rows with mixed settings 45 us (6 + 13 + 12 + 15 us).
 #include "device_common.hpp"
 #include "sample.hpp"
 
@@ -44,7 +44,10 @@ constexpr int kRowThreads = 1024;
 constexpr int kRowWaves = kRowThreads / 64;
 constexpr int kLow = 32;             // keys per bin
 constexpr int kShift = 5;
-constexpr uint32_t kFew = 256;       // candidates that one wave draws from
+// Candidates that one wave draws from, and that a row draws from at all; beyond, the chunks'
+// sums are faster (3707 candidates: 31 us a call instead of 40).  Only a top-p inside a top-k
+// needs up to kCandidates, since the chunks do not know its bin.
+constexpr uint32_t kFew = 256, kHeld = 1024;
 constexpr int kUnitBits = 24;        // u and top_p count in units of 2^-24
 constexpr int kRun = 8;              // consecutive columns per lane and step
 constexpr int kStep = 64 * kRun;     // columns per wave and step
@@ -292,6 +295,11 @@ __global__ __launch_bounds__(kChunkThreads) void chunk_weights_kernel(const Samp
   }
 }
 
+// Candidates of a row from which it is drawn.
+__device__ inline uint32_t held_limit(int32_t mode, const Row& r) {
+  return mode == kByCount && r.units < (1u << kUnitBits) ? (uint32_t)kCandidates : kHeld;
+}
+
 // What a row keeps: keys above t, and the first c columns with key t.
 struct Cut {
   uint32_t t;
@@ -429,12 +437,14 @@ __global__ __launch_bounds__(kChunkThreads) void collect_kernel(const SampleArgs
   const uint32_t min_key = smallest_key<T>(top_key, top, r.t, r.min_p, lane);
   uint32_t edge = max(1u, (uint32_t)bin << kShift);
   int32_t low_bin = bin;
-  if (mode != kByCount) {                  // with top-k the share is of the weights below min_p too
+  // (min-p; but a top-p's share inside a top-k is of the weights below min_p too)
+  if (mode != kByCount || r.units == (1u << kUnitBits)) {
     edge = max(edge, min_key);
     low_bin = max(bin, (int32_t)(min_key >> kShift));
   }
-  // more columns above the bin than the last kernel holds: none are stored
-  const bool store = mode == kAll || low_bin != bin || sh.above_count <= (uint32_t)kCandidates;
+  // more columns above the bin than the last kernel draws from: none are stored
+  const uint32_t limit = held_limit(mode, r);
+  const bool store = mode == kAll || low_bin != bin || sh.above_count <= limit;
   if (threadIdx.x < kLow) low[threadIdx.x] = 0u;
   __syncthreads();
   if (chunk == 0 && threadIdx.x == 0) {
@@ -448,7 +458,7 @@ __global__ __launch_bounds__(kChunkThreads) void collect_kernel(const SampleArgs
     p.low_bin = low_bin;
     p.min_key = min_key;
     s.plan = p;
-    if (!store) s.found = kCandidates + 1;
+    if (!store) s.found = limit + 1;
   }
   u64 mass = 0;
   for (int64_t base = begin; base < end; base += kAhead * kCols) {
@@ -486,7 +496,7 @@ __global__ __launch_bounds__(kChunkThreads) void collect_kernel(const SampleArgs
       for (; take; take &= take - 1u, ++at) {          // few: their logits are read again
         const int bit = __ffs(take) - 1;
         const int64_t c = i + (bit / kRun) * kCols + bit % kRun;
-        if (at >= (uint32_t)kCandidates) break;
+        if (at >= limit) break;
         const uint32_t k = key_of<FP16>(x[c]);
         s.candidate[at] = ((u64)k << 32) | (uint32_t)c;
         s.weight[at] = weight<T>(k, top_key, top, r.t);
@@ -593,7 +603,7 @@ __global__ __launch_bounds__(kRowThreads) void row_kernel(const SampleArgs a) {
   const uint32_t u_units = min(units_of(a.u[row]), (1u << kUnitBits) - 1u);
 
   // ---- candidates in LDS: every column that can be drawn, when they fit
-  const bool held = threshold && found <= (uint32_t)kCandidates;
+  const bool held = threshold && found <= held_limit(mode, r);
   if (held) {
     for (uint32_t i = threadIdx.x; i < found; i += kRowThreads) {
       cand[i] = s.candidate[i];
@@ -773,6 +783,7 @@ __global__ __launch_bounds__(kRowThreads) void row_kernel(const SampleArgs a) {
     }
   } else {
     // each chunk's kept weight but for its ties, and its ties: eight threads per chunk
+    if (threadIdx.x == 0) sh.begin = sh.end = 0;
     if (threadIdx.x < kLow) {
       const uint32_t key = ((uint32_t)plan.low_bin << kShift) + threadIdx.x;
       sh.low_weight[threadIdx.x] = threshold && key > cut.t && key <= top_key ? int_weight(key) : 0ull;
@@ -863,7 +874,7 @@ __global__ __launch_bounds__(kRowThreads) void row_kernel(const SampleArgs a) {
       uint32_t t = sh.before_ties;
       for (int w = 0; w < kRowWaves; ++w) {
         const u64 m = part_sum(w, t);
-        if (before + m > sh.target) {
+        if (before + m > sh.target || w == kRowWaves - 1) {   // (the range shrinks in any case)
           sh.begin = begin + w * part;
           sh.end = min(end, sh.begin + part);
           break;

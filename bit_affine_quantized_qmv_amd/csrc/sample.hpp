@@ -10,7 +10,7 @@ namespace sampling {
 constexpr int kBins = 2048;         // values of an order key's high 11 bits
 constexpr int kMaxChunks = 128;     // column chunks per row
 
-constexpr int kCandidates = 12288;  // columns of a row that the last kernel holds in LDS
+constexpr int kCandidates = 12288;  // columns of a row that the last kernel holds in LDS, at most
 
 // How a row's column is drawn.
 enum RowMode : int32_t {
@@ -28,7 +28,7 @@ struct RowPlan {
   unsigned long long above_mass, total_mass; // weight above the threshold's bin, of all columns
   uint32_t above_count;
   int32_t mode, bin;
-  int32_t low_bin;                           // bin, or the bin of min_key where that is higher (not kByCount)
+  int32_t low_bin;                           // bin, or the bin of min_key where that is higher (not with top-p inside top-k)
   uint32_t min_key;                          // smallest key whose weight reaches min_p
   uint32_t pad;
 };
@@ -41,7 +41,7 @@ struct RowSpace {
   unsigned long long top[kMaxChunks];        // each chunk's largest (key << 32 | ~column), 0: nothing to draw
   uint32_t count[kBins];
   RowPlan plan;
-  uint32_t found;                            // candidates; more than kCandidates: they are incomplete
+  uint32_t found;                            // candidates; more than the row is drawn from: they are incomplete
   uint32_t pad;
   unsigned long long candidate[kCandidates]; // key << 32 | column, in any order
   float weight[kCandidates];                 // their relative weights
