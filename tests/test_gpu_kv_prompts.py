@@ -126,3 +126,32 @@ def test_tensors_of_one_call_are_on_one_gpu():
         q.kv_attend(queries, s.cache, s.table, s.len_dev)
     with pytest.raises(ValueError, match="one GPU"):
         q.sample(torch.zeros(2, 8, dtype=torch.bfloat16), torch.zeros(2, device=s.len_dev.device))
+
+
+def test_a_pool_past_32_bit_offsets():
+    """The same rows at the start of a small pool and at the end of one of 9 GB (more than 2^31
+    words): the same bits come back, and the same outputs."""
+    import bit_affine_quantized_qmv_amd as q
+    dev = require_gpu()
+    page, heads, dim, group, n, last = 64, 8, 128, 32, 300, 110000
+    if torch.cuda.mem_get_info(dev)[0] < 16 << 30:
+        pytest.skip("needs 16 GB of free GPU memory")
+    small = q.kv_cache(8, page, heads, dim, group, "bf16", dev)
+    large = q.kv_cache(last, page, heads, dim, group, "bf16", dev)
+    assert large.data.numel() > 2 ** 31
+    blocks = -(-n // page)
+    k, v = (_rows((n, heads, dim), "bf16", seed).to(dev) for seed in (31, 32))
+    near = torch.arange(blocks, dtype=torch.int32, device=dev)[None]
+    far = last - 1 - near
+    results = []
+    for cache, table in ((small, near), (large, far)):
+        j = torch.arange(n, device=dev)
+        slots = (table[0, j // page] * page + j % page).int()
+        q.kv_append(cache, k, v, slots)
+        lengths = torch.tensor([n], dtype=torch.int32, device=dev)
+        outs = [q.kv_attend(_rows((1, q_len, 2 * heads, dim), "bf16", 33).to(dev), cache, table, lengths)
+                for q_len in (1, 150)]
+        results.append([*q.kv_read(cache, slots), *outs])
+    torch.cuda.synchronize()
+    for a, b in zip(*results):
+        assert not torch.isnan(a.float()).any() and torch.equal(a, b)
