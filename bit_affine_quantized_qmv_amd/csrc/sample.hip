@@ -29,7 +29,7 @@
 // and threshold arrive.  For many rows (2) is bound by its vector instructions, about 70 per
 // column, most of them the exponential, the division by T (a product with 1/T and a correction
 // changed nothing measurable) and the conversion to an integer.  Measured, 151936 columns: one
-// row with top-k and top-p 25 us; 32 rows with mixed settings 45 us (6 + 13 + 12 + 15 us).
+// row with top-k and top-p 25 us; 32 rows with mixed settings 40 us (5 + 11 + 10 + 14 us).
 #include "device_common.hpp"
 #include "sample.hpp"
 
@@ -953,8 +953,10 @@ hipError_t launch(const SampleArgs& a, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_sample(SampleArgs a, hipStream_t stream) {
-  // about 1024 chunks in all, each of whole 2048-column steps of its workgroup
-  const int64_t want = a.rows >= 1024 ? 1 : (1024 / a.rows < kMaxChunks ? 1024 / a.rows : kMaxChunks);
+  // at most 2048 chunks in all, each of whole 2048-column steps of its workgroup (32 rows of
+  // 151936: 1024 chunks leave some CUs four workgroups and others three, 45 us; 2048 40 us;
+  // 4096, whose histograms are cleared and joined more often, 49 us)
+  const int64_t want = a.rows >= 2048 ? 1 : (2048 / a.rows < kMaxChunks ? 2048 / a.rows : kMaxChunks);
   const int64_t steps = (a.n + kCols - 1) / kCols;
   a.chunk = (steps + want - 1) / want * kCols;
   a.chunks = (int32_t)((a.n + a.chunk - 1) / a.chunk);
