@@ -18,7 +18,7 @@
 // row's histogram or, for a row without top-k and top-p, as the chunk's sum; (3) the
 // threshold's bin, and each chunk's columns from that bin up, the candidates; (4) one
 // workgroup per row, with the candidates in its LDS, finds the threshold and draws.  Where
-// there are more candidates than LDS holds, (3) has left each chunk's weight above the bin and
+// there are more candidates than that pays for, (3) has left each chunk's weight above the bin and
 // its columns of each key in the bin, from which (4) finds the threshold and the chunk to draw
 // from.  What touches every column is spread over the chunks' workgroups: one workgroup takes
 // about 10 us for 10 instructions on each of 150000 columns.  (Two kernels with one workgroup
