@@ -640,9 +640,10 @@ __global__ __launch_bounds__(64 * row_waves(D), 1) void attend_rows_kernel(const
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
       const bool some = top > -__builtin_inff();             // false: nothing seen yet, m stays
-      const float up = over < 0.f ? (some ? top : 0.f) : fmaxf(top, 0.f);
-      over = over < 0.f && !some ? over : slack<T>();
-      const float f = __builtin_amdgcn_exp2f(-up);
+      const bool empty = over < 0.f;                         // no score yet: m may go down too
+      const float up = empty ? (some ? top : 0.f) : fmaxf(top, 0.f);
+      over = empty && !some ? over : slack<T>();
+      const float f = empty ? 1.0f : __builtin_amdgcn_exp2f(-up);   // (of zero sums: 2^-up can be infinite)
       m += up;
       l *= f;
 #pragma unroll
