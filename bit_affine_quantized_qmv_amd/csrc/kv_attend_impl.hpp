@@ -167,9 +167,7 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS>())) void attend_kernel
   const auto place = [&](int t0) {
     Place p{0, 0};
     if (t0 < hi_max && t0 + 16 > lo_min) {
-      // t0 / page_size by a rounded-up reciprocal: exact below 2^27 tiles of 16
-      const uint32_t tile = (uint32_t)t0 >> 4;
-      const int blk = (int)(((uint64_t)tile * a.page_recip) >> 40);
+      const int blk = block_of_tile((uint32_t)t0 >> 4, a.page_recip);
       p.token = t0 - blk * a.c.page_size;
       p.page = __builtin_amdgcn_readfirstlane(table[blk]);
     }
@@ -470,7 +468,7 @@ __global__ __launch_bounds__(64 * row_waves(D), 1) void attend_rows_kernel(const
       page_next[i] = 0;
       token_next[i] = 0;
       if (t < wg_hi && t + 16 > wg_lo) {
-        const int blk = (int)(((uint64_t)((uint32_t)t >> 4) * a.page_recip) >> 40);
+        const int blk = block_of_tile((uint32_t)t >> 4, a.page_recip);
         token_next[i] = t - blk * a.c.page_size;
         page_next[i] = __builtin_amdgcn_readfirstlane(table[blk]);
       }

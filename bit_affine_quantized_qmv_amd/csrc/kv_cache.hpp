@@ -49,6 +49,18 @@ __host__ __device__ constexpr int v_byte(int t, int o, int j, int head_dim) {
   return (((t / 4) * 16 + o) * (head_dim / 32) + j) * 4 + t % 4;
 }
 
+// Block (entry of a block table) of the 16-token tile `tile`: tile / d with d = page_size / 16,
+// by the reciprocal 2^38 / d rounded up.  With tiles below 2^26 (2^30 tokens) and d <= 2^12 the
+// product stays below 2^64, and the rounding adds less than 2^38 / d to it, so that the quotient
+// is exact.
+constexpr int kRecipShift = 38;
+__host__ __device__ constexpr uint64_t page_recip(int page_size) {
+  return ((1ull << kRecipShift) + (uint64_t)(page_size / 16) - 1) / (uint64_t)(page_size / 16);
+}
+__host__ __device__ constexpr int block_of_tile(uint32_t tile, uint64_t recip) {
+  return (int)(((uint64_t)tile * recip) >> kRecipShift);
+}
+
 struct CacheArgs {
   uint32_t* data;
   int64_t pages;
@@ -96,7 +108,7 @@ struct AttendArgs {
   int32_t chunk;          // tokens per split, a multiple of the tokens of one workgroup step
   int32_t splits;
   void* out;              // dense [batch, q_len, q_heads, head_dim]
-  uint64_t page_recip;    // 2^40 / (page_size / 16), rounded up
+  uint64_t page_recip;    // page_recip(page_size)
   float* part;            // splits > 1: [batch * heads * rows][splits][head_dim] sums, then their (max, sum) pairs
 };
 

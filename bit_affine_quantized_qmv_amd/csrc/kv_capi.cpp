@@ -220,7 +220,7 @@ int32_t qmm_kv_attend(const qmm_kv_cache_t* cache, const qmm_kv_attend_t* args, 
     if (workspace_bytes < need)
       return report(QMM_ERR_SHAPE, "kv_attend: workspace of " + std::to_string(workspace_bytes) + " bytes, needs " +
                                        std::to_string(need));
-    a.page_recip = ((1ull << 40) + a.c.page_size / 16 - 1) / (a.c.page_size / 16);
+    a.page_recip = kv::page_recip(a.c.page_size);
     a.chunk = p.chunk;
     a.splits = p.splits;
     a.out = out;
