@@ -18,10 +18,13 @@
 //
 // Softmax: m, the sum of p, the bias sums and both accumulators are float32.  m is raised only
 // when a score exceeds it by more than slack() (in powers of two), so most steps rescale
-// nothing; p is then at most 2^slack.  p_j s_jg goes to the matrix cores as two operands of
-// the element type, its leading bits and the rest (split2), so that the product carries 16
-// (bf16) or 22 (fp16) bits of it: with one operand, a row that attends to one token would
-// return that token's codes with an error of up to 2^-8 (bf16) of their span.
+// nothing; p is then at most 2^slack.  p_j s_jg goes to the matrix cores as two bfloat16
+// operands, its leading bits and the rest (split2), so that the product carries 16 bits of it:
+// with one operand, a row that attends to one token would return that token's codes with an
+// error of up to 2^-8 of their span.  They are bfloat16 in fp16 calls too (the codes are exact in
+// either type): fp16 has nothing below 2^-24, where the small p of a row with most of its weight
+// on one token lie, and their codes would vanish while their biases and their share of the sum
+// stay.
 #pragma once
 
 #include <cfloat>
@@ -125,6 +128,7 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS>())) void attend_kernel
   constexpr int CPG = GS / 32;
   constexpr int kRows = 16;           // query rows per workgroup
   constexpr int kPitch = D + 4;       // LDS row of the merge, padded against bank conflicts
+  using P = Bf16;                     // operands of the second product
 
   const int lane = threadIdx.x & 63, col = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -281,7 +285,7 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS>())) void attend_kernel
     // ---- probabilities
     float top = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3]));
     top = fmaxf(top, fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3]))) * scale;
-    if (__builtin_amdgcn_ballot_w64(top > m + slack<T>()) != 0ull) {
+    if (__builtin_amdgcn_ballot_w64(top > m + slack<P>()) != 0ull) {
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
       const float raised = fmaxf(m, top);
@@ -313,7 +317,7 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS>())) void attend_kernel
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
         uint32_t uh, ul;
-        split2<T>(x[2 * n], x[2 * n + 1], &uh, &ul);
+        split2<P>(x[2 * n], x[2 * n + 1], &uh, &ul);
         hi[n] = uh;
         lo[n] = ul;
       }
@@ -323,9 +327,9 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS>())) void attend_kernel
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
           const uint32_t e0 = (n ? w0 >> 4 : w0) & 0x0F0F0F0Fu, e1 = (n ? w1 >> 4 : w1) & 0x0F0F0F0Fu;
-          const u32x4 vc = {T::fp8x2_lo(e0), T::fp8x2_hi(e0), T::fp8x2_lo(e1), T::fp8x2_hi(e1)};
-          acc[2 * j + n] = T::mfma(as_v8<T>(vc), as_v8<T>(lo), acc[2 * j + n]);
-          acc[2 * j + n] = T::mfma(as_v8<T>(vc), as_v8<T>(hi), acc[2 * j + n]);
+          const u32x4 vc = {P::fp8x2_lo(e0), P::fp8x2_hi(e0), P::fp8x2_lo(e1), P::fp8x2_hi(e1)};
+          acc[2 * j + n] = P::mfma(as_v8<P>(vc), as_v8<P>(lo), acc[2 * j + n]);
+          acc[2 * j + n] = P::mfma(as_v8<P>(vc), as_v8<P>(hi), acc[2 * j + n]);
         }
       }
     }

@@ -340,7 +340,8 @@ typedef struct {
 } qmm_kv_attend_t;
 
 /* Attention over the cache: out, DEVICE, dense [batch, q_len, q_heads, head_dim] of dtype,
- * 16-byte aligned.  Scores, softmax and sums are float32.  workspace: DEVICE, 16-byte aligned,
+ * 16-byte aligned.  Scores, softmax and sums are float32; each probability times V's scale
+ * enters its product with V's codes with 16 bits and float32's range.  workspace: DEVICE, 16-byte aligned,
  * any content, at least qmm_kv_attend_workspace_bytes(cache, args) bytes (NULL when that is
  * 0); one workspace serves any number of calls in stream order, calls that may overlap need
  * their own.  The result depends only on the inputs and max_length.  Cached rows that are not
