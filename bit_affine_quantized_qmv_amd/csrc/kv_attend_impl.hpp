@@ -17,8 +17,8 @@
 // e < 4, 4h + e - 4 of the second one otherwise.
 //
 // Softmax: m, the sum of p, the bias sums and both accumulators are float32.  m is raised only
-// when a score exceeds it by more than slack() (in powers of two), so most steps rescale
-// nothing; p is then at most 2^slack.  p_j s_jg goes to the matrix cores as two bfloat16
+// when a score exceeds it by more than kSlack (in powers of two), so most steps rescale
+// nothing; p is then at most 2^kSlack.  p_j s_jg goes to the matrix cores as two bfloat16
 // operands, its leading bits and the rest (split2), so that the product carries 16 bits of it:
 // with one operand, a row that attends to one token would return that token's codes with an
 // error of up to 2^-8 of their span.  They are bfloat16 in fp16 calls too (the codes are exact in
@@ -40,24 +40,14 @@ constexpr int kThreads = 64 * kWaves;
 constexpr int kStep = 32;              // tokens per wave and step
 constexpr float kNone = -FLT_MAX;      // running maximum before any token
 
-// Largest exponent of an unnormalised probability.  fp16: p * s must stay below 65504 for
-// every scale a cache of fp16 rows can have (range / 15 <= 131008 / 15 = 8734): 2^2.9 * 8734.
-template <class T>
-constexpr float slack() { return T::kDtype == QMM_BF16 ? 8.0f : 2.9f; }
+constexpr float kSlack = 8.0f;         // largest exponent of an unnormalised probability
 
-// Two float32 values as element-type pairs hi + lo: hi their leading bits (truncated), lo the
-// rest rounded to nearest.
-template <class T>
+// Two float32 values as bfloat16 pairs hi + lo: hi their leading bits (truncated), lo the rest
+// rounded to nearest: 2^-16 of the value at most is lost.
 __device__ inline void split2(float x, float y, uint32_t* hi, uint32_t* lo) {
-  if constexpr (T::kDtype == QMM_BF16) {
-    const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
-    *hi = __builtin_amdgcn_perm(b, a, 0x07060302u);
-    *lo = T::pack2(x - __uint_as_float(a & 0xFFFF0000u), y - __uint_as_float(b & 0xFFFF0000u));
-  } else {
-    const auto t = __builtin_amdgcn_cvt_pkrtz(x, y);
-    *hi = __builtin_bit_cast(uint32_t, t);
-    *lo = T::pack2(x - (float)t[0], y - (float)t[1]);
-  }
+  const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+  *hi = __builtin_amdgcn_perm(b, a, 0x07060302u);
+  *lo = Bf16::pack2(x - __uint_as_float(a & 0xFFFF0000u), y - __uint_as_float(b & 0xFFFF0000u));
 }
 
 template <int N>
@@ -285,7 +275,7 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS>())) void attend_kernel
     // ---- probabilities
     float top = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3]));
     top = fmaxf(top, fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3]))) * scale;
-    if (__builtin_amdgcn_ballot_w64(top > m + slack<P>()) != 0ull) {
+    if (__builtin_amdgcn_ballot_w64(top > m + kSlack) != 0ull) {
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
       const float raised = fmaxf(m, top);
@@ -317,7 +307,7 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS>())) void attend_kernel
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
         uint32_t uh, ul;
-        split2<P>(x[2 * n], x[2 * n + 1], &uh, &ul);
+        split2(x[2 * n], x[2 * n + 1], &uh, &ul);
         hi[n] = uh;
         lo[n] = ul;
       }
@@ -391,9 +381,10 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS>())) void attend_kernel
 // (double-buffered, one barrier per step; the next step's words are in registers meanwhile):
 //   K  its codes as exact integers, and its scales and biases as float32: a score costs one
 //      matrix-core pass and two multiply-adds per group;
-//   V  the values s c + b themselves, as two operands (leading bits, rest), so that the
+//   V  the values s c + b themselves, as two bfloat16 operands (leading bits, rest), so that the
 //      probabilities need no scale per token and group: they are split once, and
-//      p v = p_hi v_lo + p_lo v_hi + p_hi v_hi.
+//      p v = p_hi v_lo + p_lo v_hi + p_hi v_hi, to 2^-14 of each |p v| (2^-15 in fp16 calls,
+//      where V is rounded instead of cut off).
 // (Codes and scales for V, as in the single-token form, cost 11 vector operations per score
 // more, two of them per group, against a third matrix-core pass here: 1223 us against 800 in
 // the case below.)
@@ -409,11 +400,10 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS>())) void attend_kernel
 // that gives it weight becomes NaN.
 // Scores leave the multiply-adds relative to the running maximum: -m is where they start.
 
-// split2 with hi rounded to nearest: for values below half the type's largest.
-template <class T>
+// split2 with hi rounded to nearest, for values below half the type's largest: 2^-17 is lost.
 __device__ inline void split2_near(float x, float y, uint32_t* hi, uint32_t* lo) {
-  *hi = T::pack2(x, y);
-  *lo = T::pack2(x - T::to_f32(*hi & 0xFFFFu), y - T::to_f32(*hi >> 16));
+  *hi = Bf16::pack2(x, y);
+  *lo = Bf16::pack2(x - Bf16::to_f32(*hi & 0xFFFFu), y - Bf16::to_f32(*hi >> 16));
 }
 
 // Waves per workgroup: 16 where 128 registers hold a wave, of which the first eight unpack.
@@ -425,6 +415,7 @@ __global__ __launch_bounds__(64 * row_waves(D), 1) void attend_rows_kernel(const
   constexpr int W = row_waves(D);
   constexpr int KC = D / 32, NT = D / 16, NG = D / GS, CPG = GS / 32;
   constexpr int kRows = 16;
+  using P = Bf16;                 // operands of the second product
   constexpr int kKUnits = (2 * KC + kUnpackers - 1) / kUnpackers, kVUnits = (NT + kUnpackers - 1) / kUnpackers;
   static_assert(NG * kStep <= 64 * kUnpackers, "one thread per scale word of a step");
   struct Buffer {
@@ -557,7 +548,10 @@ __global__ __launch_bounds__(64 * row_waves(D), 1) void attend_rows_kernel(const
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           uint32_t uh, ul;
-          split2<T>(v[2 * r], v[2 * r + 1], &uh, &ul);
+          if constexpr (T::kDtype == QMM_BF16)
+            split2(v[2 * r], v[2 * r + 1], &uh, &ul);        // any bfloat16: none rounds up to infinity
+          else
+            split2_near(v[2 * r], v[2 * r + 1], &uh, &ul);
           hi[2 * i + r] = uh;
           lo[2 * i + r] = ul;
         }
@@ -575,7 +569,7 @@ __global__ __launch_bounds__(64 * row_waves(D), 1) void attend_rows_kernel(const
 
   typename T::v8 q[KC];
   float qsum[NG], m = 0.f, l = 0.f;
-  float over = -__builtin_inff();    // scores above m + over raise m: any score at first, then slack
+  float over = -__builtin_inff();    // scores above m + over raise m: any score at first, then kSlack
   f32x4 acc[NT];
   const uint32_t one2 = T::pack2(1.0f, 1.0f);
   const u32x4 ones = {one2, one2, one2, one2};
@@ -644,7 +638,7 @@ __global__ __launch_bounds__(64 * row_waves(D), 1) void attend_rows_kernel(const
       const bool some = top > -__builtin_inff();             // false: nothing seen yet, m stays
       const bool empty = over < 0.f;                         // no score yet: m may go down too
       const float up = empty ? (some ? top : 0.f) : fmaxf(top, 0.f);
-      over = empty && !some ? over : slack<T>();
+      over = empty && !some ? over : kSlack;
       const float f = empty ? 1.0f : __builtin_amdgcn_exp2f(-up);   // (of zero sums: 2^-up can be infinite)
       m += up;
       l *= f;
@@ -667,7 +661,7 @@ __global__ __launch_bounds__(64 * row_waves(D), 1) void attend_rows_kernel(const
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
       uint32_t uh, ul;
-      split2_near<T>(sc[n >> 1][2 * (n & 1)], sc[n >> 1][2 * (n & 1) + 1], &uh, &ul);
+      split2_near(sc[n >> 1][2 * (n & 1)], sc[n >> 1][2 * (n & 1) + 1], &uh, &ul);
       ph[n] = uh;
       pl[n] = ul;
     }
@@ -675,10 +669,10 @@ __global__ __launch_bounds__(64 * row_waves(D), 1) void attend_rows_kernel(const
   const auto add = [&](const Buffer& buf) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const typename T::v8 vh = as_v8<T>(buf.v[0][i][lane]), vl = as_v8<T>(buf.v[1][i][lane]);
-      acc[i] = T::mfma(vl, as_v8<T>(ph), acc[i]);
-      acc[i] = T::mfma(vh, as_v8<T>(pl), acc[i]);
-      acc[i] = T::mfma(vh, as_v8<T>(ph), acc[i]);
+      const typename P::v8 vh = as_v8<P>(buf.v[0][i][lane]), vl = as_v8<P>(buf.v[1][i][lane]);
+      acc[i] = P::mfma(vl, as_v8<P>(ph), acc[i]);
+      acc[i] = P::mfma(vh, as_v8<P>(pl), acc[i]);
+      acc[i] = P::mfma(vh, as_v8<P>(ph), acc[i]);
     }
   };
   // ---- the steps

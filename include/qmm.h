@@ -340,14 +340,16 @@ typedef struct {
 } qmm_kv_attend_t;
 
 /* Attention over the cache: out, DEVICE, dense [batch, q_len, q_heads, head_dim] of dtype,
- * 16-byte aligned.  Scores, softmax and sums are float32; each probability times V's scale
- * enters its product with V's codes with 16 bits and float32's range.  workspace: DEVICE, 16-byte aligned,
- * any content, at least qmm_kv_attend_workspace_bytes(cache, args) bytes (NULL when that is
- * 0); one workspace serves any number of calls in stream order, calls that may overlap need
- * their own.  The result depends only on the inputs and max_length.  Cached rows that are not
- * finite reach only the queries that see their token: those of K make their outputs NaN, those
- * of V the elements of their group, or the whole outputs in calls with 256 query rows per kv
- * head (q_len * q_heads / heads) or more.  batch == 0 or q_len == 0 is a no-op.  One kernel is enqueued, or two when the tokens are split over workgroups. */
+ * 16-byte aligned.  Scores, softmax and sums are float32.  The operands of the product with V
+ * have float32's range and 16 bits: p s_g, whose error is at most 2^-16 of it; in calls with 256
+ * query rows per kv head (q_len * q_heads / heads) or more p and v, each product within 2^-14 of
+ * |p v|.  workspace: DEVICE, 16-byte aligned, any content, at least
+ * qmm_kv_attend_workspace_bytes(cache, args) bytes (NULL when that is 0); one workspace serves
+ * any number of calls in stream order, calls that may overlap need their own.  The result depends
+ * only on the inputs and max_length.  Cached rows that are not finite reach only the queries that
+ * see their token: those of K make their outputs NaN, those of V the elements of their group, or
+ * the whole outputs in calls with 256 such rows or more.  batch == 0 or q_len == 0 is a no-op.
+ * One kernel is enqueued, or two when the tokens are split over workgroups. */
 int32_t qmm_kv_attend(const qmm_kv_cache_t* cache, const qmm_kv_attend_t* args, void* out, void* workspace,
                       int64_t workspace_bytes, void* stream);
 

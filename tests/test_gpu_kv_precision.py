@@ -70,3 +70,15 @@ def test_small_weights_count_in_single_tokens(n, dim, group, size, gap, dtype):
     scale = dim ** -0.5
     y = attend(k, v, queries, group, dtype, scale)
     check(y, k, v, queries, group, dtype, scale, False)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("n,q_len,rep,dim,group,size,gap", [
+    (3000, 64, 4, 128, 64, 1.0, 18.0), (8192, 64, 4, 128, 32, 0.02, 14.0), (2500, 260, 4, 64, 64, 1.0, 19.0),
+    (2500, 260, 4, 256, 128, 1.0, 16.5)])
+def test_small_weights_count_in_prompts(n, q_len, rep, dim, group, size, gap, dtype):
+    k, v, direction = dominated(n, dim, dtype, size, gap, n + dim)
+    queries = (direction + 0.05 * torch.randn(q_len, rep, dim, generator=torch.Generator().manual_seed(4))).to(k.dtype)
+    scale = dim ** -0.5
+    y = attend(k, v, queries, group, dtype, scale)
+    check(y, k, v, queries, group, dtype, scale, True)
