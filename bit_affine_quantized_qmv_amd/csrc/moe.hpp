@@ -44,7 +44,7 @@ struct MoeArgs {
   // workspace
   int32_t* pair_expert;      // [tokens * top_k]: pair t * top_k + i is token t's i-th largest router logit
   float* pair_share;         // [tokens * top_k]: its unnormalised weight
-  uint16_t* h;               // [tokens * top_k][2][inter]: silu(gate) * up, leading bits and the rest
+  uint16_t* h;               // [tokens * top_k][2][inter]: silu(gate) * up in bfloat16, leading bits and the rest
   float* out;                // [tokens * top_k][splits][hidden]: each pair's product with down
   // waves that share one tile, each a part of K, and workgroups per expert, in the first and
   // the second kernel; stretches of K that different workgroups of the second kernel take

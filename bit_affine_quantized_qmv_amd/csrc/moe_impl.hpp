@@ -22,9 +22,10 @@
 // multiplied by zero.
 // Arithmetic per output as in the decode kernels, s * sum xq + b * sum x per group with exact
 // integer codes and float32 sums; sum x comes from a product with an all-ones operand.
-// h = silu(g) u reaches the second product as two operands of the element type, its leading
-// bits and the rest: the one rounding that a single operand would add is as large as the
-// output's own.
+// h = silu(g) u reaches the second product as two bfloat16 operands, its leading bits and the
+// rest (2^-17 of it is lost): the one rounding that a single operand would add is as large as
+// the output's own.  In fp16 calls too, where the codes are exact in either type: h there may
+// pass 65504, or lie where fp16 has few bits, and y still be an ordinary fp16 number.
 //
 // What bounds it: the stream, at 3.6 TB/s of the 5.2 of a copy -- each workgroup's first
 // loads wait for its users and its activations, and the last ones leave CUs idle.  Measured:
@@ -182,11 +183,12 @@ __device__ inline u32x4 even_odd(u32x4 u) {
 
 // One wave's weight stream of two 16-row tiles, through buffer descriptors over one expert: a
 // slot's offset is a scalar, the lane's row a register, rows past the last read as zeros, and
-// what a slot reads past its row's end is multiplied by zero.  The scales and biases of a
+// what a slot reads past its row's end is multiplied by zero.  Scales and biases are of type T,
+// the operands of the product of type X.  The scales and biases of a
 // round of kDepth slots are one load per tile, a round ahead: one load per slot asked for
 // twice as many cache lines as the codes (16 rows of two bytes each).  NARROW: they are read
 // one halfword at a time (rows, experts or arrays that are not whole words).
-template <class T, int BITS, int GS, bool NARROW>
+template <class T, class X, int BITS, int GS, bool NARROW>
 struct Stream {
   using S = Slot<BITS, GS>;
   static constexpr int TN = 2;
@@ -264,7 +266,7 @@ struct Stream {
   __device__ inline void consume(const SlotData<BITS, GS> (&d)[TN], const Sb& sb, int nth, int slot, const u32x4* x,
                                  int plane, int xrl, f32x4 (&acc)[TN]) const {
     constexpr int SPG = GS / 32;
-    const uint32_t one2 = T::pack2(1.0f, 1.0f);
+    const uint32_t one2 = X::pack2(1.0f, 1.0f);
     const u32x4 ones = {one2, one2, one2, one2};
     const f32x4 zero4 = {0.f, 0.f, 0.f, 0.f};
     const bool whole = (slot + 1) * S::kSpan <= K;
@@ -275,16 +277,16 @@ struct Stream {
     f32x4 part[TN], sum;
 #pragma unroll
     for (int c = 0; c < kSteps; ++c) {
-      typename T::v8 q[TN];
+      typename X::v8 q[TN];
 #pragma unroll
-      for (int t = 0; t < TN; ++t) q[t] = as_v8<T>(slot_codes<T, BITS, GS>(d[t], rc[t], c, gshift));
+      for (int t = 0; t < TN; ++t) q[t] = as_v8<X>(slot_codes<X, BITS, GS>(d[t], rc[t], c, gshift));
 #pragma unroll
       for (int p = 0; p < PLANES; ++p) {
-        const typename T::v8 av = as_v8<T>(x[p * plane + ((c * 4 + lg) << xrl) + row]);
+        const typename X::v8 av = as_v8<X>(x[p * plane + ((c * 4 + lg) << xrl) + row]);
         const bool fresh = c % SPG == 0 && p == 0;
-        sum = T::mfma(av, as_v8<T>(ones), fresh ? zero4 : sum);
+        sum = X::mfma(av, as_v8<X>(ones), fresh ? zero4 : sum);
 #pragma unroll
-        for (int t = 0; t < TN; ++t) part[t] = T::mfma(av, q[t], fresh ? zero4 : part[t]);
+        for (int t = 0; t < TN; ++t) part[t] = X::mfma(av, q[t], fresh ? zero4 : part[t]);
       }
       if ((c + 1) % SPG == 0) {
         const int g = c / SPG;
@@ -454,7 +456,7 @@ __device__ inline int fit_chunk(int rows, int parts, int* xrl) {
 // h rows of expert e's tokens.
 template <class T, int BITS, int GS, bool NARROW>
 __global__ __launch_bounds__(kThreads, kWorkgroups) void gate_up_kernel(const MoeArgs a, const int by_pair) {
-  using St = Stream<T, BITS, GS, NARROW>;
+  using St = Stream<T, T, BITS, GS, NARROW>;
   __shared__ Users u;
   __shared__ u32x4 xs[kXBytes / 16];
   __shared__ f32x4 hand[kWaves * 2 * 64];
@@ -505,9 +507,9 @@ __global__ __launch_bounds__(kThreads, kWorkgroups) void gate_up_kernel(const Mo
         const float g = acc[0][i];
         const float v = g / (1.0f + expf(-g)) * acc[1][i];
         uint16_t* h = a.h + (int64_t)u.pair[r] * 2 * a.inter + n;
-        const uint16_t hi = T::from_f32(v);
+        const uint16_t hi = Bf16::from_f32(v);
         h[0] = hi;
-        h[a.inter] = T::from_f32(v - T::to_f32(hi));
+        h[a.inter] = Bf16::from_f32(v - Bf16::to_f32(hi));
       }
     };
     Products<1, St, decltype(row), decltype(set_tiles), decltype(finish)> p{st, w};
@@ -522,7 +524,7 @@ __global__ __launch_bounds__(kThreads, kWorkgroups) void gate_up_kernel(const Mo
 // out[pair][z] = h Wd_e^T over the z-th stretch of inter, of expert e's pairs, in float32.
 template <class T, int BITS, int GS, bool NARROW>
 __global__ __launch_bounds__(kThreads, kWorkgroups) void down_kernel(const MoeArgs a, const int by_pair) {
-  using St = Stream<T, BITS, GS, NARROW>;
+  using St = Stream<T, Bf16, BITS, GS, NARROW>;
   __shared__ Users u;
   __shared__ u32x4 xs[kXBytes / 16];
   __shared__ f32x4 hand[kWaves * 2 * 64];

@@ -395,7 +395,8 @@ typedef struct {
 #define QMM_MOE_MAX_TOP_K 32
 
 /* The layer: y DEVICE [tokens, y_stride] of dtype, 2-byte aligned.  Sums in float32;
- * silu(g) * u enters the second product with twice the bits of dtype.  workspace: DEVICE, 16-byte aligned, qmm_moe_workspace_bytes(...) bytes of any content; one serves any
+ * silu(g) * u enters the second product with 16 bits (two bfloat16 parts) and float32's range.
+ * workspace: DEVICE, 16-byte aligned, qmm_moe_workspace_bytes(...) bytes of any content; one serves any
  * number of calls in stream order, calls that may overlap need their own.  The result depends
  * only on the inputs (no atomics).  tokens == 0 is a no-op.  Three kernels are enqueued. */
 int32_t qmm_moe(const qmm_moe_t* args, void* y, void* workspace, int64_t workspace_bytes, void* stream);
