@@ -12,6 +12,23 @@ constexpr int kMaxExperts = 512;
 constexpr int kMaxTopK = 32;
 constexpr int kWaves = 4;             // per workgroup
 constexpr int kMaxSplits = 16;
+constexpr int kXBytes = 40 * 1024;    // LDS of the staged activations: three workgroups per CU fit (with 48 KB, two)
+
+// How a row of K is walked, in slots (spans of K that one round of loads covers).  A workgroup's
+// walk starts at an even slot and goes on in chunks, what LDS holds of the activations; in a
+// chunk each of the `parts` waves of a tile takes a stretch, in rounds of its ring of loads.
+// Starts, chunks, stretches and rounds are all even: a round's scales are one load, which has
+// to start on a word also where a slot has one scale of two bytes.
+
+// Slots of a chunk: whole rounds of all parts where LDS holds them, else what it holds.
+// slot_entries: 16-byte entries of a slot per row, of all operand planes; 2^xrl rows; round: parts
+// times the ring's slots.
+__host__ __device__ constexpr int chunk_of(int slot_entries, int xrl, int round) {
+  const int fit = kXBytes / 16 / (slot_entries << xrl);
+  return fit >= round ? fit / round * round : fit & ~1;
+}
+// Slots of one part of n.
+__host__ __device__ constexpr int stretch_of(int n, int parts) { return ((n + parts - 1) / parts + 1) & ~1; }
 
 // A stack of quantized weights, [experts][N][K].
 struct Stack {

@@ -50,7 +50,6 @@ using decode::slot_reorder;
 
 constexpr int kThreads = 64 * kWaves;
 constexpr int kWorkgroups = 3;       // per compute unit: 168 registers per thread
-constexpr int kXBytes = 40 * 1024;   // LDS of the staged activations: three workgroups fit (with 48 KB, two)
 
 // Order key of a 16-bit float: larger values have larger keys, NaN the largest.
 template <class T>
@@ -333,13 +332,9 @@ struct Products {
   // the next slot to load
   int unit, c0, at;
 
-  // slots of a wave's stretch of a chunk: even, so that its scales start on a word; the loop
-  // goes over whole rounds of the ring, whose last slots may be the next wave's (loaded, and
-  // not used)
-  __device__ inline int stretch(int c) const {
-    const int n = min(w.chunk, w.k1 - c), per = (n + w.parts - 1) / w.parts;
-    return (per + 1) & ~1;
-  }
+  // slots of a wave's stretch of a chunk; the loop goes over whole rounds of the ring, whose last
+  // slots may be the next wave's (loaded, and not used)
+  __device__ inline int stretch(int c) const { return stretch_of(min(w.chunk, w.k1 - c), w.parts); }
   __device__ static inline int whole_rounds(int n) { return (n + kDepth - 1) / kDepth * kDepth; }
   __device__ inline int next_slot() const { return c0 + w.part * stretch(c0) + at; }
   __device__ inline void load_next(int i, Tiles& set_tiles) {
@@ -438,15 +433,14 @@ struct Products {
   }
 };
 
-// log2 of the staged rows, and the slots of `rows` rows (PLANES planes) that LDS holds, whole
-// ring rounds of every part where that many fit.
+// log2 of the staged rows, and the slots of a chunk of `rows` rows (PLANES planes).
 template <int PLANES, class St>
 __device__ inline int fit_chunk(int rows, int parts, int* xrl) {
   int l = 0;
   while ((1 << l) < rows) ++l;
   *xrl = l;
-  const int fit = kXBytes / 16 / ((St::kSlotX * PLANES) << l), round = parts * St::kDepth;
-  return fit >= round ? fit / round * round : fit;
+  static_assert(St::kDepth % 2 == 0 && chunk_of(St::kSlotX * PLANES, 4, kWaves * St::kDepth) >= 2, "even, not empty");
+  return chunk_of(St::kSlotX * PLANES, l, parts * St::kDepth);
 }
 
 // Workgroup (x, y) of both product kernels: y is an expert or, when the call has fewer (token,
@@ -545,7 +539,7 @@ __global__ __launch_bounds__(kThreads, kWorkgroups) void down_kernel(const MoeAr
     t.tile(0, first_row(unit));
     t.tile(1, first_row(unit) + 16);
   };
-  const int slots = (a.inter + St::S::kSpan - 1) / St::S::kSpan, share = ((slots + a.splits - 1) / a.splits + 1) & ~1;
+  const int slots = (a.inter + St::S::kSpan - 1) / St::S::kSpan, share = stretch_of(slots, a.splits);
   const int z = blockIdx.z;
   for (int r0 = 0; r0 < u.count; r0 += 16) {
     const int rows = min(16, u.count - r0);
