@@ -21,7 +21,7 @@ namespace qmm {
 namespace kv {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = kCopyThreads;
 
 // Address of (slot, head)'s page words, and the token inside the page.
 __device__ inline uint32_t* page_of(const CacheArgs& c, int32_t slot, int head, int* token) {
@@ -156,9 +156,7 @@ __global__ __launch_bounds__(kThreads) void read_kernel(const ReadArgs a) {
 
 template <template <class, int> class K, class A>
 hipError_t dispatch(const A& a, int64_t tokens, hipStream_t stream) {
-  const int64_t rows = kThreads / (a.c.head_dim / 8), blocks = (tokens + rows - 1) / rows * 2 * a.c.heads;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  const dim3 g((unsigned)blocks), t(kThreads);
+  const dim3 g((unsigned)copy_blocks(a.c, tokens)), t(kThreads);
   const bool bf = a.c.dtype == QMM_BF16;
   switch (a.c.head_dim) {
     case 64: bf ? K<Bf16, 64>::go(a, g, t, stream) : K<Fp16, 64>::go(a, g, t, stream); break;

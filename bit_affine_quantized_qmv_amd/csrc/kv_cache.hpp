@@ -112,6 +112,15 @@ struct AttendArgs {
   float* part;            // splits > 1: [batch * heads * rows][splits][head_dim] sums, then their (max, sum) pairs
 };
 
+// Append and read: workgroups of one call, each with the rows of one side of one head; a launch
+// has fewer than 2^32 threads along its grid.
+constexpr int kCopyThreads = 256;
+inline int64_t copy_blocks(const CacheArgs& c, int64_t tokens) {
+  const int64_t rows = kCopyThreads / (c.head_dim / 8);
+  return (tokens + rows - 1) / rows * 2 * c.heads;
+}
+constexpr int64_t kMaxCopyBlocks = 0xFFFFFFFFll / kCopyThreads;
+
 hipError_t launch_append(const AppendArgs& a, hipStream_t stream);
 hipError_t launch_read(const ReadArgs& a, hipStream_t stream);
 

@@ -148,6 +148,8 @@ int32_t qmm_kv_append(const qmm_kv_cache_t* cache, const void* k, int64_t k_toke
     const int32_t rc = kv::check_cache(cache, tokens > 0, &a.c);
     if (rc != QMM_OK) return rc;
     if (tokens < 0 || tokens > kv::kMaxInt) return report(QMM_ERR_SHAPE, "kv_append: need 0 <= tokens < 2^31");
+    if (kv::copy_blocks(a.c, tokens) > kv::kMaxCopyBlocks)
+      return report(QMM_ERR_SHAPE, "kv_append: tokens * heads * head_dim must be below 2^34");
     if (k_token_stride < 0 || k_head_stride < 0 || v_token_stride < 0 || v_head_stride < 0)
       return report(QMM_ERR_LAYOUT, "kv_append: negative stride");
     if ((k_token_stride | k_head_stride | v_token_stride | v_head_stride) % 8)
@@ -175,6 +177,8 @@ int32_t qmm_kv_read(const qmm_kv_cache_t* cache, const int32_t* slots, int64_t c
     const int32_t rc = kv::check_cache(cache, count > 0, &a.c);
     if (rc != QMM_OK) return rc;
     if (count < 0 || count > kv::kMaxInt) return report(QMM_ERR_SHAPE, "kv_read: need 0 <= count < 2^31");
+    if (kv::copy_blocks(a.c, count) > kv::kMaxCopyBlocks)
+      return report(QMM_ERR_SHAPE, "kv_read: count * heads * head_dim must be below 2^34");
     if (count == 0) return report(QMM_OK, "");
     if (!k || !v || !slots) return report(QMM_ERR_NULL, "kv_read: k, v and slots must be non-NULL");
     if ((uintptr_t)k % 16 || (uintptr_t)v % 16 || (uintptr_t)slots % 4)

@@ -299,14 +299,16 @@ typedef struct {
  * dtype.  k, v: DEVICE, dtype, element (t, h, d) at t * token_stride + h * head_stride + d;
  * 16-byte aligned, strides >= 0 and multiples of 8; finite values.  slots: DEVICE int32
  * [tokens], distinct; a slot outside [0, pages * page_size) is skipped (nothing is written for
- * it), so negative slots can pad a batch.  tokens == 0 is a no-op.  One kernel is enqueued. */
+ * it), so negative slots can pad a batch.  tokens == 0 is a no-op; tokens * heads * head_dim,
+ * tokens rounded up to 2048 / head_dim, is below 2^34 (the threads of one launch).  One kernel is enqueued. */
 int32_t qmm_kv_append(const qmm_kv_cache_t* cache, const void* k, int64_t k_token_stride, int64_t k_head_stride,
                       const void* v, int64_t v_token_stride, int64_t v_head_stride, const int32_t* slots,
                       int64_t tokens, void* stream);
 
 /* The values the cache stands for at `count` slots: k and v, DEVICE, dense
  * [count, heads, head_dim] of dtype, 16-byte aligned, round(fma(s, q, b)) of each element.  A
- * slot outside [0, pages * page_size) gives NaN rows.  count == 0 is a no-op.  One kernel. */
+ * slot outside [0, pages * page_size) gives NaN rows.  count == 0 is a no-op; count is limited as
+ * qmm_kv_append's tokens are.  One kernel. */
 int32_t qmm_kv_read(const qmm_kv_cache_t* cache, const int32_t* slots, int64_t count, void* k, void* v,
                     void* stream);
 
