@@ -48,6 +48,20 @@ def test_few_tokens_keep_the_stated_bits(length, q_len, rep, dim, group, window,
     check(y, k, v, queries, group, dtype, scale, prompt, window)
 
 
+@pytest.mark.parametrize("length,q_len,rep,dim,group,window,dtype,prompt", [
+    (1, 1, 4, 128, 64, 0, "bf16", False), (1, 1, 4, 128, 64, 0, "fp16", False), (5, 5, 4, 128, 64, 0, "bf16", False),
+    (5, 5, 4, 64, 32, 0, "fp16", False), (700, 4, 4, 128, 64, 3, "bf16", False), (300, 1, 3, 256, 64, 0, "bf16", False),
+    (140, 140, 2, 128, 64, 3, "bf16", True), (140, 140, 2, 128, 128, 3, "fp16", True),
+    (520, 520, 2, 64, 32, 2, "bf16", True), (520, 520, 2, 256, 128, 2, "fp16", True)])
+def test_scores_near_zero_keep_the_stated_bits(length, q_len, rep, dim, group, window, dtype, prompt):
+    """As above with weights that are nearly equal, where the bound is that of the operands."""
+    k, v = (_rows((length, 1, dim), dtype, seed) for seed in (1, 2))
+    queries = _rows((q_len, rep, dim), dtype, 3, loud=False) / 64
+    scale = dim ** -0.5
+    y = attend(k, v, queries, group, dtype, scale, window)
+    check(y, k, v, queries, group, dtype, scale, prompt, window)
+
+
 def dominated(n, dim, dtype, size, gap, seed):
     """Keys, values and a query direction: token 0 has the value 0 and a score `gap` above the
     others', whose values are size * (0.5 + a normal number)."""
