@@ -96,10 +96,12 @@ int64_t part_floats(const AttendArgs& a, int64_t splits) {
 // second: head_dim 128, 8192 tokens, 192 rows 60 us / 67, 256 rows 73 / 66; head_dim 64, 512
 // rows 46 / 50, 1024 rows 87 / 79; head_dim 256, 800 rows 107 / 121, 2048 rows 265 / 246.
 // Splits: as many as make one workgroup per CU in the prompt form and at head_dim 256 (only one
-// is resident: 19 us against 35 with four, 8192 tokens), two with four groups per row (17 us /
-// 20), else four (32 ragged sequences: 53 us against 63 with three; 131071 tokens: 35 us, with
-// six 39); each of at least one step of every wave (128 tokens), or 512 tokens in the prompt
-// form, where a split's sums are large.
+// is resident: 19 us against 35 with four, 8192 tokens), two, as many as are resident, with four
+// groups per row (17 us / 20), else four, which are resident with one group per row.  With two
+// groups three are, and the fourth still pays where lengths differ (32 ragged sequences, 128
+// elements in groups of 64: 53 us against 63 with three); more do not (131071 tokens, one group:
+// 35 us, with six 39).  Each split has at least one step of every wave (128 tokens), or 512 tokens
+// in the prompt form, where a split's sums are large.
 namespace {
 
 struct Shape {

@@ -324,7 +324,7 @@ typedef struct {
                             * 16-byte aligned, strides >= 0 and multiples of 8              */
   int64_t q_batch_stride, q_token_stride, q_head_stride;
   int64_t batch;           /* sequences, at most 65535                                       */
-  int64_t q_len;           /* queries per sequence                                           */
+  int64_t q_len;           /* queries per sequence, below 32768                              */
   int32_t q_heads;         /* a multiple of the cache's heads                                */
   int32_t causal;
   int64_t window;
@@ -376,7 +376,8 @@ typedef struct {
  *     p_e = softmax of the router logits over S_t (renormalize) or over all experts,
  *     y_t = sum_{e in S_t} p_e * ( silu(Wg_e x_t) * (Wu_e x_t) ) Wd_e^T,  silu(g) = g / (1 + exp(-g)).
  * gate, up: [inter, hidden] per expert, sharing bits and group_size; down: [hidden, inter],
- * any bits and group_size.  4- and 8-bit codes: w_packed 16-byte aligned, w_row_stride and
+ * any bits and group_size.  hidden and inter are at most 2^20, the codes of one expert (and of 128
+ * rows more) below 1 GiB.  4- and 8-bit codes: w_packed 16-byte aligned, w_row_stride and
  * w_expert_stride multiples of 4 words; other widths: any word. */
 typedef struct {
   const void* x;               /* DEVICE [tokens, x_stride] of dtype, 16-byte aligned, x_stride % 8 == 0 */
@@ -412,8 +413,10 @@ int64_t qmm_moe_workspace_bytes(int64_t tokens, int64_t experts, int64_t top_k, 
 typedef struct {
   const float* temperature;   /* T; <= 0 or NaN: the first largest logit, whatever u is        */
   const int32_t* top_k;       /* keep the top_k largest; <= 0: all                             */
-  const float* top_p;         /* keep the shortest prefix reaching this share; >= 1: all       */
-  const float* min_p;         /* keep weights of at least min_p times the largest; <= 0: all   */
+  const float* top_p;         /* keep the shortest prefix reaching this share; >= 1: all; NaN,
+                               * like 0, the first largest alone                              */
+  const float* min_p;         /* keep weights of at least min_p times the largest; <= 0: all;
+                               * NaN, like a number above 1, the first largest alone           */
   float temperature_all;
   int32_t top_k_all;
   float top_p_all;
