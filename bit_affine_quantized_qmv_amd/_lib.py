@@ -88,6 +88,49 @@ class KVAttendDesc(ctypes.Structure):
                 ("max_length", ctypes.c_int64)]
 
 
+class TreeAcceptDesc(ctypes.Structure):
+    _fields_ = [("parents", ctypes.c_void_p),
+                ("tokens", ctypes.c_void_p),
+                ("sampled", ctypes.c_void_p),
+                ("parents_stride", ctypes.c_int64),
+                ("tokens_stride", ctypes.c_int64),
+                ("sampled_stride", ctypes.c_int64),
+                ("batch", ctypes.c_int64),
+                ("nodes", ctypes.c_int64)]
+
+
+class KVMoveDesc(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64),
+                ("blocks", ctypes.c_int64),
+                ("to_table", ctypes.c_void_p),
+                ("to_stride", ctypes.c_int64),
+                ("to_blocks", ctypes.c_int64),
+                ("index", ctypes.c_void_p),
+                ("index_stride", ctypes.c_int64),
+                ("batch", ctypes.c_int64),
+                ("count", ctypes.c_int64),
+                ("origin", ctypes.c_void_p),
+                ("start", ctypes.c_void_p)]
+
+
+class KVForkDesc(ctypes.Structure):
+    _fields_ = [("refs", ctypes.c_void_p),
+                ("pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int32),
+                ("block_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64),
+                ("blocks", ctypes.c_int64),
+                ("lengths", ctypes.c_void_p),
+                ("batch", ctypes.c_int64),
+                ("parents", ctypes.c_void_p),
+                ("want", ctypes.c_void_p),
+                ("rows", ctypes.c_int64),
+                ("new_table", ctypes.c_void_p),
+                ("new_stride", ctypes.c_int64),
+                ("new_blocks", ctypes.c_int64)]
+
+
 class ExpertStack(ctypes.Structure):
     _fields_ = [("w", WeightDesc),
                 ("num_experts", ctypes.c_int64),
@@ -185,6 +228,23 @@ def load() -> ctypes.CDLL:
     lib.qmm_kv_attend.argtypes = [ctypes.POINTER(KVCacheDesc), ctypes.POINTER(KVAttendDesc), P, P, ctypes.c_int64, P]
     lib.qmm_kv_attend_workspace_bytes.restype = ctypes.c_int64
     lib.qmm_kv_attend_workspace_bytes.argtypes = [ctypes.POINTER(KVCacheDesc), ctypes.POINTER(KVAttendDesc)]
+    lib.qmm_tree_mask.restype = ctypes.c_int32
+    lib.qmm_tree_mask.argtypes = [P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, P, P, P]
+    lib.qmm_kv_attend_tree.restype = ctypes.c_int32
+    lib.qmm_kv_attend_tree.argtypes = [ctypes.POINTER(KVCacheDesc), ctypes.POINTER(KVAttendDesc), P, P, P, P,
+                                       ctypes.c_int64, P]
+    lib.qmm_kv_attend_tree_workspace_bytes.restype = ctypes.c_int64
+    lib.qmm_kv_attend_tree_workspace_bytes.argtypes = [ctypes.POINTER(KVCacheDesc), ctypes.POINTER(KVAttendDesc)]
+    lib.qmm_tree_accept.restype = ctypes.c_int32
+    lib.qmm_tree_accept.argtypes = [ctypes.POINTER(TreeAcceptDesc), P, P, P, P]
+    lib.qmm_kv_move.restype = ctypes.c_int32
+    lib.qmm_kv_move.argtypes = [ctypes.POINTER(KVCacheDesc), ctypes.POINTER(KVMoveDesc), P]
+    lib.qmm_kv_copy_pages.restype = ctypes.c_int32
+    lib.qmm_kv_copy_pages.argtypes = [ctypes.POINTER(KVCacheDesc), P, P, ctypes.c_int64, P]
+    lib.qmm_kv_fork.restype = ctypes.c_int32
+    lib.qmm_kv_fork.argtypes = [ctypes.POINTER(KVForkDesc), P, P, P, P, ctypes.c_int64, P]
+    lib.qmm_kv_fork_workspace_bytes.restype = ctypes.c_int64
+    lib.qmm_kv_fork_workspace_bytes.argtypes = [ctypes.POINTER(KVForkDesc)]
     lib.qmm_sample.restype = ctypes.c_int32
     lib.qmm_sample.argtypes = [P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                                ctypes.POINTER(SampleParams), P, P, P, P, P]

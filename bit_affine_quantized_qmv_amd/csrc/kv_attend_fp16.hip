@@ -5,7 +5,7 @@ namespace qmm {
 namespace kv {
 
 hipError_t launch_attend_fp16(const AttendArgs& a, const AttendPlan& p, hipStream_t stream) {
-  return launch_attend<Fp16>(a, p, stream);
+  return launch_attend<Fp16, false>(a, p, stream);
 }
 
 }  // namespace kv

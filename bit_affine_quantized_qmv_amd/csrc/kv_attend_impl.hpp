@@ -1,5 +1,6 @@
-// Attention over the 4-bit key/value cache, for one element type (included by
-// kv_attend_bf16.hip and kv_attend_fp16.hip).
+// Attention over the 4-bit key/value cache, for one element type (included by kv_attend_bf16.hip
+// and kv_attend_fp16.hip, and by kv_attend_tree_bf16.hip and kv_attend_tree_fp16.hip for trees of
+// drafted tokens).
 //
 // With k_j = s_jg c_jd + b_jg (codes c, groups g of the head dimension) the score of query q is
 //     q . k_j = sum_g ( s_jg * sum_{d in g} q_d c_jd  +  b_jg * sum_{d in g} q_d ),
@@ -68,6 +69,33 @@ __device__ inline void load_words(uint32_t (&r)[N], const uint32_t* p) {
   }
 }
 
+// What a tree's query sees (TREE): of the tokens before the tree those from row_lo on, of the
+// nodes, which are the sequence's last q_len tokens, those of its mask row.
+struct TreeRow {
+  const uint32_t* mask;
+  int words;
+  bool there;               // the row has a bit: else the query sees nothing
+
+  __device__ inline void setup(const AttendArgs& a, int64_t b, int query) {
+    words = a.mask_words;
+    mask = a.mask + (b * a.q_len + query) * words;
+    uint32_t any = 0u;
+    for (int w = 0; w < words; ++w) any |= mask[w];
+    there = any != 0u;
+  }
+  // Bits of the nodes node .. node + 31; those before the first node and past the words are zero.
+  __device__ inline uint32_t bits(int node) const {
+    const int w = node >> 5;
+    const uint32_t lo = w >= 0 && w < words ? mask[w] : 0u, hi = w + 1 >= 0 && w + 1 < words ? mask[w + 1] : 0u;
+    return (uint32_t)(((((uint64_t)hi) << 32) | lo) >> (node & 31));
+  }
+};
+// A sequence's length is in order: its tree fits in it, or it is empty.
+template <bool TREE>
+__device__ inline bool length_bad(const AttendArgs& a, int len) {
+  return len < 0 || len > a.max_length || (TREE && len > 0 && len < a.q_len);
+}
+
 // One side (K or V) of a 32-token step in registers: codes and (s, b) words of the lane's
 // tokens, for the two 16-token tiles.
 template <int D, int GS>
@@ -110,7 +138,7 @@ __device__ inline void store4(const AttendArgs& a, int64_t b, int head, int spli
 template <int D, int GS>
 constexpr int workgroups() { return D > 128 ? 1 : (D / GS == 1 ? 4 : (D / GS == 2 ? 3 : 2)); }
 
-template <class T, int D, int GS>
+template <class T, int D, int GS, bool TREE>
 __global__ __launch_bounds__(kThreads, (workgroups<D, GS>())) void attend_kernel(const AttendArgs a) {
   constexpr int KC = D / 32;          // 32-element steps of a score; code words per lane and tile
   constexpr int NT = D / 16;          // 16-element output tiles
@@ -128,15 +156,16 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS>())) void attend_kernel
   const int base = row_tile * kRows;
 
   int len = a.lengths[b];
-  const bool bad = len < 0 || len > a.max_length;
+  const bool bad = length_bad<TREE>(a, len);
   if (bad) len = 0;
   // token ranges: [lo_min, hi_max) is seen by some row of the wave, [lo_max, hi_min) by all
   const int off = len - a.q_len;
   const int i_first = base / a.rep, i_last = (min(a.rows, base + kRows) - 1) / a.rep;
-  const int hi_max = a.causal ? max(0, off + i_last + 1) : len;
-  const int hi_min = a.causal ? max(0, off + i_first + 1) : len;
-  const int lo_min = a.window ? max(0, off + i_first - a.window + 1) : 0;
-  const int lo_max = a.window ? max(0, off + i_last - a.window + 1) : 0;
+  // (a tree's rows lie between depth 0 and its number of nodes, whatever their order)
+  const int hi_max = TREE ? len : (a.causal ? max(0, off + i_last + 1) : len);
+  const int hi_min = TREE ? max(0, off) : (a.causal ? max(0, off + i_first + 1) : len);
+  const int lo_min = a.window ? max(0, off + (TREE ? 0 : i_first) - a.window + 1) : 0;
+  const int lo_max = a.window ? max(0, off + (TREE ? a.q_len - 1 : i_last) - a.window + 1) : 0;
   const int c0 = (lo_min & ~(kStep - 1)) + split * a.chunk;
   const int c1 = min(c0 + a.chunk, hi_max);
   const int stride = kStep * kWaves;
@@ -235,8 +264,13 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS>())) void attend_kernel
     for (int c = 0; c < CPG; ++c) d = T::mfma(as_v8<T>(ones), q[g * CPG + c], d);
     qsum[g] = d[0];
   }
-  const int row_hi = a.causal ? off + query + 1 : len;
-  const int row_lo = a.window ? off + query - a.window + 1 : 0;
+  const int row_hi = TREE ? off : (a.causal ? off + query + 1 : len);
+  int row_lo = a.window ? off + query - a.window + 1 : 0;
+  TreeRow tree;
+  if constexpr (TREE) {
+    tree.setup(a, b, query);
+    row_lo = a.window ? off + a.depth[b * a.q_len + query] - a.window + 1 : 0;
+  }
 
   for (int t0 = first; t0 < c1; t0 += stride) {
     const bool bad_now[2] = {bad_next[0], bad_next[1]};
@@ -262,15 +296,17 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS>())) void attend_kernel
     // ---- rows that do not see every token of the step, and tiles without a page of the pool
     if (t0 < lo_max || t0 + kStep > hi_min || bad_now[0] || bad_now[1]) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t nodes = TREE && t0 + kStep > off ? tree.bits(t0 + 16 * i + 4 * h - off) : 0u;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int token = t0 + 16 * i + 4 * h + r;
-          const bool seen = token >= row_lo && token < row_hi;
+          const bool seen = TREE && token >= off ? ((nodes >> r) & 1u) && token < len : token >= row_lo && token < row_hi;
           sc[i][r] = seen ? (bad_now[i] ? __builtin_nanf("") : sc[i][r]) : -__builtin_inff();
 #pragma unroll
           for (int g = 0; g < NG; ++g) vs.sb[i][g][r] = seen ? vs.sb[i][g][r] : 0u;   // whatever it holds, it adds nothing
         }
+      }
     }
     // ---- probabilities
     float top = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3]));
@@ -329,10 +365,6 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS>())) void attend_kernel
   // ---- the lanes' shares of the sums, and the bias term: element d = 16 i + 4 h + r of row col
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
-  if (bad) {
-    l = __builtin_nanf("");
-    m = 0.f;
-  }
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
     bsum[g] += __shfl_xor(bsum[g], 16);
@@ -340,6 +372,16 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS>())) void attend_kernel
   }
 #pragma unroll
   for (int i = 0; i < NT; ++i) acc[i] += bsum[i * 16 / GS];
+  if (TREE && !tree.there) {         // its scores were of tokens that it does not see
+    l = 0.f;
+    m = kNone;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  if (bad) {
+    l = __builtin_nanf("");
+    m = 0.f;
+  }
 
   // ---- the four waves' sums meet in LDS
   __shared__ float o_s[kWaves][kRows][kPitch];
@@ -410,7 +452,7 @@ __device__ inline void split2_near(float x, float y, uint32_t* hi, uint32_t* lo)
 constexpr int row_waves(int head_dim) { return head_dim == 256 ? 8 : 16; }
 constexpr int kUnpackers = 8;
 
-template <class T, int D, int GS>
+template <class T, int D, int GS, bool TREE>
 __global__ __launch_bounds__(64 * row_waves(D), 1) void attend_rows_kernel(const AttendArgs a) {
   constexpr int W = row_waves(D);
   constexpr int KC = D / 32, NT = D / 16, NG = D / GS, CPG = GS / 32;
@@ -434,18 +476,20 @@ __global__ __launch_bounds__(64 * row_waves(D), 1) void attend_rows_kernel(const
   const int wg_base = row_tile * W * kRows, base = wg_base + wave * kRows;
 
   int len = a.lengths[b];
-  const bool bad = len < 0 || len > a.max_length;
+  const bool bad = length_bad<TREE>(a, len);
   if (bad) len = 0;
   const int off = len - a.q_len;
-  const auto row_end = [&](int r) { return a.causal ? max(0, off + r / a.rep + 1) : len; };
-  const auto row_begin = [&](int r) { return a.window ? max(0, off + r / a.rep - a.window + 1) : 0; };
+  // (a tree's rows lie between depth 0 and its number of nodes, whatever their order)
+  const auto row_end = [&](int r) { return TREE || !a.causal ? len : max(0, off + r / a.rep + 1); };
+  const auto row_begin = [&](int r) { return a.window ? max(0, off + (TREE ? 0 : r / a.rep) - a.window + 1) : 0; };
   // ranges of the workgroup, and of this wave (empty for a wave without rows)
   const int wg_last = min(a.rows, wg_base + W * kRows) - 1;
   const int wg_lo = row_begin(wg_base), wg_hi = row_end(wg_last);
   const bool live = base < a.rows;
   const int last = min(a.rows, base + kRows) - 1;
   const int lo_min = live ? row_begin(base) : 0, hi_max = live ? row_end(last) : 0;
-  const int lo_max = live ? row_begin(last) : 0, hi_min = live ? row_end(base) : 0;
+  const int lo_max = !live ? 0 : (!TREE ? row_begin(last) : (a.window ? max(0, len - a.window) : 0));
+  const int hi_min = !live ? 0 : (!TREE ? row_end(base) : max(0, off));
   const int c0 = (wg_lo & ~(kStep - 1)) + split * a.chunk;
   const int c1 = min(c0 + a.chunk, wg_hi);
 
@@ -585,8 +629,13 @@ __global__ __launch_bounds__(64 * row_waves(D), 1) void attend_rows_kernel(const
     for (int c = 0; c < CPG; ++c) d = T::mfma(as_v8<T>(ones), q[g * CPG + c], d);
     qsum[g] = d[0];
   }
-  const int row_hi = a.causal ? off + query + 1 : len;
-  const int row_lo = a.window ? off + query - a.window + 1 : 0;
+  const int row_hi = TREE ? off : (a.causal ? off + query + 1 : len);
+  int row_lo = a.window ? off + query - a.window + 1 : 0;
+  TreeRow tree;
+  if constexpr (TREE) {
+    tree.setup(a, b, query);
+    row_lo = a.window ? off + a.depth[b * a.q_len + query] - a.window + 1 : 0;
+  }
 #pragma unroll
   for (int j = 0; j < NT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
   __syncthreads();                   // the flags are clear
@@ -625,9 +674,14 @@ __global__ __launch_bounds__(64 * row_waves(D), 1) void attend_rows_kernel(const
       }
     if (t0 < lo_max || t0 + kStep > hi_min) {     // rows that do not see every token of the step
 #pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        const int token = t0 + 16 * (n >> 2) + 4 * h + (n & 3);
-        sc[n >> 2][n & 3] = token >= row_lo && token < row_hi ? sc[n >> 2][n & 3] : -__builtin_inff();
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t nodes = TREE && t0 + kStep > off ? tree.bits(t0 + 16 * i + 4 * h - off) : 0u;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int token = t0 + 16 * i + 4 * h + n;
+          const bool seen = TREE && token >= off ? ((nodes >> n) & 1u) && token < len : token >= row_lo && token < row_hi;
+          sc[i][n] = seen ? sc[i][n] : -__builtin_inff();
+        }
       }
     }
     float top = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3]));
@@ -695,6 +749,12 @@ __global__ __launch_bounds__(64 * row_waves(D), 1) void attend_rows_kernel(const
   float* part_ml = a.part + a.batch * a.c.heads * a.rows * a.splits * D;
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
+  if (TREE && !tree.there) {         // its scores were of tokens that it does not see
+    l = 0.f;
+    m = kNone;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
   if (bad) {
     l = __builtin_nanf("");
     m = 0.f;
@@ -711,7 +771,7 @@ __global__ __launch_bounds__(64 * row_waves(D), 1) void attend_rows_kernel(const
 
 // Joins the splits of one query row: o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s.
 // D/4 lanes hold the row's elements, the other lanes of the workgroup further splits.
-template <class T, int D>
+template <class T, int D, bool TREE>
 __global__ __launch_bounds__(kThreads) void attend_join_kernel(const AttendArgs a) {
   constexpr int kLanes = D / 4, kGroups = kThreads / kLanes;
   __shared__ float top_s[kWaves];
@@ -768,36 +828,36 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(const AttendArgs 
   *(uint2*)((uint16_t*)a.out + ((b * a.q_len + i) * (int64_t)a.q_heads + head * a.rep + g) * D + 4 * lane) = u;
 }
 
-template <class T, int D, int GS>
+template <class T, int D, int GS, bool TREE>
 hipError_t launch_shape(const AttendArgs& a, const AttendPlan& p, hipStream_t stream) {
   // Workgroups go to the eight XCDs in turn, x fastest.  Of sequences of unequal length only the
   // longest have work in the last splits, so splits are the slowest index: with splits fastest
   // (4 of them), two XCDs had every first split.
   const dim3 grid((unsigned)(a.c.heads * p.row_tiles), (unsigned)a.batch, (unsigned)p.splits);
   if (p.by_rows)
-    hipLaunchKernelGGL((attend_rows_kernel<T, D, GS>), grid, dim3(64 * row_waves(D)), 0, stream, a);
+    hipLaunchKernelGGL((attend_rows_kernel<T, D, GS, TREE>), grid, dim3(64 * row_waves(D)), 0, stream, a);
   else
-    hipLaunchKernelGGL((attend_kernel<T, D, GS>), grid, dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL((attend_kernel<T, D, GS, TREE>), grid, dim3(kThreads), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  hipLaunchKernelGGL((attend_join_kernel<T, D>), dim3((unsigned)(a.batch * a.c.heads * a.rows)), dim3(kThreads), 0,
+  hipLaunchKernelGGL((attend_join_kernel<T, D, TREE>), dim3((unsigned)(a.batch * a.c.heads * a.rows)), dim3(kThreads), 0,
                      stream, a);
   return hipGetLastError();
 }
 
-template <class T>
+template <class T, bool TREE>
 hipError_t launch_attend(const AttendArgs& a, const AttendPlan& p, hipStream_t stream) {
   const int gs = a.c.group_size;
   switch (a.c.head_dim) {
-    case 64: return gs == 32 ? launch_shape<T, 64, 32>(a, p, stream) : launch_shape<T, 64, 64>(a, p, stream);
+    case 64: return gs == 32 ? launch_shape<T, 64, 32, TREE>(a, p, stream) : launch_shape<T, 64, 64, TREE>(a, p, stream);
     case 128:
-      return gs == 32   ? launch_shape<T, 128, 32>(a, p, stream)
-             : gs == 64 ? launch_shape<T, 128, 64>(a, p, stream)
-                        : launch_shape<T, 128, 128>(a, p, stream);
+      return gs == 32   ? launch_shape<T, 128, 32, TREE>(a, p, stream)
+             : gs == 64 ? launch_shape<T, 128, 64, TREE>(a, p, stream)
+                        : launch_shape<T, 128, 128, TREE>(a, p, stream);
     case 256:
-      return gs == 32   ? launch_shape<T, 256, 32>(a, p, stream)
-             : gs == 64 ? launch_shape<T, 256, 64>(a, p, stream)
-                        : launch_shape<T, 256, 128>(a, p, stream);
+      return gs == 32   ? launch_shape<T, 256, 32, TREE>(a, p, stream)
+             : gs == 64 ? launch_shape<T, 256, 64, TREE>(a, p, stream)
+                        : launch_shape<T, 256, 128, TREE>(a, p, stream);
     default: return hipErrorInvalidValue;
   }
 }

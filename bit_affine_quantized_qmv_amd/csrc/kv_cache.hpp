@@ -72,6 +72,10 @@ struct CacheArgs {
   int32_t dtype;
 };
 
+// Validate a cache descriptor and fill `out` (host only; the data pointer when `pointers`).
+constexpr int64_t kMaxInt = 0x7FFFFFFF;
+int32_t check_cache(const qmm_kv_cache_t* c, bool pointers, CacheArgs* out);
+
 struct AppendArgs {
   CacheArgs c;
   const void* x[2];     // K and V rows
@@ -109,6 +113,9 @@ struct AttendArgs {
   int32_t splits;
   void* out;              // dense [batch, q_len, q_heads, head_dim]
   uint64_t page_recip;    // page_recip(page_size)
+  const uint32_t* mask;   // trees: [batch, q_len, mask_words], the nodes that a query sees
+  int32_t mask_words;
+  const int32_t* depth;   // trees with a window: [batch, q_len]
   float* part;            // splits > 1: [batch * heads * rows][splits][head_dim] sums, then their (max, sum) pairs
 };
 
@@ -135,6 +142,8 @@ AttendPlan plan_attend(int64_t batch, const CacheArgs& c, int64_t rows, int64_t 
 
 hipError_t launch_attend_bf16(const AttendArgs& a, const AttendPlan& p, hipStream_t stream);
 hipError_t launch_attend_fp16(const AttendArgs& a, const AttendPlan& p, hipStream_t stream);
+hipError_t launch_attend_tree_bf16(const AttendArgs& a, const AttendPlan& p, hipStream_t stream);
+hipError_t launch_attend_tree_fp16(const AttendArgs& a, const AttendPlan& p, hipStream_t stream);
 
 }  // namespace kv
 }  // namespace qmm

@@ -5,13 +5,10 @@
 #include <string>
 
 #include "capi_internal.hpp"
-#include "kv_cache.hpp"
+#include "kv_pages.hpp"
 
 namespace qmm {
 namespace kv {
-namespace {
-
-constexpr int64_t kMaxInt = 0x7FFFFFFF;
 
 int32_t check_cache(const qmm_kv_cache_t* c, bool pointers, CacheArgs* out) {
   if (!c) return report(QMM_ERR_NULL, "kv: cache must be non-NULL");
@@ -36,6 +33,8 @@ int32_t check_cache(const qmm_kv_cache_t* c, bool pointers, CacheArgs* out) {
                    c->group_size, c->dtype};
   return QMM_OK;
 }
+
+namespace {
 
 int32_t check_attend(const qmm_kv_cache_t* cache, const qmm_kv_attend_t* q, bool pointers, AttendArgs* a) {
   const int32_t rc = check_cache(cache, pointers, &a->c);
@@ -135,6 +134,44 @@ static int64_t most_splits(const AttendArgs& a) {
   return std::min<int64_t>(s.want, std::max<int64_t>(1, (a.max_length + s.step - 1) / s.step));
 }
 
+// check_attend for a tree: its queries are its nodes.
+static int32_t check_tree(const qmm_kv_cache_t* cache, const qmm_kv_attend_t* q, bool pointers, AttendArgs* a) {
+  const int32_t rc = check_attend(cache, q, pointers, a);
+  if (rc != QMM_OK) return rc;
+  if (!q->causal) return report(QMM_ERR_UNSUPPORTED, "kv_attend_tree: causal must be set");
+  if (q->q_len > kMaxNodes)
+    return report(QMM_ERR_SHAPE, "kv_attend_tree: " + std::to_string(q->q_len) + " nodes, at most " + std::to_string(kMaxNodes));
+  return QMM_OK;
+}
+
+// Plans and launches a checked call; with a.mask a tree's.
+static int32_t run_attend(AttendArgs& a, void* out, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+  if (!a.q || !out || !a.lengths || (a.max_length > 0 && !a.table))
+    return report(QMM_ERR_NULL, "kv_attend: q, out, lengths and block_table must be non-NULL");
+  if ((uintptr_t)a.q % 16 || (uintptr_t)out % 16 || (uintptr_t)workspace % 16)
+    return report(QMM_ERR_ALIGN, "kv_attend: q, out and workspace must be 16-byte aligned");
+  if ((uintptr_t)a.table % 4 || (uintptr_t)a.lengths % 4)
+    return report(QMM_ERR_ALIGN, "kv_attend: block_table and lengths must be 4-byte aligned");
+  const AttendPlan p =
+      plan_attend(a.batch, a.c, a.rows, token_range(a));
+  if ((int64_t)a.c.heads * p.row_tiles > 65535)
+    return report(QMM_ERR_SHAPE, "kv_attend: too many query rows per sequence");
+  const int64_t need = part_floats(a, p.splits) * 4;
+  if (need > 0 && !workspace) return report(QMM_ERR_NULL, "kv_attend: workspace must be non-NULL");
+  if (workspace_bytes < need)
+    return report(QMM_ERR_SHAPE, "kv_attend: workspace of " + std::to_string(workspace_bytes) + " bytes, needs " +
+                                     std::to_string(need));
+  a.page_recip = page_recip(a.c.page_size);
+  a.chunk = p.chunk;
+  a.splits = p.splits;
+  a.out = out;
+  a.part = (float*)workspace;
+  if (a.mask)
+    return report_launch(a.c.dtype == QMM_BF16 ? launch_attend_tree_bf16(a, p, stream)
+                                               : launch_attend_tree_fp16(a, p, stream));
+  return report_launch(a.c.dtype == QMM_BF16 ? launch_attend_bf16(a, p, stream) : launch_attend_fp16(a, p, stream));
+}
+
 }  // namespace kv
 }  // namespace qmm
 
@@ -211,28 +248,36 @@ int32_t qmm_kv_attend(const qmm_kv_cache_t* cache, const qmm_kv_attend_t* args, 
     const int32_t rc = kv::check_attend(cache, args, !empty, &a);
     if (rc != QMM_OK) return rc;
     if (empty) return report(QMM_OK, "");
-    if (!a.q || !out || !a.lengths || (a.max_length > 0 && !a.table))
-      return report(QMM_ERR_NULL, "kv_attend: q, out, lengths and block_table must be non-NULL");
-    if ((uintptr_t)a.q % 16 || (uintptr_t)out % 16 || (uintptr_t)workspace % 16)
-      return report(QMM_ERR_ALIGN, "kv_attend: q, out and workspace must be 16-byte aligned");
-    if ((uintptr_t)a.table % 4 || (uintptr_t)a.lengths % 4)
-      return report(QMM_ERR_ALIGN, "kv_attend: block_table and lengths must be 4-byte aligned");
-    const kv::AttendPlan p =
-        kv::plan_attend(a.batch, a.c, a.rows, kv::token_range(a));
-    if ((int64_t)a.c.heads * p.row_tiles > 65535)
-      return report(QMM_ERR_SHAPE, "kv_attend: too many query rows per sequence");
-    const int64_t need = kv::part_floats(a, p.splits) * 4;
-    if (need > 0 && !workspace) return report(QMM_ERR_NULL, "kv_attend: workspace must be non-NULL");
-    if (workspace_bytes < need)
-      return report(QMM_ERR_SHAPE, "kv_attend: workspace of " + std::to_string(workspace_bytes) + " bytes, needs " +
-                                       std::to_string(need));
-    a.page_recip = kv::page_recip(a.c.page_size);
-    a.chunk = p.chunk;
-    a.splits = p.splits;
-    a.out = out;
-    a.part = (float*)workspace;
-    hipStream_t s = (hipStream_t)stream;
-    return report_launch(a.c.dtype == QMM_BF16 ? kv::launch_attend_bf16(a, p, s) : kv::launch_attend_fp16(a, p, s));
+    return kv::run_attend(a, out, workspace, workspace_bytes, (hipStream_t)stream);
+  });
+}
+
+int64_t qmm_kv_attend_tree_workspace_bytes(const qmm_kv_cache_t* cache, const qmm_kv_attend_t* args) {
+  return guarded([&]() -> int64_t {
+    kv::AttendArgs a{};
+    const int32_t rc = kv::check_tree(cache, args, false, &a);
+    if (rc != QMM_OK) return rc;
+    report(QMM_OK, "");
+    return kv::part_floats(a, kv::most_splits(a)) * 4;
+  });
+}
+
+int32_t qmm_kv_attend_tree(const qmm_kv_cache_t* cache, const qmm_kv_attend_t* args, const uint32_t* mask,
+                           const int32_t* depth, void* out, void* workspace, int64_t workspace_bytes, void* stream) {
+  return guarded([&]() -> int32_t {
+    kv::AttendArgs a{};
+    const bool empty = args && (args->batch == 0 || args->q_len == 0);
+    const int32_t rc = kv::check_tree(cache, args, !empty, &a);
+    if (rc != QMM_OK) return rc;
+    if (empty) return report(QMM_OK, "");
+    if (!mask || (a.window && !depth))
+      return report(QMM_ERR_NULL, "kv_attend_tree: mask, and depth with a window, must be non-NULL");
+    if ((uintptr_t)mask % 4 || (uintptr_t)depth % 4)
+      return report(QMM_ERR_ALIGN, "kv_attend_tree: mask and depth must be 4-byte aligned");
+    a.mask = mask;
+    a.mask_words = (a.q_len + 31) / 32;
+    a.depth = depth;
+    return kv::run_attend(a, out, workspace, workspace_bytes, (hipStream_t)stream);
   });
 }
 

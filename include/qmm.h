@@ -360,6 +360,123 @@ int32_t qmm_kv_attend(const qmm_kv_cache_t* cache, const qmm_kv_attend_t* args, 
  * one, with any window. */
 int64_t qmm_kv_attend_workspace_bytes(const qmm_kv_cache_t* cache, const qmm_kv_attend_t* args);
 
+/* ---- Trees of drafted tokens, and the pages of the cache.
+ * A tree of a sequence has `nodes` nodes; parents[i] is node i's parent, an earlier node
+ * (0 <= parents[i] < i), or -1 for a root.  Anything else there means that i is no node (padding
+ * of a smaller tree), and so are its descendants.  The nodes are the last `nodes` tokens of the
+ * sequence: node i is appended at position c + i, c = length - nodes, and stands for position
+ * c + depth(i) of the text (depth 0: a root). */
+#define QMM_TREE_MAX_NODES 1024
+
+/* Which nodes a node sees, once per tree for every layer: bit j of the row of node i
+ * ([batch, nodes, ceil(nodes / 32)] words, bit j % 32 of word j / 32) is set for i itself and its
+ * ancestors, with window > 0 for the nearest `window` of them.  The row of what is no node is zero.
+ * depth: [batch, nodes], the number of ancestors (0 for what is no node), or NULL.  parents:
+ * DEVICE int32 [batch, parents_stride].  mask, depth: DEVICE, dense, 4-byte aligned.  batch at most
+ * 65535; batch == 0 or nodes == 0 is a no-op.  One kernel. */
+int32_t qmm_tree_mask(const int32_t* parents, int64_t parents_stride, int64_t batch, int64_t nodes, int64_t window,
+                      uint32_t* mask, int32_t* depth, void* stream);
+
+/* Attention of a tree's nodes over the cache: qmm_kv_attend (arguments, arithmetic, limits,
+ * workspace), except for what a query sees.  Query i is node i of its sequence's tree; it sees the
+ * tokens j < c before the tree, with a window only j > c + depth[i] - window, and the nodes of its
+ * row of `mask`; a row of zeros sees nothing and gives zeros.  mask and depth (read with a window
+ * only, which may then not be NULL) are qmm_tree_mask's for this batch and q_len = nodes at most
+ * QMM_TREE_MAX_NODES, or the caller's own; a window is applied to a mask by qmm_tree_mask.  causal
+ * must be set.  A length of zero gives zeros; another one below q_len, like one above max_length,
+ * makes the sequence's outputs NaN. */
+int32_t qmm_kv_attend_tree(const qmm_kv_cache_t* cache, const qmm_kv_attend_t* args, const uint32_t* mask,
+                           const int32_t* depth, void* out, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Host-only: workspace bytes of a qmm_kv_attend_tree call, as qmm_kv_attend_workspace_bytes. */
+int64_t qmm_kv_attend_tree_workspace_bytes(const qmm_kv_cache_t* cache, const qmm_kv_attend_t* args);
+
+/* The path that verification accepts.  tokens[i] is the token that node i drafts, sampled[i] the
+ * one that the model draws after it.  The path starts with node 0 (a root: a token that is already
+ * certain) and goes on to the lowest child i of its last node l with tokens[i] == sampled[l].
+ * path: DEVICE int32 [batch, nodes], its nodes in order, then -1; count: [batch], their number;
+ * last: [batch], what is sampled after the path's end, the next certain token.  Where node 0 is no
+ * root: count 0, last -1.  At least one node, batch at most 65535; batch == 0 is a no-op.  One
+ * kernel. */
+typedef struct {
+  const int32_t* parents;   /* DEVICE int32 [batch, stride] each, 4-byte aligned */
+  const int32_t* tokens;
+  const int32_t* sampled;
+  int64_t parents_stride, tokens_stride, sampled_stride;
+  int64_t batch;
+  int64_t nodes;
+} qmm_tree_accept_t;
+int32_t qmm_tree_accept(const qmm_tree_accept_t* args, int32_t* path, int32_t* count, int32_t* last, void* stream);
+
+/* Move cached rows of a sequence, as they are: the K and V rows of every head at position
+ * origin[n] + index[n, i] of sequence n go to position start[n] + i.  Entries whose index is
+ * negative, or whose positions are negative or have no page in [0, pages), move nothing.
+ * Without to_table the rows stay in the sequence's pages (a path's rows moved up to the tree's
+ * first position; kept rows moved together): the indices that move must then ascend and no row may
+ * move up, origin[n] + index[n, i] >= start[n] + i; every row arrives as it was before the call.
+ * With to_table they go to the pages that it names, none of which the call may read.  Pages that
+ * are written belong to one sequence. */
+typedef struct {
+  const int32_t* block_table;   /* DEVICE int32 [batch, table_stride], as in qmm_kv_attend */
+  int64_t table_stride, blocks;
+  const int32_t* to_table;      /* DEVICE int32 [batch, to_stride], or NULL                */
+  int64_t to_stride, to_blocks;
+  const int32_t* index;         /* DEVICE int32 [batch, index_stride]                      */
+  int64_t index_stride;
+  int64_t batch;                /* at most 65535, batch * heads below 2^24                 */
+  int64_t count;                /* entries per sequence, at most 2^30                      */
+  const int32_t* origin;        /* DEVICE int32 [batch], or NULL: 0                        */
+  const int32_t* start;         /* DEVICE int32 [batch], >= 0                              */
+} qmm_kv_move_t;
+/* batch == 0 or count == 0 is a no-op.  One kernel. */
+int32_t qmm_kv_move(const qmm_kv_cache_t* cache, const qmm_kv_move_t* args, void* stream);
+
+/* Copy pages src[i] to dst[i], all heads, i < count.  A pair with a page outside [0, pages) is
+ * skipped.  The dst are distinct and no src.  DEVICE int32 [count]; count == 0 is a no-op.  One
+ * kernel. */
+int32_t qmm_kv_copy_pages(const qmm_kv_cache_t* cache, const int32_t* src, const int32_t* dst, int64_t count,
+                          void* stream);
+
+/* One step of a program's block tables: beams and samples that continue one sequence, sequences
+ * that begin, grow or are cut back, and those that end.  refs[p] counts the entries of the
+ * program's tables that name page p; 0: the page is free.  The old table (batch rows) is replaced
+ * by the new one (rows rows): row i continues row parents[i], or begins empty if that is outside
+ * [0, batch).  It keeps the first min(length, want) tokens and has room for want[i] (NULL: the
+ * parent's length); with s = page_size
+ *   - blocks of which every token stays name the old page, which all such rows share;
+ *   - the block that is kept in part, and those after it up to ceil(want / s), go to the first row
+ *     (lowest i) of a parent where its old page is held by nobody else (refs 1); otherwise they get
+ *     fresh pages: entry number k of these, by row and block, gets the k-th lowest page that was
+ *     free before the call.  Rows of a fresh page for a block kept in part are to be copied:
+ *     copy_src[i] -> copy_dst[i] with qmm_kv_copy_pages, for each layer's cache (-1: nothing);
+ *   - other entries are -1, and so are those for which no page is left or new_blocks is too small:
+ *     *short_of counts these (of each row at most 16384 past new_blocks).
+ * refs is brought up to date: pages that only old rows named become free for the next call.
+ * Entries outside [0, pages) name no page.  new_table must not overlap the old one.
+ * copy_src, copy_dst: DEVICE int32 [rows]; short_of: DEVICE int32 [1]; workspace: DEVICE, 4-byte
+ * aligned, qmm_kv_fork_workspace_bytes(args) bytes of any content; one serves any number of calls
+ * in stream order.  Three kernels.  batch, rows <= 65535; rows * new_blocks <= 2^30; the limits of
+ * pages and page_size are the cache's. */
+typedef struct {
+  int32_t* refs;                /* DEVICE int32 [pages]                                    */
+  int64_t pages;
+  int32_t page_size;
+  const int32_t* block_table;   /* DEVICE int32 [batch, table_stride]                      */
+  int64_t table_stride, blocks;
+  const int32_t* lengths;       /* DEVICE int32 [batch]; negative counts as 0              */
+  int64_t batch;
+  const int32_t* parents;       /* DEVICE int32 [rows]                                     */
+  const int32_t* want;          /* DEVICE int32 [rows] or NULL; negative counts as 0       */
+  int64_t rows;
+  int32_t* new_table;           /* DEVICE int32 [rows, new_stride]                         */
+  int64_t new_stride, new_blocks;
+} qmm_kv_fork_t;
+int32_t qmm_kv_fork(const qmm_kv_fork_t* args, int32_t* copy_src, int32_t* copy_dst, int32_t* short_of, void* workspace,
+                    int64_t workspace_bytes, void* stream);
+
+/* Host-only: workspace bytes of a qmm_kv_fork call (its pointers may be NULL), or a negative error code. */
+int64_t qmm_kv_fork_workspace_bytes(const qmm_kv_fork_t* args);
+
 /* ---- A mixture-of-experts layer for a few tokens.
  * Expert stack: num_experts quantized weights that share N, K, group_size, bits and dtype
  * (w describes expert 0; expert e's codes are w_expert_stride words further, its scales and
