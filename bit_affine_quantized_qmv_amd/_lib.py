@@ -252,6 +252,15 @@ def load() -> ctypes.CDLL:
     lib.qmm_moe.argtypes = [ctypes.POINTER(MoeDesc), P, P, ctypes.c_int64, P]
     lib.qmm_moe_workspace_bytes.restype = ctypes.c_int64
     lib.qmm_moe_workspace_bytes.argtypes = [ctypes.c_int64] * 5
+    lib.qmm_moe_prompt.restype = ctypes.c_int32
+    lib.qmm_moe_prompt.argtypes = [ctypes.POINTER(MoeDesc), P, P, ctypes.c_int64, P]
+    lib.qmm_moe_prompt_workspace_bytes.restype = ctypes.c_int64
+    lib.qmm_moe_prompt_workspace_bytes.argtypes = [ctypes.c_int64] * 5
+    lib.qmm_grouped.restype = ctypes.c_int32
+    lib.qmm_grouped.argtypes = [P, ctypes.c_int64, ctypes.c_int64, ctypes.POINTER(ExpertStack), P, P, ctypes.c_int64, P,
+                                ctypes.c_int64, P]
+    lib.qmm_grouped_workspace_bytes.restype = ctypes.c_int64
+    lib.qmm_grouped_workspace_bytes.argtypes = [ctypes.c_int64, ctypes.POINTER(ExpertStack)]
     _lib = lib
     return lib
 

@@ -1,0 +1,105 @@
+// Launch interface of the matrix products grouped by expert, and of the expert layer built on them.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "moe.hpp"
+
+namespace qmm {
+namespace grouped {
+
+using moe::Stack;
+
+constexpr int kThreads = 256;
+constexpr int kBlockN = 256;          // weight rows per workgroup: four waves of four 16-row tiles
+constexpr int kStepK = 128;           // columns between two barriers
+constexpr int kPlanes = 3;            // bfloat16 parts of a group's sum of activations
+constexpr int kSumPad = 32;           // groups per row of the sums, rounded up to this
+constexpr int kMaxPairs = 1 << 20;    // rows of one call
+
+// What becomes of a product x W_e^T.
+enum Kind {
+  kPlain,      // y, rounded to dtype
+  kGated,      // two products (gate, up): h = silu(g) u in two bfloat16 parts, and the sums of its groups
+  kDown,       // x in two parts; float32, to the row of the (token, choice) pair
+};
+
+// Up to `rows` consecutive rows of one expert.
+struct Tile {
+  int32_t expert;
+  int32_t first;
+  int32_t rows;
+  int32_t unused;
+};
+
+struct Args {
+  const uint16_t* x;         // row r at r * x_stride, its rest (kDown) x_plane further
+  int64_t x_stride;
+  int64_t x_plane;
+  uint32_t x_bytes;          // kGated: bytes of all rows, below 2^31
+  const uint16_t* sums;      // [x row][kPlanes][sum_groups]
+  int32_t sum_groups;
+  Stack w[2];                // kGated: gate and up; else twice the same
+  int32_t n, k;
+  const Tile* tiles;
+  const int32_t* tile_count;
+  int32_t max_tiles;
+  int32_t n_blocks;
+  const int32_t* pairs;      // kGated, kDown: pair (token * top_k + choice) of a row
+  int32_t top_k;
+  uint16_t* y;               // kPlain
+  int64_t y_stride;
+  uint16_t* h;               // kGated: [row][2][h_cols]
+  int32_t h_cols;
+  uint16_t* h_sums;          // kGated: [row][kPlanes][h_sum_groups]
+  int32_t h_sum_groups;
+  int32_t h_group;
+  float* out;                // kDown: [pair][n]
+};
+
+// Sums of x's groups and the tiles of a grouped product: one kernel.
+struct PrepareArgs {
+  const uint16_t* x;
+  int64_t x_stride;
+  int64_t rows;
+  int32_t k;
+  int32_t group;
+  int32_t dtype;
+  uint16_t* sums;            // [rows][kPlanes][sum_groups]
+  int32_t sum_groups;
+  int32_t experts;
+  const int32_t* offsets;    // [experts + 1]; null: no tiles are made
+  int32_t tile_rows;
+  Tile* tiles;
+  int32_t max_tiles;
+  int32_t* tile_count;
+};
+
+// Routing of the expert layer: each token's choices, then the rows of every expert.
+struct RouteArgs {
+  const uint16_t* router;
+  int64_t router_stride;
+  int32_t tokens;
+  int32_t experts;
+  int32_t top_k;
+  int32_t renormalize;
+  int32_t dtype;
+  int32_t* pair_expert;      // [tokens * top_k]
+  float* pair_share;
+  int32_t* pairs;            // [tokens * top_k]: pair of each row, by expert
+  int32_t tile_rows;
+  Tile* tiles;
+  int32_t max_tiles;
+  int32_t* tile_count;
+};
+
+hipError_t launch_prepare(const PrepareArgs& a, hipStream_t stream);
+hipError_t launch_route(const RouteArgs& r, const PrepareArgs& p, hipStream_t stream);
+// tile_rows: 32 or 64
+hipError_t launch_b4(const Args& a, Kind kind, int dtype, int tile_rows, hipStream_t stream);
+hipError_t launch_b8(const Args& a, Kind kind, int dtype, int tile_rows, hipStream_t stream);
+hipError_t launch_bn(const Args& a, Kind kind, int dtype, int tile_rows, hipStream_t stream);
+
+}  // namespace grouped
+}  // namespace qmm

@@ -1,0 +1,298 @@
+// extern "C" entry points of the products grouped by expert: validate, plan, launch.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <string>
+
+#include "capi_internal.hpp"
+#include "dispatch.hpp"
+#include "grouped.hpp"
+
+namespace qmm {
+namespace grouped {
+namespace {
+
+int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
+int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// Rows per tile: 64 or 32.  A tile is a pass over its expert's weights, so the taller one where an
+// expert has more than 32 rows on average.
+int tile_rows_of(int64_t rows, int64_t experts) { return rows > 32 * experts ? 64 : 32; }
+// Tiles at most: a part of a tile for each expert with rows.
+int64_t max_tiles_of(int64_t rows, int64_t experts) {
+  return rows / 32 + std::min(rows, experts);
+}
+
+int64_t sum_groups_of(int64_t k, int64_t group) { return round_up(k / group, kSumPad); }
+// Bytes of the sums of `rows` rows, whatever the group size.
+int64_t sums_bytes(int64_t rows, int64_t k) { return align256(rows * kPlanes * 2 * round_up((k + 31) / 32, kSumPad)); }
+int64_t tiles_bytes(int64_t rows, int64_t experts) {
+  return align256(16) + align256(max_tiles_of(rows, experts) * (int64_t)sizeof(Tile));
+}
+
+hipError_t launch(const Args& a, Kind kind, int dtype, int tile_rows, hipStream_t s) {
+  const int bits = a.w[0].bits;
+  return bits == 4 ? launch_b4(a, kind, dtype, tile_rows, s)
+                   : (bits == 8 ? launch_b8(a, kind, dtype, tile_rows, s) : launch_bn(a, kind, dtype, tile_rows, s));
+}
+
+// The kernels address a workgroup's weight rows, some past the last, with 32-bit byte offsets.
+int32_t check_rows(const char* who, const Stack& k, int64_t n) {
+  if ((n + kBlockN) * k.w_row_stride * 4 >= (1ll << 31) || (n + kBlockN) * k.sb_row_stride * 2 >= (1ll << 31))
+    return report(QMM_ERR_SHAPE, std::string(who) + ": one expert's codes must be smaller than 1 GiB");
+  return QMM_OK;
+}
+
+int32_t check_grouped(int64_t rows, const qmm_expert_stack_t* w, bool pointers, Stack* out) {
+  if (!w) return report(QMM_ERR_NULL, "grouped: weights must be non-NULL");
+  if (rows < 0 || rows > kMaxPairs) return report(QMM_ERR_SHAPE, "grouped: need 0 <= rows <= 2^20");
+  if (w->num_experts < 1 || w->num_experts > moe::kMaxExperts)
+    return report(QMM_ERR_SHAPE, "grouped: need 1 <= experts <= 512");
+  if (w->w.N < 1 || w->w.N > (1 << 20) || w->w.K < 1 || w->w.K > (1 << 20))
+    return report(QMM_ERR_SHAPE, "grouped: need 1 <= N, K <= 2^20");
+  if (!pointers) return QMM_OK;
+  int32_t rc = moe::check_stack("grouped", w, w->w.N, w->w.K, (int32_t)w->num_experts, w->w.dtype, out);
+  if (rc == QMM_OK) rc = check_rows("grouped", *out, w->w.N);
+  return rc;
+}
+
+int32_t check_sizes(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, int64_t inter) {
+  if (tokens < 0 || tokens > 65535) return report(QMM_ERR_SHAPE, "moe_prompt: need 0 <= tokens <= 65535");
+  if (experts < 1 || experts > moe::kMaxExperts) return report(QMM_ERR_SHAPE, "moe_prompt: need 1 <= experts <= 512");
+  if (top_k < 1 || top_k > moe::kMaxTopK || top_k > experts)
+    return report(QMM_ERR_SHAPE, "moe_prompt: need 1 <= top_k <= min(experts, 32)");
+  if (tokens * top_k > kMaxPairs) return report(QMM_ERR_SHAPE, "moe_prompt: tokens * top_k must be at most 2^20");
+  if (hidden < 1 || hidden > (1 << 20) || inter < 1 || inter > (1 << 20))
+    return report(QMM_ERR_SHAPE, "moe_prompt: need 1 <= hidden, inter <= 2^20");
+  return QMM_OK;
+}
+
+// Workspace of the layer, in this order.
+struct LayerBytes {
+  int64_t expert, share, pairs, tiles, sums, h, h_sums, out;
+  int64_t all() const { return expert + share + pairs + tiles + sums + h + h_sums + out; }
+};
+LayerBytes layer_bytes(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, int64_t inter) {
+  const int64_t n = tokens * top_k, cols = round_up(inter, kStepK);
+  return LayerBytes{align256(4 * n),          align256(4 * n),         align256(4 * n), tiles_bytes(n, experts),
+                    sums_bytes(tokens, hidden), align256(4 * n * cols), sums_bytes(n, cols), align256(4 * n * hidden)};
+}
+
+}  // namespace
+}  // namespace grouped
+}  // namespace qmm
+
+using namespace qmm;
+
+extern "C" {
+
+int64_t qmm_grouped_workspace_bytes(int64_t rows, const qmm_expert_stack_t* w) {
+  return guarded([&]() -> int64_t {
+    const int32_t rc = grouped::check_grouped(rows, w, false, nullptr);
+    if (rc != QMM_OK) return rc;
+    report(QMM_OK, "");
+    return grouped::tiles_bytes(rows, w->num_experts) + grouped::sums_bytes(rows, w->w.K);
+  });
+}
+
+int32_t qmm_grouped(const void* x, int64_t x_stride, int64_t rows, const qmm_expert_stack_t* weights,
+                    const int32_t* offsets, void* y, int64_t y_stride, void* workspace, int64_t workspace_bytes,
+                    void* stream) {
+  return guarded([&]() -> int32_t {
+    grouped::Args a{};
+    const int32_t rc = grouped::check_grouped(rows, weights, true, &a.w[0]);
+    if (rc != QMM_OK) return rc;
+    const int64_t n = weights->w.N, k = weights->w.K;
+    if (x_stride < 0 || y_stride < 0) return report(QMM_ERR_LAYOUT, "grouped: negative stride");
+    if (x_stride % 8) return report(QMM_ERR_ALIGN, "grouped: x_stride must be a multiple of 8 elements");
+    if (x_stride > (1 << 23)) return report(QMM_ERR_SHAPE, "grouped: x_stride must be at most 2^23");
+    if (rows > 1 && y_stride < n) return report(QMM_ERR_SHAPE, "grouped: y_stride < N");
+    if (rows == 0) return report(QMM_OK, "");
+    if (!x || !offsets || !y || !workspace)
+      return report(QMM_ERR_NULL, "grouped: x, offsets, y and workspace must be non-NULL");
+    if ((uintptr_t)x % 16 || (uintptr_t)workspace % 16 || (uintptr_t)offsets % 4 || (uintptr_t)y % 2)
+      return report(QMM_ERR_ALIGN, "grouped: x and workspace must be 16-byte, offsets 4-byte, y 2-byte aligned");
+    const int64_t experts = weights->num_experts;
+    const int64_t tiles_bytes = grouped::tiles_bytes(rows, experts), need = tiles_bytes + grouped::sums_bytes(rows, k);
+    if (workspace_bytes < need)
+      return report(QMM_ERR_SHAPE, "grouped: workspace of " + std::to_string(workspace_bytes) + " bytes, needs " +
+                                       std::to_string(need));
+    const int tile_rows = grouped::tile_rows_of(rows, experts);
+    char* ws = (char*)workspace;
+    grouped::PrepareArgs p{};
+    p.x = (const uint16_t*)x;
+    p.x_stride = x_stride;
+    p.rows = rows;
+    p.k = (int32_t)k;
+    p.group = weights->w.group_size;
+    p.dtype = weights->w.dtype;
+    p.sums = (uint16_t*)(ws + tiles_bytes);
+    p.sum_groups = (int32_t)grouped::sum_groups_of(k, p.group);
+    p.experts = (int32_t)experts;
+    p.offsets = offsets;
+    p.tile_rows = tile_rows;
+    p.tile_count = (int32_t*)ws;
+    p.tiles = (grouped::Tile*)(ws + grouped::align256(16));
+    p.max_tiles = (int32_t)(rows / tile_rows + std::min(rows, experts));
+    a.w[1] = a.w[0];
+    a.x = p.x;
+    a.x_stride = x_stride;
+    a.sums = p.sums;
+    a.sum_groups = p.sum_groups;
+    a.n = (int32_t)n;
+    a.k = (int32_t)k;
+    a.tiles = p.tiles;
+    a.tile_count = p.tile_count;
+    a.max_tiles = p.max_tiles;
+    a.n_blocks = (int32_t)((n + grouped::kBlockN - 1) / grouped::kBlockN);
+    a.y = (uint16_t*)y;
+    a.y_stride = y_stride;
+    if ((int64_t)a.max_tiles * a.n_blocks >= (1 << 24))
+      return report(QMM_ERR_SHAPE, "grouped: rows * N too large for one call");
+    hipStream_t s = (hipStream_t)stream;
+    hipError_t e = grouped::launch_prepare(p, s);
+    if (e == hipSuccess) e = grouped::launch(a, grouped::kPlain, p.dtype, tile_rows, s);
+    return report_launch(e);
+  });
+}
+
+int64_t qmm_moe_prompt_workspace_bytes(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, int64_t inter) {
+  return guarded([&]() -> int64_t {
+    const int32_t rc = grouped::check_sizes(tokens, experts, top_k, hidden, inter);
+    if (rc != QMM_OK) return rc;
+    report(QMM_OK, "");
+    return grouped::layer_bytes(tokens, experts, top_k, hidden, inter).all();
+  });
+}
+
+int32_t qmm_moe_prompt(const qmm_moe_t* m, void* y, void* workspace, int64_t workspace_bytes, void* stream) {
+  return guarded([&]() -> int32_t {
+    if (!m) return report(QMM_ERR_NULL, "moe_prompt: args must be non-NULL");
+    if (m->dtype != QMM_BF16 && m->dtype != QMM_FP16)
+      return report(QMM_ERR_UNSUPPORTED, "moe_prompt: dtype must be QMM_BF16 or QMM_FP16");
+    if (!m->gate || !m->up || !m->down) return report(QMM_ERR_NULL, "moe_prompt: gate, up and down must be non-NULL");
+    const int64_t hidden = m->gate->w.K, inter = m->gate->w.N, experts = m->gate->num_experts;
+    int32_t rc = grouped::check_sizes(m->tokens, experts, m->top_k, hidden, inter);
+    if (rc != QMM_OK) return rc;
+    grouped::Stack gate, up, down;
+    rc = moe::check_stack("moe_prompt: gate", m->gate, inter, hidden, (int32_t)experts, m->dtype, &gate);
+    if (rc == QMM_OK) rc = moe::check_stack("moe_prompt: up", m->up, inter, hidden, (int32_t)experts, m->dtype, &up);
+    if (rc == QMM_OK) rc = moe::check_stack("moe_prompt: down", m->down, hidden, inter, (int32_t)experts, m->dtype, &down);
+    if (rc == QMM_OK) rc = grouped::check_rows("moe_prompt: gate", gate, inter);
+    if (rc == QMM_OK) rc = grouped::check_rows("moe_prompt: up", up, inter);
+    if (rc == QMM_OK) rc = grouped::check_rows("moe_prompt: down", down, hidden);
+    if (rc != QMM_OK) return rc;
+    if (up.bits != gate.bits || up.group_size != gate.group_size)
+      return report(QMM_ERR_UNSUPPORTED, "moe_prompt: gate and up must share bits and group_size");
+    if (m->x_stride < 0 || m->router_stride < 0 || m->y_stride < 0)
+      return report(QMM_ERR_LAYOUT, "moe_prompt: negative stride");
+    if (m->x_stride % 8) return report(QMM_ERR_ALIGN, "moe_prompt: x_stride must be a multiple of 8 elements");
+    if (m->tokens > 1 && m->y_stride < hidden) return report(QMM_ERR_SHAPE, "moe_prompt: y_stride < hidden");
+    if (m->tokens == 0) return report(QMM_OK, "");
+    const int64_t x_bytes = ((m->tokens - 1) * m->x_stride + hidden) * 2;
+    if (x_bytes >= (1ll << 30)) return report(QMM_ERR_SHAPE, "moe_prompt: the rows of x must span less than 1 GiB");
+    if (!m->x || !m->router_logits || !y || !workspace)
+      return report(QMM_ERR_NULL, "moe_prompt: x, router_logits, y and workspace must be non-NULL");
+    if ((uintptr_t)m->x % 16 || (uintptr_t)m->router_logits % 2 || (uintptr_t)y % 2 || (uintptr_t)workspace % 16)
+      return report(QMM_ERR_ALIGN, "moe_prompt: x and workspace must be 16-byte, router_logits and y 2-byte aligned");
+    const int64_t n = m->tokens * m->top_k;
+    const grouped::LayerBytes b = grouped::layer_bytes(m->tokens, experts, m->top_k, hidden, inter);
+    if (workspace_bytes < b.all())
+      return report(QMM_ERR_SHAPE, "moe_prompt: workspace of " + std::to_string(workspace_bytes) + " bytes, needs " +
+                                       std::to_string(b.all()));
+    char* ws = (char*)workspace;
+    const auto take = [&](int64_t bytes) {
+      char* p = ws;
+      ws += bytes;
+      return p;
+    };
+    const int tile_rows = grouped::tile_rows_of(n, experts);
+    grouped::RouteArgs r{};
+    r.router = (const uint16_t*)m->router_logits;
+    r.router_stride = m->router_stride;
+    r.tokens = (int32_t)m->tokens;
+    r.experts = (int32_t)experts;
+    r.top_k = m->top_k;
+    r.renormalize = m->renormalize != 0;
+    r.dtype = m->dtype;
+    r.pair_expert = (int32_t*)take(b.expert);
+    r.pair_share = (float*)take(b.share);
+    r.pairs = (int32_t*)take(b.pairs);
+    r.tile_rows = tile_rows;
+    char* tiles = take(b.tiles);
+    r.tile_count = (int32_t*)tiles;
+    r.tiles = (grouped::Tile*)(tiles + grouped::align256(16));
+    r.max_tiles = (int32_t)(n / tile_rows + std::min(n, experts));
+    grouped::PrepareArgs p{};
+    p.x = (const uint16_t*)m->x;
+    p.x_stride = m->x_stride;
+    p.rows = m->tokens;
+    p.k = (int32_t)hidden;
+    p.group = gate.group_size;
+    p.dtype = m->dtype;
+    p.sums = (uint16_t*)take(b.sums);
+    p.sum_groups = (int32_t)grouped::sum_groups_of(hidden, p.group);
+
+    grouped::Args g{};
+    g.x = p.x;
+    g.x_stride = m->x_stride;
+    g.x_bytes = (uint32_t)x_bytes;
+    g.sums = p.sums;
+    g.sum_groups = p.sum_groups;
+    g.w[0] = gate;
+    g.w[1] = up;
+    g.n = (int32_t)inter;
+    g.k = (int32_t)hidden;
+    g.tiles = r.tiles;
+    g.tile_count = r.tile_count;
+    g.max_tiles = r.max_tiles;
+    g.h_cols = (int32_t)grouped::round_up(inter, grouped::kStepK);
+    g.n_blocks = g.h_cols / (grouped::kBlockN / 2);
+    g.pairs = r.pairs;
+    g.top_k = m->top_k;
+    g.h = (uint16_t*)take(b.h);
+    g.h_sums = (uint16_t*)take(b.h_sums);
+    g.h_group = down.group_size;
+    g.h_sum_groups = (int32_t)grouped::sum_groups_of(g.h_cols, down.group_size);
+
+    grouped::Args d{};
+    d.x = g.h;
+    d.x_stride = 2 * (int64_t)g.h_cols;
+    d.x_plane = g.h_cols;
+    d.sums = g.h_sums;
+    d.sum_groups = g.h_sum_groups;
+    d.w[0] = d.w[1] = down;
+    d.n = (int32_t)hidden;
+    d.k = (int32_t)inter;
+    d.tiles = r.tiles;
+    d.tile_count = r.tile_count;
+    d.max_tiles = r.max_tiles;
+    d.n_blocks = (int32_t)((hidden + grouped::kBlockN - 1) / grouped::kBlockN);
+    d.pairs = r.pairs;
+    d.top_k = m->top_k;
+    d.out = (float*)take(b.out);
+    if ((int64_t)g.max_tiles * std::max(g.n_blocks, d.n_blocks) >= (1 << 24))
+      return report(QMM_ERR_SHAPE, "moe_prompt: tokens * top_k * max(hidden, inter) too large for one call");
+
+    moe::MoeArgs sum{};                                // the weighted sum of a token's pairs
+    sum.tokens = r.tokens;
+    sum.top_k = m->top_k;
+    sum.renormalize = r.renormalize;
+    sum.hidden = (int32_t)hidden;
+    sum.dtype = m->dtype;
+    sum.y = (uint16_t*)y;
+    sum.y_stride = m->y_stride;
+    sum.pair_share = r.pair_share;
+    sum.out = d.out;
+    sum.splits = 1;
+
+    hipStream_t s = (hipStream_t)stream;
+    hipError_t e = grouped::launch_route(r, p, s);
+    if (e == hipSuccess) e = grouped::launch(g, grouped::kGated, m->dtype, tile_rows, s);
+    if (e == hipSuccess) e = grouped::launch(d, grouped::kDown, m->dtype, tile_rows, s);
+    if (e == hipSuccess) e = moe::launch_sum(sum, s);
+    return report_launch(e);
+  });
+}
+
+}  // extern "C"

@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "../../include/qmm.h"
+
 namespace qmm {
 namespace moe {
 
@@ -67,6 +69,10 @@ struct MoeArgs {
   // the second kernel; stretches of K that different workgroups of the second kernel take
   int32_t parts, down_parts, blocks, down_blocks, splits;
 };
+
+// Validate one stack of an expert layer (host only): [n, cols] per expert, of dtype.
+int32_t check_stack(const char* name, const qmm_expert_stack_t* k, int64_t n, int64_t cols, int32_t experts, int32_t dtype,
+                    Stack* out);
 
 hipError_t launch_b4(const MoeArgs& a, hipStream_t stream, bool down);
 hipError_t launch_b8(const MoeArgs& a, hipStream_t stream, bool down);

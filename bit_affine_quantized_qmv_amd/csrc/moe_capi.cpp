@@ -29,9 +29,11 @@ int64_t out_bytes(int64_t tokens, int64_t top_k, int64_t hidden, int64_t splits)
 // each, of which LDS holds two tokens' operands at once.
 int64_t splits_of(int64_t inter) { return std::min<int64_t>(kMaxSplits, (inter + 6143) / 6144); }
 
+}  // namespace
+
 int32_t check_stack(const char* name, const qmm_expert_stack_t* k, int64_t n, int64_t cols, int32_t experts,
                     int32_t dtype, Stack* out) {
-  const std::string who = std::string("moe: ") + name + ": ";
+  const std::string who = std::string(name) + ": ";
   if (!k) return report(QMM_ERR_NULL, who + "must be non-NULL");
   const qmm_weight_desc_t& w = k->w;
   std::string err;
@@ -61,6 +63,8 @@ int32_t check_stack(const char* name, const qmm_expert_stack_t* k, int64_t n, in
                (const uint16_t*)w.biases, w.sb_row_stride, k->sb_expert_stride, w.bits, w.group_size};
   return QMM_OK;
 }
+
+namespace {
 
 int32_t check_sizes(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, int64_t inter) {
   if (tokens < 0 || tokens > kMaxTokens)
@@ -110,9 +114,9 @@ int32_t qmm_moe(const qmm_moe_t* m, void* y, void* workspace, int64_t workspace_
     int32_t rc = moe::check_sizes(m->tokens, experts, m->top_k, hidden, inter);
     if (rc != QMM_OK) return rc;
     moe::MoeArgs a{};
-    rc = moe::check_stack("gate", m->gate, inter, hidden, (int32_t)experts, m->dtype, &a.gate);
-    if (rc == QMM_OK) rc = moe::check_stack("up", m->up, inter, hidden, (int32_t)experts, m->dtype, &a.up);
-    if (rc == QMM_OK) rc = moe::check_stack("down", m->down, hidden, inter, (int32_t)experts, m->dtype, &a.down);
+    rc = moe::check_stack("moe: gate", m->gate, inter, hidden, (int32_t)experts, m->dtype, &a.gate);
+    if (rc == QMM_OK) rc = moe::check_stack("moe: up", m->up, inter, hidden, (int32_t)experts, m->dtype, &a.up);
+    if (rc == QMM_OK) rc = moe::check_stack("moe: down", m->down, hidden, inter, (int32_t)experts, m->dtype, &a.down);
     if (rc != QMM_OK) return rc;
     if (a.up.bits != a.gate.bits || a.up.group_size != a.gate.group_size)
       return report(QMM_ERR_UNSUPPORTED, "moe: gate and up must share bits and group_size");

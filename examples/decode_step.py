@@ -65,10 +65,9 @@ class Decoder:
         return (x.float() * torch.rsqrt(x.float().square().mean(-1, keepdim=True) + 1e-6)).to(x.dtype)
 
     def moe(self, x, layer):
-        """The expert layer for any number of rows, 32 at a time."""
-        logits = q.qmm_t(x, layer["router"])
-        return torch.cat([q.moe(x[i:i + 32], logits[i:i + 32], layer["gate"], layer["up"], layer["down"],
-                                self.cfg.top_k) for i in range(0, x.shape[0], 32)])
+        """The expert layer: few rows, or the rows of a prompt."""
+        call = q.moe if x.shape[0] <= 32 else q.moe_prompt
+        return call(x, q.qmm_t(x, layer["router"]), layer["gate"], layer["up"], layer["down"], self.cfg.top_k)
 
     def logits(self, tokens, slots, table, lengths, longest):
         """Logits of the last token of each sequence.  tokens int32 [batch, n]: the n tokens that

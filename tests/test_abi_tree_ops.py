@@ -156,3 +156,102 @@ def test_python_arguments():
         q.tree_accept(i, i, i)
     with pytest.raises(ValueError, match="q"):
         q.kv_attend_tree(torch.zeros(2, 4, 2), c, i, i[:, 0], i)
+
+
+# ---------------------------------------------------------------- grouped products and the layer
+
+def weight(n=96, k=128, **kw):
+    d = dict(w_packed=P, w_row_stride=16, scales=P, biases=P, sb_row_stride=2, N=n, K=k, group_size=64, bits=4, dtype=1)
+    return _lib.WeightDesc(*[{**d, **kw}[f] for f, _ in _lib.WeightDesc._fields_])
+
+
+def experts(count=4, expert=None, **kw):
+    w = weight(**kw)
+    return _lib.ExpertStack(w, count, w.N * w.w_row_stride if expert is None else expert, w.N * w.sb_row_stride)
+
+
+def test_grouped():
+    lib = q.load()
+
+    def call(x=P, stride=128, rows=50, offsets=P, y=P, ys=96, ws=P, size=1 << 40, w=None):
+        return lib.qmm_grouped(x, stride, rows, R(experts() if w is None else w), offsets, y, ys, ws, size, None)
+
+    expect(lib.qmm_grouped(P, 128, 50, None, P, P, 96, P, 1 << 40, None), "NULL", "weights")
+    for name in ("x", "offsets", "y", "ws"):
+        expect(call(**{name: None}), "NULL")
+    for name, at in (("x", P + 8), ("ws", P + 8), ("offsets", P + 2), ("y", P + 1)):
+        expect(call(**{name: at}), "ALIGN")
+    expect(call(rows=-1), "SHAPE")
+    expect(call(rows=2 ** 20 + 1), "SHAPE")
+    expect(call(stride=-128), "LAYOUT")
+    expect(call(stride=132), "ALIGN")
+    expect(call(stride=2 ** 23 + 8), "SHAPE")
+    expect(call(ys=95), "SHAPE")
+    expect(call(w=experts(count=513)), "SHAPE", "experts")
+    expect(call(w=experts(count=0)), "SHAPE")
+    expect(call(w=experts(bits=7)), "UNSUPPORTED")
+    expect(call(w=experts(group_size=16)), "UNSUPPORTED")
+    expect(call(w=experts(k=96)), "SHAPE")                          # not a multiple of the group
+    expect(call(w=experts(w_row_stride=15)), "SHAPE")
+    expect(call(w=experts(w_row_stride=18)), "ALIGN")
+    expect(call(w=experts(expert=96 * 16 - 4)), "SHAPE", "expert")
+    expect(call(w=experts(w_packed=P + 8)), "ALIGN")
+    expect(call(w=experts(scales=P + 1)), "ALIGN")
+    expect(call(w=experts(biases=None)), "NULL")
+    expect(call(w=experts(n=2 ** 20, w_row_stride=512)), "SHAPE", "1 GiB")
+    need = lib.qmm_grouped_workspace_bytes(50, R(experts(w_packed=None, scales=None, biases=None)))
+    assert need > 0
+    expect(call(size=need - 1), "SHAPE", "workspace")
+    assert lib.qmm_grouped_workspace_bytes(2 ** 20 + 1, R(experts())) == CODE["QMM_ERR_SHAPE"]
+    assert lib.qmm_grouped_workspace_bytes(5, None) == CODE["QMM_ERR_NULL"]
+    assert lib.qmm_grouped_workspace_bytes(2 ** 20, R(experts())) >= 2 ** 20 // 64 * 16
+    assert call(rows=0, x=None, offsets=None, y=None, ws=None, size=0) == 0
+
+
+def layer(**kw):
+    gate, up, down = (kw.pop(n, d) for n, d in (("gate", experts()), ("up", experts()),
+                                                ("down", experts(n=128, k=96, w_row_stride=12, sb_row_stride=3,
+                                                                 group_size=32))))
+    d = dict(x=P, x_stride=128, router_logits=P, router_stride=4, tokens=40, top_k=2, renormalize=1, dtype=1,
+             gate=ctypes.pointer(gate), up=ctypes.pointer(up), down=ctypes.pointer(down), y_stride=128)
+    return _lib.MoeDesc(**{**d, **kw})
+
+
+def test_moe_prompt():
+    lib = q.load()
+
+    def call(y=P, ws=P, size=1 << 50, **kw):
+        return lib.qmm_moe_prompt(R(layer(**kw)), y, ws, size, None)
+
+    expect(lib.qmm_moe_prompt(None, P, P, 0, None), "NULL")
+    for name in ("x", "router_logits"):
+        expect(call(**{name: None}), "NULL")
+    expect(call(y=None), "NULL")
+    expect(call(ws=None), "NULL")
+    expect(call(x=P + 8), "ALIGN")
+    expect(call(ws=P + 8), "ALIGN")
+    expect(call(y=P + 1), "ALIGN")
+    expect(call(dtype=3), "UNSUPPORTED")
+    expect(call(dtype=2), "UNSUPPORTED", "dtype")
+    expect(call(tokens=-1), "SHAPE")
+    expect(call(tokens=65536), "SHAPE")
+    expect(call(top_k=0), "SHAPE")
+    expect(call(top_k=5), "SHAPE")
+    expect(call(x_stride=132), "ALIGN")
+    expect(call(x_stride=-8), "LAYOUT")
+    expect(call(y_stride=120), "SHAPE")
+    expect(call(x_stride=2 ** 24, tokens=65), "SHAPE", "1 GiB")
+    expect(call(up=experts(group_size=32, sb_row_stride=4)), "UNSUPPORTED", "share")
+    expect(call(up=experts(count=5)), "SHAPE", "experts")
+    expect(call(down=experts()), "SHAPE", "down")
+    need = lib.qmm_moe_prompt_workspace_bytes(40, 4, 2, 128, 96)
+    expect(call(size=need - 1), "SHAPE", "workspace")
+    sizes = [40, 4, 2, 128, 96]
+    for i in range(5):
+        more = list(sizes)
+        more[i] += 64 if i != 2 else 1
+        assert lib.qmm_moe_prompt_workspace_bytes(*more) >= need
+    for bad in ([65536, 4, 2, 128, 96], [40, 513, 2, 128, 96], [40, 4, 5, 128, 96], [40, 4, 2, 0, 96],
+                [40, 4, 2, 128, 2 ** 20 + 1], [65535, 64, 32, 128, 96]):
+        assert lib.qmm_moe_prompt_workspace_bytes(*bad) == CODE["QMM_ERR_SHAPE"]
+    assert call(tokens=0, x=None, router_logits=None, y=None, ws=None, size=0) == 0
