@@ -7,20 +7,27 @@ namespace qmm {
 namespace grouped {
 namespace {
 
-// Sums of the groups of 2048 elements of a row (thread `at` of 256 has eight of them), in three
-// bfloat16 parts; the groups that a row is padded to are zero.  float32, eight in order, then the
-// lanes in pairs.  Bound by memory.
+// 2048 elements of a row (thread `at` of 256 has eight of them) as the products take them, and the
+// sums of their groups in three bfloat16 parts; what a row is padded to is zero.  Sums in float32,
+// eight in order, then the lanes in pairs.  Bound by memory.
+__host__ __device__ inline int64_t blocks_per_row(const PrepareArgs& a) {
+  const int64_t sums = (int64_t)a.sum_groups * a.group, n = sums > a.cols ? sums : a.cols;
+  return (n + 8 * kThreads - 1) / (8 * kThreads);
+}
+
 template <class T>
-__device__ inline void group_sums_of(const PrepareArgs& a, int64_t block, int at) {
-  const int per_row = (a.sum_groups * a.group + 8 * kThreads - 1) / (8 * kThreads);
+__device__ inline void stage_rows(const PrepareArgs& a, int64_t block, int at) {
+  const int per_row = (int)blocks_per_row(a);
   const int64_t row = block / per_row;
   const int k = (int)(block - row * per_row) * 8 * kThreads + 8 * at;
   float sum = 0.f;
+  u32x4 u = {0u, 0u, 0u, 0u};
   if (k < a.k) {
-    const u32x4 u = *(const u32x4*)(a.x + row * a.x_stride + k);
+    u = *(const u32x4*)(a.x + row * a.x_stride + k);
 #pragma unroll
     for (int e = 0; e < 4; ++e) sum += T::to_f32(u[e] & 0xFFFFu) + T::to_f32(u[e] >> 16);
   }
+  if (k < a.cols) *(u32x4*)(a.staged + row * a.cols + k) = a.bits == 4 ? interleave_even_odd(u) : u;
   sum += __shfl_xor(sum, 1);
   sum += __shfl_xor(sum, 2);
   if (a.group >= 64) sum += __shfl_xor(sum, 4);
@@ -28,10 +35,6 @@ __device__ inline void group_sums_of(const PrepareArgs& a, int64_t block, int at
   const int g = k / a.group;
   if (k % a.group == 0 && g < a.sum_groups)
     store_sum(a.sums + row * kPlanes * a.sum_groups + g, a.sum_groups, sum);
-}
-
-__device__ inline int64_t sum_blocks(const PrepareArgs& a) {
-  return a.rows * ((a.sum_groups * a.group + 8 * kThreads - 1) / (8 * kThreads));
 }
 
 // Inclusive prefix of one number per thread of the first 512, over the workgroup (kMake threads).
@@ -58,12 +61,12 @@ __device__ inline void make_tiles(int begin, int count, int tile_rows, Tile* til
   for (int i = 0; i < n; ++i) {
     const int at = end - n + i;
     if (at < max_tiles)
-      tiles[at] = Tile{(int)threadIdx.x, begin + i * tile_rows, min(tile_rows, count - i * tile_rows), 0};
+      tiles[at] = Tile{(int)threadIdx.x, begin + i * tile_rows, min(tile_rows, count - i * tile_rows), end - n, n, {}};
   }
   if (threadIdx.x == kMake - 1) *tile_count = min(end, max_tiles);
 }
 
-// Tiles of given offsets, by the last workgroup; the sums by the others.  An expert's rows start
+// Tiles of given offsets, by the last workgroup; the activations by the others.  An expert's rows start
 // where all before it have ended, whatever the offsets are.
 template <class T>
 __global__ __launch_bounds__(kMake) void prepare_kernel(const PrepareArgs a) {
@@ -71,7 +74,7 @@ __global__ __launch_bounds__(kMake) void prepare_kernel(const PrepareArgs a) {
   __shared__ int most[kMake / 64];
   if (blockIdx.x + 1 < gridDim.x) {
     const int64_t block = (int64_t)blockIdx.x * (kMake / kThreads) + threadIdx.x / kThreads;
-    if (block < sum_blocks(a)) group_sums_of<T>(a, block, threadIdx.x % kThreads);
+    if (block < a.rows * blocks_per_row(a)) stage_rows<T>(a, block, threadIdx.x % kThreads);
     return;
   }
   const int e = threadIdx.x;
@@ -91,11 +94,11 @@ __global__ __launch_bounds__(kMake) void prepare_kernel(const PrepareArgs a) {
 }
 
 // A token's choices, largest first, and their weights exp(l - max l) (over the sum of all experts
-// unless renormalised), by one wave; the sums of the activations' groups by the other workgroups.
+// unless renormalised), by one wave; the activations by the other workgroups.
 template <class T>
 __global__ __launch_bounds__(kThreads) void route_kernel(const RouteArgs a, const PrepareArgs p, const int route_blocks) {
   if ((int)blockIdx.x >= route_blocks) {
-    group_sums_of<T>(p, (int64_t)blockIdx.x - route_blocks, threadIdx.x);
+    stage_rows<T>(p, (int64_t)blockIdx.x - route_blocks, threadIdx.x);
     return;
   }
   const int lane = threadIdx.x & 63, t = blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
@@ -168,14 +171,63 @@ __global__ __launch_bounds__(kMake) void list_kernel(const RouteArgs a) {
   }
 }
 
-int64_t host_sum_blocks(const PrepareArgs& a) {
-  return a.rows * (((int64_t)a.sum_groups * a.group + 8 * kThreads - 1) / (8 * kThreads));
+// y_t = sum of t's pairs, each by its share, in the order of its choices, rounded to dtype; four
+// columns per thread.  Bound by memory.
+template <class T>
+__global__ __launch_bounds__(kThreads) void sum_kernel(const SumArgs a) {
+  const int n = 4 * (int)(blockIdx.x * kThreads + threadIdx.x), t = blockIdx.y;
+  if (n >= a.hidden) return;
+  const float* o = a.out + (int64_t)t * a.top_k * a.hidden + n;
+  const float* share = a.share + t * a.top_k;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  float sum = 0.f;
+  constexpr int kAhead = 8;          // choices whose loads are in flight together
+  for (int i0 = 0; i0 < a.top_k; i0 += kAhead) {
+    f32x4 w[kAhead];
+    float f[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int at = min(i0 + i, a.top_k - 1);
+      w[i] = *(const f32x4*)(o + (int64_t)at * a.hidden);
+      f[i] = share[at];
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (i0 + i >= a.top_k) break;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(f[i], w[i][e], v[e]);
+      sum += f[i];
+    }
+  }
+  if (a.renormalize) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] /= sum;
+  }
+  uint16_t* y = a.y + t * a.y_stride + n;
+  const uint2 u = {T::pack2(v[0], v[1]), T::pack2(v[2], v[3])};
+  if (((uintptr_t)a.y & 7u) == 0u && (a.y_stride & 3) == 0) {
+    *(uint2*)y = u;
+  } else {
+    y[0] = (uint16_t)u.x;
+    y[1] = (uint16_t)(u.x >> 16);
+    y[2] = (uint16_t)u.y;
+    y[3] = (uint16_t)(u.y >> 16);
+  }
 }
 
 }  // namespace
 
+hipError_t launch_sum(const SumArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)((a.hidden + 4 * kThreads - 1) / (4 * kThreads)), (unsigned)a.tokens);
+  if (a.dtype == QMM_BF16)
+    hipLaunchKernelGGL(sum_kernel<Bf16>, grid, dim3(kThreads), 0, stream, a);
+  else
+    hipLaunchKernelGGL(sum_kernel<Fp16>, grid, dim3(kThreads), 0, stream, a);
+  return hipGetLastError();
+}
+
 hipError_t launch_prepare(const PrepareArgs& a, hipStream_t stream) {
-  const int64_t per = kMake / kThreads, blocks = (host_sum_blocks(a) + per - 1) / per + 1;
+  const int64_t per = kMake / kThreads, blocks = (a.rows * blocks_per_row(a) + per - 1) / per + 1;
   if (a.dtype == QMM_BF16)
     hipLaunchKernelGGL(prepare_kernel<Bf16>, dim3((unsigned)blocks), dim3(kMake), 0, stream, a);
   else
@@ -185,7 +237,7 @@ hipError_t launch_prepare(const PrepareArgs& a, hipStream_t stream) {
 
 hipError_t launch_route(const RouteArgs& r, const PrepareArgs& p, hipStream_t stream) {
   const int route_blocks = (r.tokens + kThreads / 64 - 1) / (kThreads / 64);
-  const dim3 grid((unsigned)(route_blocks + host_sum_blocks(p)));
+  const dim3 grid((unsigned)(route_blocks + p.rows * blocks_per_row(p)));
   if (r.dtype == QMM_BF16)
     hipLaunchKernelGGL(route_kernel<Bf16>, grid, dim3(kThreads), 0, stream, r, p, route_blocks);
   else

@@ -13,7 +13,7 @@ using moe::Stack;
 
 constexpr int kThreads = 256;
 constexpr int kBlockN = 256;          // weight rows per workgroup: four waves of four 16-row tiles
-constexpr int kStepK = 128;           // columns between two barriers
+constexpr int kStepK = 128;           // rows of staged activations are whole steps of this
 constexpr int kPlanes = 3;            // bfloat16 parts of a group's sum of activations
 constexpr int kSumPad = 32;           // groups per row of the sums, rounded up to this
 constexpr int kMaxPairs = 1 << 20;    // rows of one call
@@ -30,11 +30,15 @@ struct Tile {
   int32_t expert;
   int32_t first;
   int32_t rows;
-  int32_t unused;
+  int32_t expert_first;      // the expert's first tile, and the number of its tiles
+  int32_t expert_tiles;
+  int32_t unused[3];
 };
 
 struct Args {
-  const uint16_t* x;         // row r at r * x_stride, its rest (kDown) x_plane further
+  // Activations, rows of whole steps (zeros behind k), each eight elements in the order in which the
+  // weights' codes are expanded: row r at r * x_stride, its rest (kDown) x_plane further.
+  const uint16_t* x;
   int64_t x_stride;
   int64_t x_plane;
   uint32_t x_bytes;          // kGated: bytes of all rows, below 2^31
@@ -55,13 +59,17 @@ struct Args {
   uint16_t* h_sums;          // kGated: [row][kPlanes][h_sum_groups]
   int32_t h_sum_groups;
   int32_t h_group;
+  int32_t h_bits;            // width and group size of the weights that take h
   float* out;                // kDown: [pair][n]
 };
 
-// Sums of x's groups and the tiles of a grouped product: one kernel.
+// x as the products take it, the sums of its groups, and the tiles of given offsets: one kernel.
 struct PrepareArgs {
   const uint16_t* x;
   int64_t x_stride;
+  uint16_t* staged;          // [rows][cols]
+  int32_t cols;              // k rounded up to whole steps
+  int32_t bits;
   int64_t rows;
   int32_t k;
   int32_t group;
@@ -94,6 +102,20 @@ struct RouteArgs {
   int32_t* tile_count;
 };
 
+// The weighted sum of a token's pairs.
+struct SumArgs {
+  int32_t tokens;
+  int32_t top_k;
+  int32_t renormalize;
+  int32_t hidden;            // a multiple of 4
+  int32_t dtype;
+  const float* out;          // [tokens * top_k][hidden]
+  const float* share;        // [tokens * top_k]
+  uint16_t* y;               // [tokens][y_stride]
+  int64_t y_stride;
+};
+
+hipError_t launch_sum(const SumArgs& a, hipStream_t stream);
 hipError_t launch_prepare(const PrepareArgs& a, hipStream_t stream);
 hipError_t launch_route(const RouteArgs& r, const PrepareArgs& p, hipStream_t stream);
 // tile_rows: 32 or 64

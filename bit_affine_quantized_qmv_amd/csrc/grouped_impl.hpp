@@ -10,12 +10,15 @@
 // scales do.
 //
 // A workgroup takes 16 FM rows of one expert (a Tile) and 256 weight rows, each of its four waves
-// 64 of them, so a code is unpacked once per tile.  Weights go from memory to the registers of the
-// wave that needs them, a step of 128 columns ahead.  Activations are shared: direct loads put
-// them into LDS in operand order (a load moves the 16 rows x 32 columns that one matrix
-// instruction takes), double-buffered, a step ahead too, with one barrier per step.  A wave reads
-// each operand once per step for the products with its four tiles: half of the LDS' rate when the
-// matrix cores are busy all the time.
+// 64 of them, so a code is unpacked once per tile.  Codes and activations go from memory to LDS
+// by direct loads, a step of STEP columns ahead, and from there to registers as operands; a wave's
+// codes are its own, the activations are shared and double-buffered, with one barrier per step.
+//
+// What decides is how the lanes of a load are laid out.  Four consecutive lanes that stay within
+// 64 bytes move 54 to 59 bytes per cycle and CU from L2, also straight to LDS; in the layout that the
+// matrix instruction takes, lane = row, they are in four rows, and the same load moves 15.5.  With
+// codes loaded that way into registers (and activations 16 rows x 64 bytes at a time) the products of
+// 4094 rows, 4096 x 14336, took 1240 us (gate, up) and 1040 (down).
 #pragma once
 
 #include <type_traits>
@@ -27,22 +30,13 @@ namespace qmm {
 namespace grouped {
 
 constexpr int TN = 4;                          // weight tiles per wave
-constexpr int kMfmaSteps = kStepK / 32;
 constexpr uint32_t kPast = 0x7FFFFF00u;        // an offset past every descriptor: reads zero
 
 typedef __attribute__((address_space(3))) void lds_void_t;
 
-// 16 bytes per lane, at byte offset `off`, to the wave's 1 KB of LDS at `to`.
-__device__ inline void load_to_lds(__amdgpu_buffer_rsrc_t rs, u32x4* to, uint32_t off) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)to, 16, off, 0, 0, 0);
-}
-
-// Eight 4-bit codes in natural order.
-template <class X>
-__device__ inline u32x4 codes4_natural(uint32_t w) {
-  const uint32_t even = w & 0x0F0F0F0Fu, odd = (w >> 4) & 0x0F0F0F0Fu;
-  const uint32_t lo = __builtin_amdgcn_perm(odd, even, 0x05010400u), hi = __builtin_amdgcn_perm(odd, even, 0x07030602u);
-  return u32x4{X::fp8x2_lo(lo), X::fp8x2_hi(lo), X::fp8x2_lo(hi), X::fp8x2_hi(hi)};
+// 16 bytes per lane, at byte offset `off` + `soff`, to the wave's 1 KB of LDS at `to`.
+__device__ inline void load_to_lds(__amdgpu_buffer_rsrc_t rs, u32x4* to, uint32_t off, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)to, 16, off, soff, 0, 0);
 }
 
 // x as leading bits and rest, both bfloat16.
@@ -62,139 +56,82 @@ __device__ inline void store_sum(uint16_t* to, int64_t plane, float sum) {
   to[2 * plane] = Bf16::from_f32(rest - __uint_as_float(b));
 }
 
-// The weights of a wave's four tiles over one step.  GS = 0: a width other than 4 and 8, whose
-// group size is an argument.
-template <class T, class X, int BITS, int GS>
-struct Weights {
-  static constexpr bool kWide = BITS == 4 || BITS == 8;   // 16-byte loads
-  static constexpr int kVec = BITS == 4 ? 1 : 2;
-  static constexpr int kLoads = TN * (kWide ? kVec : 2 * kMfmaSteps);   // loads of codes per step
-  // halfwords of scales per load: two steps of them
-  static constexpr int kPeriod = GS == 0 ? 1 : 2;
-  static constexpr int NH = GS == 0 ? 4 : kPeriod * kStepK / (GS == 0 ? 1 : GS);
-  static constexpr int kScaleRegs = GS == 0 ? 4 : NH / 2;
-
-  __amdgpu_buffer_rsrc_t w_rs[2], s_rs[2];
-  int w_voff[TN], s_voff[TN];
-  u32x4 v[TN][kWide ? kVec : 1];
-  uint32_t w[TN][kWide ? 1 : 2 * kMfmaSteps];
-  uint32_t s[TN][kScaleRegs], s_next[TN][kScaleRegs];
-  uint32_t gshift;
-  int groups, group_shift;
-  bool narrow;
-
-  // row(j): first weight row of tile j; two: tiles from TN / 2 on are of the second matrix
-  template <class Row>
-  __device__ inline void setup(const Args& a, int e, int lane, Row row, bool two) {
-    const int lg = lane >> 4, col = lane & 15;
-    int gword = 0;
-    gshift = 0u;
-    if constexpr (!kWide) decode::generic_lane_offsets<BITS>(lg, gword, gshift);
-    const int gs = a.w[0].group_size;
-    group_shift = __builtin_ctz((unsigned)gs);
-    groups = a.k >> group_shift;
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const Stack& k = a.w[m];
-      const uint32_t w_bytes = (uint32_t)(a.n - 1) * (uint32_t)(k.w_row_stride * 4) + (uint32_t)(a.k / 32 * BITS * 4);
-      const uint32_t s_bytes = (uint32_t)(a.n - 1) * (uint32_t)(k.sb_row_stride * 2) + (uint32_t)(groups * 2);
-      w_rs[m] = decode::make_rsrc(k.w + e * k.w_expert_stride, w_bytes);
-      s_rs[m] = decode::make_rsrc(k.s + e * k.sb_expert_stride, s_bytes);
-    }
-    // scales as words: rows, experts and arrays start on one, and a row ends on one
-    narrow = (groups & 1) != 0 || (((uintptr_t)a.w[0].s | (uintptr_t)a.w[1].s | (uintptr_t)a.w[0].b | (uintptr_t)a.w[1].b) % 4) != 0 ||
-             ((a.w[0].sb_row_stride | a.w[1].sb_row_stride | a.w[0].sb_expert_stride | a.w[1].sb_expert_stride) & 1) != 0;
-#pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      const Stack& k = a.w[two && j >= TN / 2 ? 1 : 0];
-      const int r = row(j) + col;
-      w_voff[j] = r * (int)(k.w_row_stride * 4) + (kWide ? 16 * lg : 4 * gword);
-      s_voff[j] = r * (int)(k.sb_row_stride * 2);
-    }
-  }
-  __device__ inline void load_half(int j, int half, int t) {
-    const auto u = __builtin_amdgcn_raw_buffer_load_b128(w_rs[j >= TN / 2], w_voff[j] + 64 * half, t * (kStepK * BITS / 8), 0);
-    v[j][half] = u32x4{u[0], u[1], u[2], u[3]};
-  }
-  __device__ inline void load_generic(int j, int c, int t) {
-    const int soff = t * (kStepK * BITS / 8);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      w[j][2 * c + i] = __builtin_amdgcn_raw_buffer_load_b32(w_rs[j >= TN / 2], w_voff[j] + 4 * c * BITS + 4 * i, soff, 0);
-  }
-  __device__ inline void load_codes(int t) {
-#pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      if constexpr (kWide) {
-#pragma unroll
-        for (int h = 0; h < kVec; ++h) load_half(j, h, t);
-      } else {
-#pragma unroll
-        for (int c = 0; c < kMfmaSteps; ++c) load_generic(j, c, t);
-      }
-    }
-  }
-  // Scales from step t on, into s_next.
-  __device__ inline void load_scales(int t) {
-#pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      const __amdgpu_buffer_rsrc_t rs = s_rs[j >= TN / 2];
-      if constexpr (GS == 0) {
-#pragma unroll
-        for (int c = 0; c < kMfmaSteps; ++c)
-          s_next[j][c] = __builtin_amdgcn_raw_buffer_load_b16(rs, s_voff[j], ((t * kStepK + 32 * c) >> group_shift) * 2, 0);
-      } else {
-        const int soff = t * (kStepK / GS) * 2;
-        decode::SbRegs<NH> r;
-        if (narrow)
-          decode::load_sb_buf_narrow<NH>(r, rs, s_voff[j], soff);
-        else
-          decode::load_sb_buf<NH>(r, rs, s_voff[j], soff);
-#pragma unroll
-        for (int i = 0; i < NH / 2; ++i) s_next[j][i] = r.v[i];
-      }
-    }
-  }
-  __device__ inline void next_scales() {
-#pragma unroll
-    for (int j = 0; j < TN; ++j)
-#pragma unroll
-      for (int i = 0; i < kScaleRegs; ++i) s[j][i] = s_next[j][i];
-  }
-  // Scale of tile j in matrix step c of step t, the nth since the scales were loaded.
-  __device__ inline float scale(int j, int nth, int c) const {
-    if constexpr (GS == 0) return T::to_f32(s[j][c]);
-    const int i = nth * (kStepK / (GS == 0 ? 1 : GS)) + c * 32 / (GS == 0 ? 1 : GS);
-    return T::to_f32((s[j][i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
-  }
-};
-
-// LDS of the activations of one step: [plane][32-column step][row tile] of 64 operands.
-template <int FM, int PLANES>
+// LDS of the activations of one step: [plane][64-column half][row][8 chunks of 8 columns]; chunk q of row
+// r is at place q ^ Codes::x_place(r).  A direct load moves 8 rows of 128 bytes.
+template <int FM, int PLANES, int STEP>
 struct Shared {
-  static constexpr int kEntries = PLANES * kMfmaSteps * FM * 64;
+  static constexpr int kHalf = 16 * FM * 8;              // entries of one half
+  static constexpr int kEntries = PLANES * (STEP / 64) * kHalf;
 };
+
+// How the codes of a wave's 64 rows lie in LDS and reach the operands.  A row has 64 bytes there (128
+// 4-bit or 64 8-bit codes), 16-byte piece p of row r at place p ^ row_place(r).  A chunk is eight consecutive codes, what a lane gives to one matrix step.  Any chunks of a group
+// can meet in a matrix step, as long as the activations' are the same: a lane group takes kRun
+// consecutive chunks, as many as the group allows, for one wide read.
+template <int BITS, int GS, int STEP>
+struct Codes {
+  static constexpr int kSteps = STEP / 32;                // matrix steps
+  static constexpr int kRun = GS == 32 ? 1 : (STEP == 128 && GS == 128 ? 4 : 2);
+  static constexpr int kReads = kSteps / kRun;            // reads per tile and step
+  static constexpr int kBytes = kRun * BITS;              // of one
+  static constexpr int kBlockSteps = BITS == 4 ? 128 / STEP : 1;   // steps that a direct load covers
+  // The LDS serves a 16-byte read of lane = row in groups of 16 lanes: of two neighbouring lane groups
+  // rows 0-3 and 12-15 of the first with 4-11 of the second, then the others.  The places put such
+  // a group's 16 pieces into different banks, where the two lane groups read different chunks.
+  __device__ static constexpr int row_place(int r) {
+    const int t = (r >> 2) & 3;
+    return (((t << 1) ^ t) & 2) | (t >> 1);
+  }
+  __device__ static constexpr int x_place(int r) {
+    const int p = (r >> 1) & 7;
+    return kRun == 1 ? p : ((p << 1) & 6) | (((p >> 2) ^ (p >> 1)) & 1);
+  }
+  // place and offset of the lane group's first chunk; what read r of a step is xored with
+  __device__ static constexpr int piece(int lg) { return kBytes == 16 ? lg : (kBytes == 8 ? lg >> 1 : 0); }
+  __device__ static constexpr int offset(int lg) { return kBytes == 16 ? 0 : (kBytes == 8 ? 8 * (lg & 1) : 4 * lg); }
+  __device__ static constexpr int read_piece(int r, int half) {
+    return kBytes == 16 ? 0 : (kBytes == 8 ? 2 * (r + half) : r + 2 * half);
+  }
+  // the activations' chunk of lane group lg in matrix step c: 64-column half, and place in it
+  __device__ static constexpr int lane_half(int lg) { return kRun == 4 ? lg >> 1 : 0; }
+  __device__ static constexpr int lane_chunk(int lg) { return kRun == 4 ? 4 * (lg & 1) : (kRun == 2 ? 2 * lg : lg); }
+  __device__ static constexpr int step_half(int c) { return kRun == 4 ? 0 : c >> 1; }
+  __device__ static constexpr int step_chunk(int c) { return kRun == 4 ? c : (kRun == 2 ? c & 1 : 4 * (c & 1)); }
+};
+
+typedef uint32_t u32x4_by4 __attribute__((ext_vector_type(4), aligned(4)));
 
 template <class T, class X, int BITS, int GS, int FM, int KIND>
 __global__ __launch_bounds__(kThreads, FM == 2 ? 3 : 2) void grouped_kernel(const Args a) {
   constexpr int PLANES = KIND == kDown ? 2 : 1;
-  constexpr int kDma = PLANES * kMfmaSteps * FM / 4;      // direct loads per wave and step
-  using W = Weights<T, X, BITS, GS>;
-  __shared__ u32x4 as0[Shared<FM, PLANES>::kEntries];
-  __shared__ u32x4 as1[Shared<FM, PLANES>::kEntries];
-  __shared__ float tile_s[KIND == kDown ? 1 : 16 * 132];
+  constexpr bool kLds = BITS == 4 || BITS == 8;           // other widths: codes from memory to registers
+  // columns of a step: what leaves room for two workgroups per CU
+  constexpr int STEP = BITS == 4 && PLANES == 1 ? 128 : 64;
+  constexpr int MS = STEP / 32;
+  constexpr int kGroupSteps = GS == 0 ? 1 : GS / 32;      // matrix steps of a group
+  constexpr int kHalves = kGroupSteps > MS ? kGroupSteps / MS : 1;   // steps of a group
+  constexpr int kDma = PLANES * (STEP / 64) * (FM / 2);   // direct loads of activations per wave and step
+  using L = Shared<FM, PLANES, STEP>;
+  using C = Codes<kLds ? BITS : 4, GS == 0 ? 32 : GS, STEP>;
+  __shared__ u32x4 as0[L::kEntries], as1[L::kEntries];
+  __shared__ u32x4 bs[kLds ? 1024 : 528];                 // codes of four waves; then rows of the result
+  __shared__ u32x4 ss[256];                               // eight scales of each weight row
 
-  // Workgroups go to the eight XCDs in turn.  Each XCD takes a run of consecutive tiles of a run
-  // of consecutive weight blocks, tiles fastest: the tiles of an expert share its weights there.
-  const int total = a.max_tiles * a.n_blocks, run = (total + 7) / 8;
+  // Workgroups go to the eight XCDs in turn.  Each XCD takes a run of the work in the order expert,
+  // weight block, tile: what runs there at a time shares both weights and activations.  (In the
+  // order weight block, tile, expert each XCD went through all activations for every block.)
+  const int total = *a.tile_count * a.n_blocks, run = (total + 7) / 8;
   const int id = (int)(blockIdx.x & 7) * run + (int)(blockIdx.x >> 3);
-  if (id >= total) return;
-  const int nb = id / a.max_tiles, mt = id - nb * a.max_tiles;
-  if (mt >= *a.tile_count) return;
-  Tile tile = a.tiles[mt];                     // the same in every lane, which the descriptors need to know
-  tile.expert = __builtin_amdgcn_readfirstlane(tile.expert);
-  tile.first = __builtin_amdgcn_readfirstlane(tile.first);
-  tile.rows = __builtin_amdgcn_readfirstlane(tile.rows);
+  if ((int)(blockIdx.x >> 3) >= run || id >= total) return;
+  const Tile* any = a.tiles + id / a.n_blocks;             // a tile of the same expert
+  const int local = id - any->expert_first * a.n_blocks;
+  const int nb = __builtin_amdgcn_readfirstlane(local / any->expert_tiles);
+  const Tile* mine = a.tiles + any->expert_first + (local - nb * any->expert_tiles);
+  // the same in every lane, which the descriptors need to know
+  struct {
+    int expert, first, rows;
+  } tile = {__builtin_amdgcn_readfirstlane(mine->expert), __builtin_amdgcn_readfirstlane(mine->first),
+            __builtin_amdgcn_readfirstlane(mine->rows)};
 
   const int lane = threadIdx.x & 63, lg = lane >> 4, col = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -203,134 +140,270 @@ __global__ __launch_bounds__(kThreads, FM == 2 ? 3 : 2) void grouped_kernel(cons
   const auto weight_row = [&](int j) {
     return kTwo ? nb * (kBlockN / 2) + wave * 32 + 16 * (j & 1) : nb * kBlockN + wave * 64 + 16 * j;
   };
-  W w;
-  w.setup(a, tile.expert, lane, weight_row, kTwo);
+  const auto stack = [&](int j) -> const Stack& { return a.w[kTwo && j >= TN / 2 ? 1 : 0]; };
+  const int group_shift = __builtin_ctz((unsigned)a.w[0].group_size), groups = a.k >> group_shift;
+  const int steps = (a.k + STEP - 1) / STEP;
 
-  // ---- activations: load d of the wave is row tile di, matrix step dc, plane dp
+  // ---- codes
+  __amdgpu_buffer_rsrc_t w_rs[2];
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const Stack& k = a.w[m];
+    w_rs[m] = decode::make_rsrc(k.w + tile.expert * k.w_expert_stride,
+                                (uint32_t)(a.n - 1) * (uint32_t)(k.w_row_stride * 4) + (uint32_t)(a.k / 32 * BITS * 4));
+  }
+  int w_voff[TN];                                          // rows past the last read as zeros
+  int gword = 0;
+  uint32_t gshift = 0u;
+  if constexpr (!kLds) decode::generic_lane_offsets<BITS>(lg, gword, gshift);
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {
+    const int row_bytes = (int)(stack(j).w_row_stride * 4);
+    if constexpr (kLds) {
+      const int r = lane >> 2, piece = (lane & 3) ^ C::row_place(r);
+      w_voff[j] = (weight_row(j) + r) * row_bytes + 16 * piece;
+    } else {
+      w_voff[j] = (weight_row(j) + col) * row_bytes + 4 * gword;
+    }
+  }
+  // direct loads of the codes of block `blk` (64 bytes of each row), to the wave's part of LDS
+  u32x4* const my_codes = bs + (kLds ? wave * 256 : 0);
+  const auto load_codes = [&](int blk) {
+    if constexpr (kLds) {
+#pragma unroll
+      for (int j = 0; j < TN; ++j) load_to_lds(w_rs[kTwo && j >= TN / 2], my_codes + 64 * j, w_voff[j], 64 * blk);
+    }
+  };
+  const int code_at = wave * 4096 + 64 * col + C::offset(lg), code_piece = C::piece(lg) ^ C::row_place(col);
+  u32x4 rc[TN];                                            // a step's codes of the lane
+  const auto read_codes = [&](int half) {
+    if constexpr (kLds) {
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int r = 0; r < C::kReads; ++r) {
+          const char* p = (const char*)bs + code_at + 1024 * j + 16 * (code_piece ^ C::read_piece(r, half));
+          if constexpr (C::kBytes == 16) {
+            rc[j] = *(const u32x4*)p;
+          } else if constexpr (C::kBytes == 8) {
+            const uint2 u = *(const uint2*)p;
+            rc[j][2 * r] = u.x;
+            rc[j][2 * r + 1] = u.y;
+          } else {
+            rc[j][r] = *(const uint32_t*)p;
+          }
+        }
+    }
+  };
+  uint32_t gw[TN][kLds ? 1 : 2 * MS];                      // other widths
+  const auto load_generic = [&](int j, int c, int t) {
+    if constexpr (!kLds) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        gw[j][2 * c + i] = __builtin_amdgcn_raw_buffer_load_b32(w_rs[kTwo && j >= TN / 2], w_voff[j] + 4 * c * BITS + 4 * i,
+                                                                t * (STEP * BITS / 8), 0);
+    }
+  };
+
+  // ---- scales: lane r loads those of the wave's weight row r, eight groups at a time, well ahead, and
+  // leaves them in LDS when their first step comes.  Groups and rows past the last are zero.
+  const bool narrow = (((uintptr_t)a.w[0].s | (uintptr_t)a.w[1].s | (uintptr_t)a.w[0].b | (uintptr_t)a.w[1].b) & 3) != 0 ||
+                      ((a.w[0].sb_row_stride | a.w[1].sb_row_stride | a.w[0].sb_expert_stride | a.w[1].sb_expert_stride) & 1) != 0;
+  const Stack& s_stack = a.w[kTwo ? lane >> 5 : 0];
+  const int s_row = weight_row(lane >> 4) + col;
+  const uint16_t* s_ptr = s_stack.s + tile.expert * s_stack.sb_expert_stride + (int64_t)min(s_row, a.n - 1) * s_stack.sb_row_stride;
+  const uint32_t s_mask = s_row < a.n ? 0xFFFFFFFFu : 0u;
+  u32x4 s_next = {0u, 0u, 0u, 0u};
+  const auto load_scales = [&](int g0) {
+    if (!narrow && g0 + 8 <= groups) {
+      s_next = *(const u32x4_by4*)(s_ptr + g0);
+    } else {
+      s_next = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (g0 + e < groups) s_next[e >> 1] |= (uint32_t)s_ptr[g0 + e] << (16 * (e & 1));
+    }
+  };
+  const char* const my_scales = (const char*)(ss + wave * 64 + col);
+
+  // ---- activations
   const auto x_row = [&](int m) -> int64_t {               // row of x of the tile's row m < rows
     if constexpr (KIND == kGated) return a.pairs[tile.first + m] / a.top_k;
     return (int64_t)tile.first + m;
   };
-  // descriptor over all of x where rows are looked up, else over the tile's rows
+  // descriptor over all of x where rows are looked up, else over the tile's rows; rows are whole steps
   const uint16_t* x_base = KIND == kGated ? a.x : a.x + (int64_t)tile.first * a.x_stride;
-  const uint32_t x_bytes = KIND == kGated ? a.x_bytes : (uint32_t)((int64_t)(tile.rows - 1) * a.x_stride * 2 +
-                                                                   a.x_plane * (PLANES - 1) * 2 + (int64_t)a.k * 2);
+  const uint32_t x_bytes = KIND == kGated ? a.x_bytes : (uint32_t)(tile.rows * a.x_stride * 2);
   const __amdgpu_buffer_rsrc_t x_rs = decode::make_rsrc(x_base, x_bytes);
-  // FM = 4: wave w loads row tile w, all its steps and planes; FM = 2: row tile w / 2, half of them
-  static_assert(FM == 4 || FM == 2, "loads divide evenly");
-  const int di = FM == 4 ? wave : wave >> 1, d0 = FM == 4 ? 0 : (wave & 1) * kDma;
-  uint32_t x_off = kPast;                                  // of the lane's row
-  if (16 * di + col < tile.rows)
-    x_off = (uint32_t)((KIND == kGated ? x_row(16 * di + col) : 16 * di + col) * a.x_stride * 2);
-  const int sub = decode::lane_group_of_sub<BITS>(lg);     // (its own inverse)
-  uint32_t off[kDma];
+  // load d of the wave: 8 rows of one half and plane; the wave's rows are the same in all of them
+  constexpr int kMine = FM / 2;                            // octets of rows of the wave
+  uint32_t x_off[kMine];                                   // of the lane's rows and chunk
+#pragma unroll
+  for (int u = 0; u < kMine; ++u) {
+    const int m = 8 * (wave + 4 * u) + (lane >> 3);
+    const int chunk = (lane & 7) ^ C::x_place(m);
+    x_off[u] = kPast;
+    if (m < tile.rows) x_off[u] = (uint32_t)((KIND == kGated ? x_row(m) : m) * a.x_stride * 2) + 16 * chunk;
+  }
   const auto load_x = [&](int t, u32x4* buf) {
 #pragma unroll
     for (int d = 0; d < kDma; ++d) {
-      const int dd = d0 + d, dp = dd / kMfmaSteps, dc = dd - dp * kMfmaSteps;
-      const int k = t * kStepK + 32 * dc + 8 * sub;
-      off[d] = k < a.k && x_off != kPast ? x_off + (uint32_t)(2 * (k + dp * (int)a.x_plane)) : kPast;
-      load_to_lds(x_rs, buf + ((dp * kMfmaSteps + dc) * FM + di) * 64, off[d]);
+      const int u = d % kMine, half = d / kMine % (STEP / 64), p = d / kMine / (STEP / 64);
+      load_to_lds(x_rs, buf + (p * (STEP / 64) + half) * L::kHalf + 64 * (wave + 4 * u), x_off[u],
+                  2 * (t * STEP + 64 * half + p * (int)a.x_plane));
     }
   };
+  const int x_entry = C::lane_half(lg) * L::kHalf + 8 * col, x_chunk = C::lane_chunk(lg) ^ C::x_place(col);
 
-  f32x4 acc[TN][FM];
+  f32x4 acc[TN][FM], part[TN][FM];
   const f32x4 zero4 = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int j = 0; j < TN; ++j)
 #pragma unroll
-    for (int i = 0; i < FM; ++i) acc[j][i] = zero4;
+    for (int i = 0; i < FM; ++i) acc[j][i] = part[j][i] = zero4;
 
-  const int steps = (a.k + kStepK - 1) / kStepK;
-  w.load_scales(0);
+  load_scales(0);
   load_x(0, as0);
-  w.load_codes(0);
-  w.next_scales();
+  load_codes(0);
+  if constexpr (!kLds) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int c = 0; c < MS; ++c) load_generic(j, c, 0);
+  }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   lds_barrier();
 
-  // Step t: reads `cur`, loads step t + 1 into `nxt` and the registers that it has emptied.  The
-  // two memory fences keep the loads of codes between them, so that the count at the end says
-  // that the direct loads, which came before, have landed.
-  // The last step loads itself once more, which nobody uses.
-  const auto step = [&](int t_in, const u32x4* cur, u32x4* nxt, auto nth_c) __attribute__((always_inline)) {
-    constexpr int nth = decltype(nth_c)::value;
+  // Step t reads `cur` and loads step t + 1 into `nxt`, and into the places that it has emptied; the last
+  // step loads itself once more, which nobody uses.  half: which step of the group, or of the block of
+  // codes, it is.
+  const auto step = [&](int t_in, const u32x4* cur, u32x4* nxt, auto half_c) __attribute__((always_inline)) {
+    constexpr int half = decltype(half_c)::value;
     const int t = __builtin_amdgcn_readfirstlane(t_in);    // (else it may be kept per lane, offset and all)
     const int next = min(t + 1, steps - 1);
-    if (nth == W::kPeriod - 1) w.load_scales(next);
-    asm volatile("" ::: "memory");
     load_x(next, nxt);
-    asm volatile("" ::: "memory");
-    const bool whole = (t + 1) * kStepK <= a.k;
-    f32x4 part[TN][FM];
-    u32x4 rc[TN];
+    const int g0 = (t * STEP) >> group_shift;              // the step's first group
+    if (((t * STEP) & ((8 << group_shift) - 1)) == 0) {
+      ss[wave * 64 + lane] = s_next & s_mask;
+      if (g0 + 8 < groups) load_scales(g0 + 8);
+    }
+    read_codes(C::kBlockSteps == 2 ? half : 0);
+    // scales of the groups that end in the step, as many as one read has
+    constexpr int kScales = GS == 0 ? MS : (MS / kGroupSteps > 0 ? MS / kGroupSteps : 1);
+    uint32_t sc[TN][(kScales + 1) / 2];
 #pragma unroll
-    for (int c = 0; c < kMfmaSteps; ++c) {
-      __builtin_amdgcn_sched_barrier(0);       // (else operands of several steps are unpacked first, and spilled)
-      if constexpr (BITS == 4) {
-        if (c == 0) {
+    for (int j = 0; j < TN; ++j) {
+      const char* p = my_scales + 256 * j + 2 * (g0 & 7);
+      if constexpr (GS == 0) {
+        sc[j][0] = 0u;
 #pragma unroll
-          for (int j = 0; j < TN; ++j) rc[j] = decode::transpose_lane_groups(w.v[j][0]);
-#pragma unroll
-          for (int j = 0; j < TN; ++j) w.load_half(j, 0, next);
-        }
-      } else if constexpr (BITS == 8) {
-        if (c % 2 == 0) {
-#pragma unroll
-          for (int j = 0; j < TN; ++j) rc[j] = decode::swap_halves(w.v[j][c / 2]);
-#pragma unroll
-          for (int j = 0; j < TN; ++j) w.load_half(j, c / 2, next);
-        }
+        for (int c = 0; c < MS; ++c)
+          sc[j][0] |= (uint32_t)*(const uint16_t*)(my_scales + 256 * j + 2 * (((t * STEP + 32 * c) >> group_shift) & 7)) << (16 * c);
+      } else if constexpr (kScales == 1) {
+        sc[j][0] = *(const uint16_t*)p;
+      } else if constexpr (kScales == 2) {
+        sc[j][0] = *(const uint32_t*)p;
+      } else {
+        const uint2 u = *(const uint2*)p;
+        sc[j][0] = u.x;
+        sc[j][kScales / 4] = u.y;
       }
-      typename X::v8 av[PLANES][FM];
+    }
+    typename X::v8 av[2][PLANES][FM];
+    const auto read_x = [&](int c) {
 #pragma unroll
       for (int p = 0; p < PLANES; ++p)
 #pragma unroll
-        for (int i = 0; i < FM; ++i) av[p][i] = as_v8<X>(cur[((p * kMfmaSteps + c) * FM + i) * 64 + lane]);
-      constexpr int kGroupSteps = GS == 0 ? 1 : GS / 32;
-      const bool fresh = c % kGroupSteps == 0, last = (c + 1) % kGroupSteps == 0;
+        for (int i = 0; i < FM; ++i)
+          av[c & 1][p][i] = as_v8<X>(
+              cur[(p * (STEP / 64) + C::step_half(c)) * L::kHalf + 128 * i + x_entry + (x_chunk ^ C::step_chunk(c))]);
+    };
+    read_x(0);
+    if constexpr (kLds) {
+      if (C::kBlockSteps == 1 || half == 1) {              // the codes are out of LDS: the next ones may come
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        load_codes(min(t / C::kBlockSteps + 1, (steps - 1) / C::kBlockSteps));
+      }
+    }
+    // operand of tile j in matrix step c
+    const auto codes = [&](int j, int c) {
+      if constexpr (BITS == 4) {
+        return codes4_to_v8<X>(rc[j][c]);
+      } else if constexpr (BITS == 8) {
+        return c % 2 ? codes8_to_v8<X>(rc[j].z, rc[j].w) : codes8_to_v8<X>(rc[j].x, rc[j].y);
+      } else {
+        const u32x4 q = codesN_to_v8<X, BITS>(gw[j][2 * c], gw[j][2 * c + 1], gshift);
+        load_generic(j, c, next);
+        return q;
+      }
+    };
+    const auto last_of_group = [](int c) { return (half % kHalves * MS + c + 1) % kGroupSteps == 0; };
+    const auto first_of_group = [](int c) { return (half % kHalves * MS + c) % kGroupSteps == 0; };
+    // a finished group of tile j: its products, scaled, to the sums
+    const auto add_group = [&](int j, int c) {
+      const int i = GS == 0 ? c : (kScales == 1 ? 0 : c / kGroupSteps);
+      const float s = T::to_f32((sc[j][i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
+#pragma unroll
+      for (int m = 0; m < FM; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[j][m][r] = __builtin_fmaf(s, part[j][m][r], acc[j][m][r]);
+    };
+    u32x4 q = codes(0, 0);
+    // The products of a tile, with the unpacking of the next one's codes and the scaling of the last
+    // one's group between them, one by one: the matrix core works while the vector unit does.
+#pragma unroll
+    for (int c = 0; c < MS; ++c) {
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
-        u32x4 q;
-        if constexpr (BITS == 4) {
-          q = codes4_natural<X>(rc[j][c]);
-        } else if constexpr (BITS == 8) {
-          q = c % 2 ? codes8_to_v8<X>(rc[j].z, rc[j].w) : codes8_to_v8<X>(rc[j].x, rc[j].y);
-        } else {
-          q = codesN_to_v8<X, BITS>(w.w[j][2 * c], w.w[j][2 * c + 1], w.gshift);
-          w.load_generic(j, c, next);
-        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (j == 0 && c + 1 < MS) read_x(c + 1);
+        u32x4 q_next = q;
+        if (j + 1 < TN)
+          q_next = codes(j + 1, c);
+        else if (c + 1 < MS)
+          q_next = codes(0, c + 1);
         const typename X::v8 bq = as_v8<X>(q);
 #pragma unroll
         for (int p = PLANES - 1; p >= 0; --p)
 #pragma unroll
-          for (int i = 0; i < FM; ++i) part[j][i] = X::mfma(av[p][i], bq, fresh && p == PLANES - 1 ? zero4 : part[j][i]);
-        if (last) {
-          // groups past K: their scales are not theirs
-          const bool ok = whole || t * kStepK + 32 * c < a.k;
-          const float s = ok ? w.scale(j, nth, c) : 0.f;
-#pragma unroll
           for (int i = 0; i < FM; ++i)
+            part[j][i] = X::mfma(av[c & 1][p][i], bq, first_of_group(c) && p == PLANES - 1 ? zero4 : part[j][i]);
+        const bool adds = j > 0 ? last_of_group(c) : (c > 0 && last_of_group(c - 1));
+        if (j > 0 && last_of_group(c)) add_group(j - 1, c);
+        if (j == 0 && c > 0 && last_of_group(c - 1)) add_group(TN - 1, c - 1);
+        // (the mask's bits: 8 a matrix instruction, 2 a vector one)
+        const int each = ((adds ? 4 * FM : 0) + 10 + FM * PLANES - 1) / (FM * PLANES);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[j][i][r] = __builtin_fmaf(s, part[j][i][r], acc[j][i][r]);
+        for (int i = 0; i < FM * PLANES; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          if (each <= 1) __builtin_amdgcn_sched_group_barrier(0x002, 1, 0);
+          else if (each == 2) __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
+          else if (each == 3) __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
+          else if (each <= 6) __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);
+          else __builtin_amdgcn_sched_group_barrier(0x002, 10, 0);
         }
+        q = q_next;
       }
     }
-    if (nth == W::kPeriod - 1) w.next_scales();
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0F70 | (W::kLoads & 15) | ((W::kLoads >> 4) << 14));   // vmcnt(kLoads)
-    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    if (last_of_group(MS - 1)) add_group(TN - 1, MS - 1);
+    // (the sums are taken here: else the multiply-adds sink below the next step's branches, and
+    // the products that they wait for fill the registers)
 #pragma unroll
-    for (int d = 0; d < kDma; ++d) asm volatile("" ::"v"(off[d]));
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int i = 0; i < FM; ++i) asm volatile("" : "+v"(acc[j][i]));
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");       // the next step's loads, a step old
     lds_barrier();
   };
   using First = std::integral_constant<int, 0>;
-  using Second = std::integral_constant<int, W::kPeriod - 1>;
-  for (int t = 0; t < steps; t += 2) {
+  using Second = std::integral_constant<int, 1>;
+  int t = 0;
+  for (; t + 1 < steps; t += 2) {
     step(t, as0, as1, First{});
-    if (t + 1 >= steps) break;
     step(t + 1, as1, as0, Second{});
   }
+  if (t < steps) step(t, as0, as1, First{});
 
   // ---- biases: 32 groups at a time
   {
@@ -338,7 +411,7 @@ __global__ __launch_bounds__(kThreads, FM == 2 ? 3 : 2) void grouped_kernel(cons
 #pragma unroll
     for (int i = 0; i < FM; ++i)
       sum_rows[i] = a.sums + x_row(min(16 * i + col, tile.rows - 1)) * (kPlanes * (int64_t)a.sum_groups) + 8 * lg;
-    for (int g0 = 0; g0 < w.groups; g0 += 32) {
+    for (int g0 = 0; g0 < groups; g0 += 32) {
       bf16x8 sv[kPlanes][FM];
 #pragma unroll
       for (int p = 0; p < kPlanes; ++p)
@@ -346,12 +419,12 @@ __global__ __launch_bounds__(kThreads, FM == 2 ? 3 : 2) void grouped_kernel(cons
         for (int i = 0; i < FM; ++i) sv[p][i] = as_v8<Bf16>(*(const u32x4*)(sum_rows[i] + p * a.sum_groups + g0));
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
-        const Stack& k = a.w[kTwo && j >= TN / 2 ? 1 : 0];
+        const Stack& k = stack(j);
         const int row = weight_row(j) + col;
         uint32_t b[4] = {0u, 0u, 0u, 0u};
         const uint16_t* p = k.b + tile.expert * k.sb_expert_stride + (int64_t)min(row, a.n - 1) * k.sb_row_stride + g0 + 8 * lg;
-        const int left = w.groups - g0 - 8 * lg;
-        if (!w.narrow && left >= 8) {
+        const int left = groups - g0 - 8 * lg;
+        if (!narrow && left >= 8) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) b[e] = ((const uint32_t*)p)[e];
         } else {
@@ -399,6 +472,7 @@ __global__ __launch_bounds__(kThreads, FM == 2 ? 3 : 2) void grouped_kernel(cons
       }
   } else if constexpr (KIND == kGated) {
     // 16 rows at a time through LDS, so that a thread has eight consecutive columns of a row
+    float* const tile_s = (float*)bs;                      // [16][132]
     const int row = threadIdx.x >> 4, c8 = (threadIdx.x & 15) * 8;
     const int n0 = nb * (kBlockN / 2);
 #pragma unroll
@@ -433,6 +507,10 @@ __global__ __launch_bounds__(kThreads, FM == 2 ? 3 : 2) void grouped_kernel(cons
           hi[e] = h;
           lo[e] = l;
         }
+        if (a.h_bits == 4) {                               // the order in which 4-bit codes are expanded
+          hi = interleave_even_odd(hi);
+          lo = interleave_even_odd(lo);
+        }
         uint16_t* to = a.h + pos * 2 * a.h_cols + n0 + c8;
         *(u32x4*)to = hi;
         *(u32x4*)(to + a.h_cols) = lo;
@@ -449,7 +527,7 @@ __global__ __launch_bounds__(kThreads, FM == 2 ? 3 : 2) void grouped_kernel(cons
       }
     }
   } else {
-    uint16_t* ys = (uint16_t*)tile_s;                      // [16][264]
+    uint16_t* const ys = (uint16_t*)bs;                    // [16][264]
     const int row = threadIdx.x >> 4, c16 = (threadIdx.x & 15) * 16;
     const int n0 = nb * kBlockN;
     const bool vec = a.y_stride % 8 == 0 && ((uintptr_t)a.y & 15u) == 0u;

@@ -529,15 +529,14 @@ int64_t qmm_moe_workspace_bytes(int64_t tokens, int64_t experts, int64_t top_k, 
  *     y[r] = x[r] W_e^T   for offsets[e] <= r < offsets[e + 1]
  * over a stack of quantized weights [N, K]; the weight that a code stands for, s * q + b, is not
  * rounded (codes are exact operands, scales and biases enter in float32, as in qmv).
- * x: DEVICE [rows, x_stride] of dtype, 16-byte aligned, x_stride % 8 == 0 and at most 2^23.
+ * x: DEVICE [rows, x_stride] of dtype, 16-byte aligned, x_stride % 8 == 0.
  * offsets: DEVICE int32 [num_experts + 1], ascending; they are taken into [0, rows], and an expert's
  * rows start where those of all before it have ended.  Rows of y that belong to no expert are left
  * as they are.  y: DEVICE [rows, y_stride] of dtype, 2-byte aligned, y_stride >= N.  rows at most
  * 2^20, num_experts at most QMM_MOE_MAX_EXPERTS, N and K at most 2^20; the limits and alignments
  * of qmm_moe's stacks.  workspace: DEVICE, 16-byte aligned, qmm_grouped_workspace_bytes(rows, weights)
  * bytes of any content; one serves any number of calls in stream order, calls that may overlap need
- * their own.  A row's result depends only on the row, its expert and whether rows exceeds
- * 32 * num_experts.  rows == 0 is a no-op.  Two kernels. */
+ * their own.  A row's result depends on nothing but the row and its expert.  rows == 0 is a no-op.  Two kernels. */
 int32_t qmm_grouped(const void* x, int64_t x_stride, int64_t rows, const qmm_expert_stack_t* weights,
                     const int32_t* offsets, void* y, int64_t y_stride, void* workspace, int64_t workspace_bytes,
                     void* stream);
@@ -546,8 +545,8 @@ int32_t qmm_grouped(const void* x, int64_t x_stride, int64_t rows, const qmm_exp
  * NULL), or a negative error code. */
 int64_t qmm_grouped_workspace_bytes(int64_t rows, const qmm_expert_stack_t* weights);
 
-/* The layer of qmm_moe for any number of tokens (at most 65535, tokens * top_k at most 2^20, the
- * rows of x within 1 GiB): arguments, formula, arithmetic and alignments are qmm_moe's, the
+/* The layer of qmm_moe for any number of tokens (at most 65535, tokens * top_k at most 2^20,
+ * tokens * hidden, each row rounded up to 128, below 2^29): arguments, formula, arithmetic and alignments are qmm_moe's, the
  * workspace is qmm_moe_prompt_workspace_bytes(...) bytes.  tokens == 0 is a no-op.  Five kernels.
  * For up to 32 tokens qmm_moe is the faster one. */
 int32_t qmm_moe_prompt(const qmm_moe_t* args, void* y, void* workspace, int64_t workspace_bytes, void* stream);

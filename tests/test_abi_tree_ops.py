@@ -185,7 +185,6 @@ def test_grouped():
     expect(call(rows=2 ** 20 + 1), "SHAPE")
     expect(call(stride=-128), "LAYOUT")
     expect(call(stride=132), "ALIGN")
-    expect(call(stride=2 ** 23 + 8), "SHAPE")
     expect(call(ys=95), "SHAPE")
     expect(call(w=experts(count=513)), "SHAPE", "experts")
     expect(call(w=experts(count=0)), "SHAPE")
@@ -240,7 +239,9 @@ def test_moe_prompt():
     expect(call(x_stride=132), "ALIGN")
     expect(call(x_stride=-8), "LAYOUT")
     expect(call(y_stride=120), "SHAPE")
-    expect(call(x_stride=2 ** 24, tokens=65), "SHAPE", "1 GiB")
+    wide = dict(gate=experts(k=16384, w_row_stride=2048, sb_row_stride=256), up=experts(k=16384, w_row_stride=2048, sb_row_stride=256),
+                down=experts(n=16384, k=96, w_row_stride=12, sb_row_stride=3, group_size=32))
+    expect(call(x_stride=16384, y_stride=16384, tokens=65535, top_k=1, **wide), "SHAPE", "2^29")
     expect(call(up=experts(group_size=32, sb_row_stride=4)), "UNSUPPORTED", "share")
     expect(call(up=experts(count=5)), "SHAPE", "experts")
     expect(call(down=experts()), "SHAPE", "down")

@@ -137,8 +137,19 @@ def test_grouped_offsets_out_of_order():
         assert torch.equal(y, want)
 
 
+def test_grouped_rows_are_the_same_in_tiles_of_any_height():
+    import bit_affine_quantized_qmv_amd as q
+    dev = require_gpu()
+    for bits, group in ((4, 32), (4, 64), (4, 128), (8, 32), (8, 128), (6, 64)):
+        w = stack(200, 384, group, bits, "bf16", 2, 1, dev)
+        x = synth.normal_x((190, 384), "bf16", seed=1).to(dev)
+        tall = q.grouped_qmm(x, w, torch.tensor([0, 100, 190], dtype=torch.int32, device=dev))
+        low = q.grouped_qmm(x[90:150], w, torch.tensor([0, 10, 60], dtype=torch.int32, device=dev))
+        assert torch.equal(tall[90:150], low)
+
+
 def test_grouped_rows_are_their_own():
-    """A row's result is the same in any company (of the same tile height), NaN rows aside."""
+    """A row's result is the same in any company, NaN rows aside."""
     import bit_affine_quantized_qmv_amd as q
     dev = require_gpu()
     w = stack(70, 320, 64, 8, "fp16", 3, 1, dev)
