@@ -26,7 +26,9 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqmm.so")
 EXPORTS = ("qmm_abi_version", "qmm_last_error", "qmm_quantize", "qmv", "qmm_t", "qmm_plan", "qmm_gather_qmv",
            "qmm_dequantize", "qmm_embedding", "qmm_qmv_argmax", "qmm_qmv_argmax_noalloc", "qmm_topk",
            "qmm_qmv_topk", "qmm_kv_append", "qmm_kv_read", "qmm_kv_attend", "qmm_kv_attend_workspace_bytes", "qmm_sample", "qmm_moe",
-           "qmm_moe_workspace_bytes")
+           "qmm_moe_workspace_bytes", "qmm_tree_mask", "qmm_kv_attend_tree", "qmm_kv_attend_tree_workspace_bytes",
+           "qmm_tree_accept", "qmm_kv_move", "qmm_kv_copy_pages", "qmm_kv_fork", "qmm_kv_fork_workspace_bytes",
+           "qmm_grouped", "qmm_grouped_workspace_bytes", "qmm_moe_prompt", "qmm_moe_prompt_workspace_bytes")
 
 
 class TensorDesc(ctypes.Structure):
