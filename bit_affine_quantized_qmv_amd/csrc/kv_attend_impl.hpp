@@ -29,6 +29,7 @@
 #pragma once
 
 #include <cfloat>
+#include <type_traits>
 
 #include "device_common.hpp"
 #include "kv_cache.hpp"
@@ -96,6 +97,22 @@ __device__ inline bool length_bad(const AttendArgs& a, int len) {
   return len < 0 || len > a.max_length || (TREE && len > 0 && len < a.q_len);
 }
 
+// The sequence of a tree call's workgroups with blockIdx.y = at: the at-th longest, so that what
+// starts last is short (16 sequences of 512 to 8192 tokens, 128 query rows: 112 to 124 us; in the
+// order of the batch, their lengths rising, 151).  At most 64 sequences, one per lane, are
+// ordered: of more, each fills the chip for a smaller part of the call.
+__device__ inline int by_length(const AttendArgs& a, int at) {
+  if (a.batch > 64) return at;
+  const int i = threadIdx.x & 63, n = (int)a.batch;
+  const int mine = i < n ? a.lengths[i] : -1;
+  int rank = 0;
+  for (int j = 0; j < n; ++j) {
+    const int other = __builtin_amdgcn_readlane(mine, j);
+    rank += other > mine || (other == mine && j < i);
+  }
+  return __builtin_ctzll(__builtin_amdgcn_ballot_w64(i < n && rank == at));
+}
+
 // One side (K or V) of a 32-token step in registers: codes and (s, b) words of the lane's
 // tokens, for the two 16-token tiles.
 template <int D, int GS>
@@ -128,6 +145,8 @@ __device__ inline void store4(const AttendArgs& a, int64_t b, int head, int spli
 // step after it are looked up already.  Two tiles of 16 rows per wave would unpack each code
 // once for 32 rows, but their registers leave one or two waves per SIMD: slower at every size
 // measured (20 rows: 63 us against 42; 128 rows: 66 against 43; 8192 tokens, 8 heads of 128).
+// Trees of many query rows take them all the same (R = 2), where the other choice is a workgroup
+// of 256 rows.
 // What bounds it: a step is 384 vector instructions, about 1600 cycles, for 4.6 KB of codes and
 // scales, so at 5 TB/s the vector units are as busy as the memory; with lengths that differ,
 // what is left is the longest sequences' share.  Measured: 131071 tokens, 8 cached heads of
@@ -138,13 +157,13 @@ __device__ inline void store4(const AttendArgs& a, int64_t b, int head, int spli
 template <int D, int GS>
 constexpr int workgroups() { return D > 128 ? 1 : (D / GS == 1 ? 4 : (D / GS == 2 ? 3 : 2)); }
 
-template <class T, int D, int GS, bool TREE>
-__global__ __launch_bounds__(kThreads, (workgroups<D, GS>())) void attend_kernel(const AttendArgs a) {
+template <class T, int D, int GS, bool TREE, int R>
+__global__ __launch_bounds__(kThreads, (R > 1 ? 2 : workgroups<D, GS>())) void attend_kernel(const AttendArgs a) {
   constexpr int KC = D / 32;          // 32-element steps of a score; code words per lane and tile
   constexpr int NT = D / 16;          // 16-element output tiles
   constexpr int NG = D / GS;
   constexpr int CPG = GS / 32;
-  constexpr int kRows = 16;           // query rows per workgroup
+  constexpr int kRows = 16 * R;       // query rows per workgroup
   constexpr int kPitch = D + 4;       // LDS row of the merge, padded against bank conflicts
   using P = Bf16;                     // operands of the second product
 
@@ -152,7 +171,7 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS>())) void attend_kernel
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int split = blockIdx.z;
   const int head = blockIdx.x % a.c.heads, row_tile = blockIdx.x / a.c.heads;
-  const int64_t b = blockIdx.y;
+  const int64_t b = TREE ? by_length(a, blockIdx.y) : blockIdx.y;
   const int base = row_tile * kRows;
 
   int len = a.lengths[b];
@@ -174,10 +193,15 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS>())) void attend_kernel
   const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
   const float magnitude = __builtin_fabsf(a.scale_log2), scale = magnitude < FLT_MIN ? FLT_MIN : magnitude;
 
-  float m = kNone, l = 0.f, bsum[NG] = {};
-  f32x4 acc[NT];
+  float m[R], l[R], bsum[R][NG] = {};
+  f32x4 acc[R][NT];
 #pragma unroll
-  for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int k = 0; k < R; ++k) {
+    m[k] = kNone;
+    l[k] = 0.f;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[k][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
 
   // The page of a 16-token tile that starts at token t0, and the token's place in it.  Tiles
   // that no row sees read page 0 (their tokens are masked), and so do needed ones that have no
@@ -200,16 +224,16 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS>())) void attend_kernel
   const auto base_of = [&](const Place& p) -> const uint32_t* {
     return a.c.data + ((int64_t)(outside(p) ? 0 : p.page) * a.c.heads + head) * page_words;
   };
-  const int code_at = h * KC;
+  const uint32_t lane_k = (uint32_t)(col * (D / 8) + h * KC), lane_v = (uint32_t)((h * 16 + col) * KC), lane_sb = 4u * h;
   Side<D, GS> ks, vs;
   auto load_side = [&](Side<D, GS>& s, int tile, const uint32_t* p, int token, bool value) {
     if (value)
-      load_words<KC>(s.code[tile], p + (token / 4 + h) * (16 * KC) + col * KC);
+      load_words<KC>(s.code[tile], p + (int64_t)(token / 4) * (16 * KC) + lane_v);
     else
-      load_words<KC>(s.code[tile], p + (token + col) * (D / 8) + code_at);
-    const uint32_t* sb = p + (int64_t)a.c.page_size * (D / 8) + token + 4 * h;
+      load_words<KC>(s.code[tile], p + (int64_t)token * (D / 8) + lane_k);
+    const uint32_t* sb = p + (int64_t)a.c.page_size * (D / 8) + token;
 #pragma unroll
-    for (int g = 0; g < NG; ++g) load_words<4>(s.sb[tile][g], sb + g * a.c.page_size);
+    for (int g = 0; g < NG; ++g) load_words<4>(s.sb[tile][g], sb + (int64_t)g * a.c.page_size + lane_sb);
   };
   // the next step's tiles, and the pages of the step after it
   const uint32_t* base_next[2] = {nullptr, nullptr};
@@ -247,46 +271,58 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS>())) void attend_kernel
   }
 
   // query operands: column col is query row base + col (rows past the last repeat it and are not stored)
-  typename T::v8 q[KC];
-  float qsum[NG];
+  typename T::v8 q[R][KC];
+  float qsum[R][NG];
   const uint32_t one2 = T::pack2(1.0f, 1.0f);
   const u32x4 ones = {one2, one2, one2, one2};
-  const int row = min(base + col, a.rows - 1);
-  const int query = row / a.rep;
-  const uint16_t* qp = (const uint16_t*)a.q + b * a.q_batch_stride + (int64_t)query * a.q_token_stride +
-                       (int64_t)(head * a.rep + row - query * a.rep) * a.q_head_stride + 8 * h;
+  int row_lo[R], row_hi[R];
+  TreeRow tree[R];
 #pragma unroll
-  for (int c = 0; c < KC; ++c) q[c] = as_v8<T>(interleave_even_odd(*(const u32x4*)(qp + 32 * c) ^ flip));
+  for (int k = 0; k < R; ++k) {
+    const int row = min(base + 16 * k + col, a.rows - 1);
+    const int query = row / a.rep;
+    const uint16_t* qp = (const uint16_t*)a.q + b * a.q_batch_stride + (int64_t)query * a.q_token_stride +
+                         (int64_t)(head * a.rep + row - query * a.rep) * a.q_head_stride + 8 * h;
 #pragma unroll
-  for (int g = 0; g < NG; ++g) {
-    f32x4 d = {0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < KC; ++c) q[k][c] = as_v8<T>(interleave_even_odd(*(const u32x4*)(qp + 32 * c) ^ flip));
 #pragma unroll
-    for (int c = 0; c < CPG; ++c) d = T::mfma(as_v8<T>(ones), q[g * CPG + c], d);
-    qsum[g] = d[0];
-  }
-  const int row_hi = TREE ? off : (a.causal ? off + query + 1 : len);
-  int row_lo = a.window ? off + query - a.window + 1 : 0;
-  TreeRow tree;
-  if constexpr (TREE) {
-    tree.setup(a, b, query);
-    row_lo = a.window ? off + a.depth[b * a.q_len + query] - a.window + 1 : 0;
+    for (int g = 0; g < NG; ++g) {
+      f32x4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < CPG; ++c) d = T::mfma(as_v8<T>(ones), q[k][g * CPG + c], d);
+      qsum[k][g] = d[0];
+    }
+    row_hi[k] = TREE ? off : (a.causal ? off + query + 1 : len);
+    row_lo[k] = a.window ? off + query - a.window + 1 : 0;
+    if constexpr (TREE) {
+      tree[k].setup(a, b, query);
+      row_lo[k] = a.window ? off + a.depth[b * a.q_len + query] - a.window + 1 : 0;
+    }
   }
 
   for (int t0 = first; t0 < c1; t0 += stride) {
     const bool bad_now[2] = {bad_next[0], bad_next[1]};
-    // ---- scores: sc[i][r] of token t0 + 16 i + 4 h + r
-    float sc[2][4];
+    // ---- scores: sc[k][i][r] of token t0 + 16 i + 4 h + r
+    float sc[R][2][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        f32x4 d = {0.f, 0.f, 0.f, 0.f};
+        f32x4 d[R];
 #pragma unroll
-        for (int c = g * CPG; c < (g + 1) * CPG; ++c) d = T::mfma(as_v8<T>(codes4_to_v8<T>(ks.code[i][c])), q[c], d);
+        for (int k = 0; k < R; ++k) d[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = g * CPG; c < (g + 1) * CPG; ++c) {
+          const typename T::v8 codes = as_v8<T>(codes4_to_v8<T>(ks.code[i][c]));
+#pragma unroll
+          for (int k = 0; k < R; ++k) d[k] = T::mfma(codes, q[k][c], d[k]);
+        }
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float s = T::to_f32(ks.sb[i][g][r] & 0xFFFFu), kb = T::to_f32(ks.sb[i][g][r] >> 16);
-          sc[i][r] = __builtin_fmaf(s, d[r], g == 0 ? kb * qsum[0] : __builtin_fmaf(kb, qsum[g], sc[i][r]));
+#pragma unroll
+          for (int k = 0; k < R; ++k)
+            sc[k][i][r] = __builtin_fmaf(s, d[k][r], g == 0 ? kb * qsum[k][0] : __builtin_fmaf(kb, qsum[k][g], sc[k][i][r]));
         }
       }
     }
@@ -294,58 +330,80 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS>())) void attend_kernel
     load_k();
     find(t0 + 2 * stride);
     // ---- rows that do not see every token of the step, and tiles without a page of the pool
-    if (t0 < lo_max || t0 + kStep > hi_min || bad_now[0] || bad_now[1]) {
+    const bool edge = t0 < lo_max || t0 + kStep > hi_min || bad_now[0] || bad_now[1];
+    if (edge) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint32_t nodes = TREE && t0 + kStep > off ? tree.bits(t0 + 16 * i + 4 * h - off) : 0u;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int token = t0 + 16 * i + 4 * h + r;
-          const bool seen = TREE && token >= off ? ((nodes >> r) & 1u) && token < len : token >= row_lo && token < row_hi;
-          sc[i][r] = seen ? (bad_now[i] ? __builtin_nanf("") : sc[i][r]) : -__builtin_inff();
+        for (int k = 0; k < R; ++k) {
+          const uint32_t nodes = TREE && t0 + kStep > off ? tree[k].bits(t0 + 16 * i + 4 * h - off) : 0u;
 #pragma unroll
-          for (int g = 0; g < NG; ++g) vs.sb[i][g][r] = seen ? vs.sb[i][g][r] : 0u;   // whatever it holds, it adds nothing
+          for (int r = 0; r < 4; ++r) {
+            const int token = t0 + 16 * i + 4 * h + r;
+            const bool seen =
+                TREE && token >= off ? ((nodes >> r) & 1u) && token < len : token >= row_lo[k] && token < row_hi[k];
+            sc[k][i][r] = seen ? (bad_now[i] ? __builtin_nanf("") : sc[k][i][r]) : -__builtin_inff();
+            if constexpr (R == 1) {
+#pragma unroll
+              for (int g = 0; g < NG; ++g) vs.sb[i][g][r] = seen ? vs.sb[i][g][r] : 0u;   // whatever it holds, it adds nothing
+            }
+          }
         }
       }
     }
     // ---- probabilities
-    float top = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3]));
-    top = fmaxf(top, fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3]))) * scale;
-    if (__builtin_amdgcn_ballot_w64(top > m + kSlack) != 0ull) {
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      const float raised = fmaxf(m, top);
-      const float f = __builtin_amdgcn_exp2f(m - raised);
-      m = raised;
-      l *= f;
 #pragma unroll
-      for (int g = 0; g < NG; ++g) bsum[g] *= f;
+    for (int k = 0; k < R; ++k) {
+      float(&x)[2][4] = sc[k];
+      float top = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3]));
+      top = fmaxf(top, fmaxf(fmaxf(x[1][0], x[1][1]), fmaxf(x[1][2], x[1][3]))) * scale;
+      if (__builtin_amdgcn_ballot_w64(top > m[k] + kSlack) != 0ull) {
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float raised = fmaxf(m[k], top);
+        const float f = __builtin_amdgcn_exp2f(m[k] - raised);
+        m[k] = raised;
+        l[k] *= f;
 #pragma unroll
-      for (int i = 0; i < NT; ++i) acc[i] *= f;
-    }
+        for (int g = 0; g < NG; ++g) bsum[k][g] *= f;
 #pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      float& p = sc[n >> 2][n & 3];
-      p = __builtin_amdgcn_exp2f(__builtin_fmaf(p, scale, -m));
-      l += p;
+        for (int i = 0; i < NT; ++i) acc[k][i] *= f;
+      }
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        float& p = x[n >> 2][n & 3];
+        p = __builtin_amdgcn_exp2f(__builtin_fmaf(p, scale, -m[k]));
+        l[k] += p;
+      }
     }
     // ---- second product, group by group
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      float x[8];
+      u32x4 hi[R], lo[R];
 #pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        const uint32_t sb = vs.sb[n >> 2][g][n & 3];
-        x[n] = sc[n >> 2][n & 3] * T::to_f32(sb & 0xFFFFu);
-        bsum[g] = __builtin_fmaf(sc[n >> 2][n & 3], T::to_f32(sb >> 16), bsum[g]);
-      }
-      u32x4 hi, lo;
+      for (int k = 0; k < R; ++k) {
+        float x[8];
+        const auto weighted = [&](auto guarded) {
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        uint32_t uh, ul;
-        split2(x[2 * n], x[2 * n + 1], &uh, &ul);
-        hi[n] = uh;
-        lo[n] = ul;
+          for (int n = 0; n < 8; ++n) {
+            // (a token that only the wave's other rows see adds nothing, whatever it holds)
+            const float p = sc[k][n >> 2][n & 3];
+            const uint32_t sb = decltype(guarded)::value && p == 0.f ? 0u : vs.sb[n >> 2][g][n & 3];
+            x[n] = p * T::to_f32(sb & 0xFFFFu);
+            bsum[k][g] = __builtin_fmaf(p, T::to_f32(sb >> 16), bsum[k][g]);
+          }
+        };
+        if (R > 1 && edge)
+          weighted(std::true_type{});
+        else
+          weighted(std::false_type{});
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          uint32_t uh, ul;
+          split2(x[2 * n], x[2 * n + 1], &uh, &ul);
+          hi[k][n] = uh;
+          lo[k][n] = ul;
+        }
       }
 #pragma unroll
       for (int j = g * CPG; j < (g + 1) * CPG; ++j) {
@@ -354,8 +412,11 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS>())) void attend_kernel
         for (int n = 0; n < 2; ++n) {
           const uint32_t e0 = (n ? w0 >> 4 : w0) & 0x0F0F0F0Fu, e1 = (n ? w1 >> 4 : w1) & 0x0F0F0F0Fu;
           const u32x4 vc = {P::fp8x2_lo(e0), P::fp8x2_hi(e0), P::fp8x2_lo(e1), P::fp8x2_hi(e1)};
-          acc[2 * j + n] = P::mfma(as_v8<P>(vc), as_v8<P>(lo), acc[2 * j + n]);
-          acc[2 * j + n] = P::mfma(as_v8<P>(vc), as_v8<P>(hi), acc[2 * j + n]);
+#pragma unroll
+          for (int k = 0; k < R; ++k) {
+            acc[k][2 * j + n] = P::mfma(as_v8<P>(vc), as_v8<P>(lo[k]), acc[k][2 * j + n]);
+            acc[k][2 * j + n] = P::mfma(as_v8<P>(vc), as_v8<P>(hi[k]), acc[k][2 * j + n]);
+          }
         }
       }
     }
@@ -363,32 +424,38 @@ __global__ __launch_bounds__(kThreads, (workgroups<D, GS>())) void attend_kernel
   }
 
   // ---- the lanes' shares of the sums, and the bias term: element d = 16 i + 4 h + r of row col
-  l += __shfl_xor(l, 16);
-  l += __shfl_xor(l, 32);
 #pragma unroll
-  for (int g = 0; g < NG; ++g) {
-    bsum[g] += __shfl_xor(bsum[g], 16);
-    bsum[g] += __shfl_xor(bsum[g], 32);
-  }
+  for (int k = 0; k < R; ++k) {
+    l[k] += __shfl_xor(l[k], 16);
+    l[k] += __shfl_xor(l[k], 32);
 #pragma unroll
-  for (int i = 0; i < NT; ++i) acc[i] += bsum[i * 16 / GS];
-  if (TREE && !tree.there) {         // its scores were of tokens that it does not see
-    l = 0.f;
-    m = kNone;
+    for (int g = 0; g < NG; ++g) {
+      bsum[k][g] += __shfl_xor(bsum[k][g], 16);
+      bsum[k][g] += __shfl_xor(bsum[k][g], 32);
+    }
 #pragma unroll
-    for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
-  if (bad) {
-    l = __builtin_nanf("");
-    m = 0.f;
+    for (int i = 0; i < NT; ++i) acc[k][i] += bsum[k][i * 16 / GS];
+    if (TREE && !tree[k].there) {    // its scores were of tokens that it does not see
+      l[k] = 0.f;
+      m[k] = kNone;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) acc[k][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    if (bad) {
+      l[k] = __builtin_nanf("");
+      m[k] = 0.f;
+    }
   }
 
   // ---- the four waves' sums meet in LDS
   __shared__ float o_s[kWaves][kRows][kPitch];
   __shared__ float2 ml_s[kWaves][kRows];
 #pragma unroll
-  for (int i = 0; i < NT; ++i) *(f32x4*)&o_s[wave][col][16 * i + 4 * h] = acc[i];
-  if (h == 0) ml_s[wave][col] = float2{m, l};
+  for (int k = 0; k < R; ++k) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) *(f32x4*)&o_s[wave][16 * k + col][16 * i + 4 * h] = acc[k][i];
+    if (h == 0) ml_s[wave][16 * k + col] = float2{m[k], l[k]};
+  }
   __syncthreads();
   const int64_t row0 = (b * a.c.heads + head) * a.rows;
   float* part_ml = a.part + a.batch * a.c.heads * a.rows * a.splits * D;
@@ -834,10 +901,13 @@ hipError_t launch_shape(const AttendArgs& a, const AttendPlan& p, hipStream_t st
   // longest have work in the last splits, so splits are the slowest index: with splits fastest
   // (4 of them), two XCDs had every first split.
   const dim3 grid((unsigned)(a.c.heads * p.row_tiles), (unsigned)a.batch, (unsigned)p.splits);
-  if (p.by_rows)
+  if (p.form == kRowsForm)
     hipLaunchKernelGGL((attend_rows_kernel<T, D, GS, TREE>), grid, dim3(64 * row_waves(D)), 0, stream, a);
-  else
-    hipLaunchKernelGGL((attend_kernel<T, D, GS, TREE>), grid, dim3(kThreads), 0, stream, a);
+  else if (p.form == kPairsForm) {
+    if constexpr (TREE && has_pairs(D, GS))
+      hipLaunchKernelGGL((attend_kernel<T, D, GS, TREE, 2>), grid, dim3(kThreads), 0, stream, a);
+  } else
+    hipLaunchKernelGGL((attend_kernel<T, D, GS, TREE, 1>), grid, dim3(kThreads), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   hipLaunchKernelGGL((attend_join_kernel<T, D, TREE>), dim3((unsigned)(a.batch * a.c.heads * a.rows)), dim3(kThreads), 0,

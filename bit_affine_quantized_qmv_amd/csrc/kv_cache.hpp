@@ -131,14 +131,20 @@ constexpr int64_t kMaxCopyBlocks = 0xFFFFFFFFll / kCopyThreads;
 hipError_t launch_append(const AppendArgs& a, hipStream_t stream);
 hipError_t launch_read(const ReadArgs& a, hipStream_t stream);
 
+// What the waves of a workgroup share out: the tokens, for 16 query rows or (trees) for two tiles
+// of 16, or the query rows.
+enum AttendForm { kTokensForm, kPairsForm, kRowsForm };
+// Two tiles' registers fit two waves per SIMD.
+constexpr bool has_pairs(int head_dim, int group) { return head_dim == 128 && group >= 64; }
+
 // Splits of the token range and tokens per split of an attention call (host only).
 struct AttendPlan {
-  int32_t by_rows;        // the workgroup's waves take different query rows (else tokens)
+  int32_t form;           // AttendForm
   int32_t row_tiles;      // workgroups along the rows of one cached head
   int32_t chunk;
   int32_t splits;
 };
-AttendPlan plan_attend(int64_t batch, const CacheArgs& c, int64_t rows, int64_t range);
+AttendPlan plan_attend(int64_t batch, const CacheArgs& c, int64_t rows, int64_t range, bool tree);
 
 hipError_t launch_attend_bf16(const AttendArgs& a, const AttendPlan& p, hipStream_t stream);
 hipError_t launch_attend_fp16(const AttendArgs& a, const AttendPlan& p, hipStream_t stream);

@@ -101,36 +101,46 @@ int64_t part_floats(const AttendArgs& a, int64_t splits) {
 // elements in groups of 64: 53 us against 63 with three); more do not (131071 tokens, one group:
 // 35 us, with six 39).  Each split has at least one step of every wave (128 tokens), or 512 tokens
 // in the prompt form, where a split's sums are large.
+// Trees of 256 query rows and more, 128 elements in one or two groups, take the first form with two
+// tiles of 16 rows per wave, two workgroups per CU: their workgroups fill the chip where 256 rows
+// in one leave half of it idle (group 64, batch 16, 2048 tokens, 256 rows 98 us against 123; batch
+// 1, 8192 tokens, 256 rows 42 / 59; one group, 512 rows, 131071 tokens 526 / 600; the other way
+// only for a single long sequence in two groups: 65536 tokens, 256 rows 182 / 162).  With fewer
+// rows they gain where lengths are alike (128 rows, batch 16, 8192 tokens 176 us / 212) and lose
+// where they differ (121 / 112) or three do not fill a CU (batch 12: 118 / 100).
 namespace {
 
 struct Shape {
-  int32_t by_rows, row_tiles;
+  AttendForm form;
+  int32_t row_tiles;
   int64_t step, want;
 };
 
-Shape shape_of(int64_t batch, int heads, int head_dim, int group, int64_t rows) {
+Shape shape_of(int64_t batch, int heads, int head_dim, int group, int64_t rows, bool tree) {
   Shape s{};
-  s.by_rows = rows >= (head_dim == 128 ? 256 : 1024);
-  const int64_t wg_rows = s.by_rows ? (head_dim == 256 ? 128 : 256) : 16;
+  s.form = rows < (head_dim == 128 ? 256 : 1024) ? kTokensForm
+           : tree && has_pairs(head_dim, group)  ? kPairsForm
+                                                 : kRowsForm;
+  const int64_t wg_rows = s.form == kRowsForm ? (head_dim == 256 ? 128 : 256) : (s.form == kPairsForm ? 32 : 16);
   s.row_tiles = (int32_t)((rows + wg_rows - 1) / wg_rows);
-  s.step = s.by_rows ? 512 : 128;
-  const int64_t per_cu = s.by_rows || head_dim == 256 ? 1 : (head_dim == 4 * group ? 2 : 4);
+  s.step = s.form == kRowsForm ? 512 : 128;
+  const int64_t per_cu = s.form == kRowsForm || head_dim == 256 ? 1 : (head_dim == 4 * group || s.form == kPairsForm ? 2 : 4);
   s.want = std::max<int64_t>(1, 256 * per_cu / std::max<int64_t>(1, batch * heads * s.row_tiles));
   return s;
 }
 
 }  // namespace
 
-AttendPlan plan_attend(int64_t batch, const CacheArgs& c, int64_t rows, int64_t range) {
-  const Shape s = shape_of(batch, c.heads, c.head_dim, c.group_size, rows);
+AttendPlan plan_attend(int64_t batch, const CacheArgs& c, int64_t rows, int64_t range, bool tree) {
+  const Shape s = shape_of(batch, c.heads, c.head_dim, c.group_size, rows, tree);
   const int64_t steps = std::max<int64_t>(1, (range + s.step - 1) / s.step);
   const int64_t per = std::max<int64_t>(1, (steps + s.want - 1) / s.want);
-  return AttendPlan{s.by_rows, s.row_tiles, (int32_t)(per * s.step), (int32_t)((steps + per - 1) / per)};
+  return AttendPlan{s.form, s.row_tiles, (int32_t)(per * s.step), (int32_t)((steps + per - 1) / per)};
 }
 
 // Splits that no shorter range of the same call exceeds.
-static int64_t most_splits(const AttendArgs& a) {
-  const Shape s = shape_of(a.batch, a.c.heads, a.c.head_dim, a.c.group_size, a.rows);
+static int64_t most_splits(const AttendArgs& a, bool tree) {
+  const Shape s = shape_of(a.batch, a.c.heads, a.c.head_dim, a.c.group_size, a.rows, tree);
   return std::min<int64_t>(s.want, std::max<int64_t>(1, (a.max_length + s.step - 1) / s.step));
 }
 
@@ -153,7 +163,7 @@ static int32_t run_attend(AttendArgs& a, void* out, void* workspace, int64_t wor
   if ((uintptr_t)a.table % 4 || (uintptr_t)a.lengths % 4)
     return report(QMM_ERR_ALIGN, "kv_attend: block_table and lengths must be 4-byte aligned");
   const AttendPlan p =
-      plan_attend(a.batch, a.c, a.rows, token_range(a));
+      plan_attend(a.batch, a.c, a.rows, token_range(a), a.mask != nullptr);
   if ((int64_t)a.c.heads * p.row_tiles > 65535)
     return report(QMM_ERR_SHAPE, "kv_attend: too many query rows per sequence");
   const int64_t need = part_floats(a, p.splits) * 4;
@@ -236,7 +246,7 @@ int64_t qmm_kv_attend_workspace_bytes(const qmm_kv_cache_t* cache, const qmm_kv_
     const int32_t rc = kv::check_attend(cache, args, false, &a);
     if (rc != QMM_OK) return rc;
     report(QMM_OK, "");
-    return kv::part_floats(a, kv::most_splits(a)) * 4;
+    return kv::part_floats(a, kv::most_splits(a, false)) * 4;
   });
 }
 
@@ -258,7 +268,7 @@ int64_t qmm_kv_attend_tree_workspace_bytes(const qmm_kv_cache_t* cache, const qm
     const int32_t rc = kv::check_tree(cache, args, false, &a);
     if (rc != QMM_OK) return rc;
     report(QMM_OK, "");
-    return kv::part_floats(a, kv::most_splits(a)) * 4;
+    return kv::part_floats(a, kv::most_splits(a, true)) * 4;
   });
 }
 

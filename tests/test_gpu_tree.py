@@ -168,6 +168,45 @@ def test_attend_tree_unseen_nodes_that_are_not_finite():
         assert (np.abs(y[0] - ref) <= tol).all() and (y[0, 9] == 0).all()
 
 
+def test_attend_tree_nodes_that_are_not_finite_reach_their_descendants_only():
+    import bit_affine_quantized_qmv_amd as q
+    nodes, dim = 34, 128
+    for rep, group in ((2, 64), (8, 64), (16, 128)):     # one tile of 16 rows per wave, and two
+        s = Setup([120], 1, dim, group, 16, "bf16", seed=14)
+        dev = s.len_dev.device
+        parents = random_parents(1, nodes, 21)
+        row = parents[0].tolist()
+        lost = next(i for i in range(3, nodes) if sum(i in path_up(row, j) for j in range(nodes)) >= 3)
+        bad = torch.full((1, 1, dim), float("inf"), dtype=torch.bfloat16, device=dev)
+        q.kv_append(s.cache, bad, bad, s.slots[120 - nodes + lost:120 - nodes + lost + 1])
+        mask, _ = q.tree_mask(parents.to(dev))
+        queries = _rows((1, nodes, rep, dim), "bf16", 6, loud=False)
+        y = values(q.kv_attend_tree(queries.to(dev), s.cache, s.table, s.len_dev, mask))[0]
+        ref, tol = masked_reference(queries[0], s.k[0], s.v[0], seen_by(row, 120, 0), group, "bf16", dim ** -0.5,
+                                    nodes * rep >= 256)
+        for i in range(nodes):
+            if lost in path_up(row, i):
+                assert np.isnan(y[i]).all(), i
+            else:
+                assert (np.abs(y[i] - ref[i]) <= tol[i]).all(), i
+
+
+def test_attend_tree_of_many_sequences_in_any_order_of_lengths():
+    import bit_affine_quantized_qmv_amd as q
+    nodes, heads, rep, dim = 5, 1, 2, 64
+    for batch in (64, 65, 130):
+        lengths = [(0 if i % 9 == 4 else nodes + (37 * i) % 61) for i in range(batch)]
+        s = Setup(lengths, heads, dim, 32, 16, "bf16", seed=batch)
+        dev = s.len_dev.device
+        parents = random_parents(batch, nodes, 3)
+        mask, depth = q.tree_mask(parents.to(dev))
+        queries = _rows((batch, nodes, heads * rep, dim), "bf16", 6, loud=False).to(dev)
+        y = q.kv_attend_tree(queries, s.cache, s.table, s.len_dev, mask, depth)
+        for b in range(batch):
+            one = q.kv_attend_tree(queries[b:b + 1], s.cache, s.table[b:b + 1], s.len_dev[b:b + 1], mask[b:b + 1])
+            assert torch.equal(one[0], y[b]), b
+
+
 def test_attend_tree_strides_workspace_and_stream():
     import bit_affine_quantized_qmv_amd as q
     nodes, heads, rep, dim = 24, 2, 2, 64
