@@ -178,6 +178,7 @@ __global__ __launch_bounds__(kThreads) void sum_kernel(const SumArgs a) {
   const int n = 4 * (int)(blockIdx.x * kThreads + threadIdx.x), t = blockIdx.y;
   if (n >= a.hidden) return;
   const float* o = a.out + (int64_t)t * a.top_k * a.hidden + n;
+  const int64_t to_split = (int64_t)a.tokens * a.top_k * a.hidden;
   const float* share = a.share + t * a.top_k;
   f32x4 v = {0.f, 0.f, 0.f, 0.f};
   float sum = 0.f;
@@ -190,6 +191,13 @@ __global__ __launch_bounds__(kThreads) void sum_kernel(const SumArgs a) {
       const int at = min(i0 + i, a.top_k - 1);
       w[i] = *(const f32x4*)(o + (int64_t)at * a.hidden);
       f[i] = share[at];
+    }
+    for (int s = 1; s < a.splits; ++s) {
+      f32x4 u[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) u[i] = *(const f32x4*)(o + s * to_split + (int64_t)min(i0 + i, a.top_k - 1) * a.hidden);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) w[i] += u[i];
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {

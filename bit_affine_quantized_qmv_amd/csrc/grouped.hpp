@@ -17,6 +17,7 @@ constexpr int kStepK = 128;           // rows of staged activations are whole st
 constexpr int kPlanes = 3;            // bfloat16 parts of a group's sum of activations
 constexpr int kSumPad = 32;           // groups per row of the sums, rounded up to this
 constexpr int kMaxPairs = 1 << 20;    // rows of one call
+constexpr int kSplitGroups = 32;      // a split of the columns is whole runs of so many groups
 
 // What becomes of a product x W_e^T.
 enum Kind {
@@ -60,7 +61,12 @@ struct Args {
   int32_t h_sum_groups;
   int32_t h_group;
   int32_t h_bits;            // width and group size of the weights that take h
-  float* out;                // kDown: [pair][n]
+  // kDown: the columns are shared out over `splits` workgroups, split_cols each (whole runs of
+  // kSplitGroups groups, or all of them), which leave a result of their own each.
+  int32_t splits;
+  int32_t split_cols;
+  float* out;                // kDown: [split][pair][n]
+  int64_t out_split;         // elements from one split to the next
 };
 
 // x as the products take it, the sums of its groups, and the tiles of given offsets: one kernel.
@@ -109,7 +115,8 @@ struct SumArgs {
   int32_t renormalize;
   int32_t hidden;            // a multiple of 4
   int32_t dtype;
-  const float* out;          // [tokens * top_k][hidden]
+  int32_t splits;
+  const float* out;          // [split][tokens * top_k][hidden]
   const float* share;        // [tokens * top_k]
   uint16_t* y;               // [tokens][y_stride]
   int64_t y_stride;
@@ -118,7 +125,7 @@ struct SumArgs {
 hipError_t launch_sum(const SumArgs& a, hipStream_t stream);
 hipError_t launch_prepare(const PrepareArgs& a, hipStream_t stream);
 hipError_t launch_route(const RouteArgs& r, const PrepareArgs& p, hipStream_t stream);
-// tile_rows: 32 or 64
+// tile_rows: 16, 32 or 64
 hipError_t launch_b4(const Args& a, Kind kind, int dtype, int tile_rows, hipStream_t stream);
 hipError_t launch_b8(const Args& a, Kind kind, int dtype, int tile_rows, hipStream_t stream);
 hipError_t launch_bn(const Args& a, Kind kind, int dtype, int tile_rows, hipStream_t stream);

@@ -15,18 +15,42 @@ namespace {
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
-// Rows per tile.  Taller ones unpack a code for more rows, lower ones leave three workgroups per CU
-// instead of two and less of a tile empty.  Measured, 32 rows against 64, us for the product of 64
-// experts of [1024, 2048] in 4 bits: 24 rows per expert 30 / 40, 64 rows 41 / 43, 96 rows 55 / 47, 160 rows
-// 78 / 70; the layer of 64 experts of [704, 1408] in 8 bits: 24 rows 74 / 80, 64 rows 120 / 136, 96 rows
-// 149 / 141.
-int tile_rows_of(int64_t rows, int64_t experts) { return rows >= 80 * experts ? 64 : 32; }
+// Rows per tile.  Taller ones unpack a code for more rows, lower ones leave more workgroups per CU (four
+// of 16 rows, three of 32, two of 64) and less of a tile empty.  Measured, 32 rows against 64, us for
+// the product of 64 experts of [1024, 2048] in 4 bits: 24 rows per expert 30 / 40, 64 rows 41 / 43, 96
+// rows 55 / 47, 160 rows 78 / 70; the layer of 64 experts of [704, 1408] in 8 bits: 24 rows 74 / 80, 64
+// rows 120 / 136, 96 rows 149 / 141.  16 rows against 32, the gated product of 8 experts of [14336, 4096]:
+// 2 rows per expert 137 / 152, 8 rows 150 / 153, 16 rows 175 / 156; of 128 experts of [704, 1408]: 3
+// rows 32 / 35, 6 rows 34 / 36, 12 rows 39 / 38.
+int tile_rows_of(int64_t rows, int64_t experts) {
+  return rows >= 80 * experts ? 64 : (rows <= 8 * experts ? 16 : 32);
+}
+// Workgroups of tiles of so many rows that the chip holds.
+int64_t slots_of(int tile_rows) { return tile_rows == 16 ? 1024 : (tile_rows == 32 ? 768 : 512); }
 // Tiles at most: a part of a tile for each expert with rows.
 int64_t max_tiles_of(int64_t rows, int64_t experts) {
-  return rows / 32 + std::min(rows, experts);
+  return rows / 16 + std::min(rows, experts);
 }
 
 int64_t sum_groups_of(int64_t k, int64_t group) { return round_up(k / group, kSumPad); }
+// Splits of the second product's columns: while `tiles` times `blocks` workgroups leave half of the chip's
+// slots empty, as many as fill them, of whole runs of groups.  (A few rows of 14336 columns, 8 experts
+// of [4096, 14336]: 183 us in one piece, 80 in four.)
+struct Splits {
+  int64_t count, cols;
+};
+Splits splits_of(int64_t tiles, int64_t blocks, int tile_rows, int64_t k, int64_t group) {
+  const int64_t run = kSplitGroups * group, runs = (k + run - 1) / run;
+  const int64_t want = std::max<int64_t>(1, std::min(runs, slots_of(tile_rows) / (tiles * blocks)));
+  const int64_t per = (runs + want - 1) / want;
+  return want == 1 ? Splits{1, k} : Splits{(runs + per - 1) / per, per * run};
+}
+// Bytes of their results, [split][pair][n], at most: several splits have no more rows and columns than
+// all slots' tiles.
+int64_t out_bytes(int64_t pairs, int64_t n, int64_t k) {
+  const int64_t runs = (k + kSplitGroups * 32 - 1) / (kSplitGroups * 32);
+  return align256(4 * std::max(pairs * n, std::min(runs * pairs * n, (int64_t)512 * 64 * kBlockN)));
+}
 // Bytes of the staged activations, and of the sums of `rows` rows, whatever the group size.
 int64_t staged_bytes(int64_t rows, int64_t k) { return align256(2 * rows * round_up(k, kStepK)); }
 int64_t sums_bytes(int64_t rows, int64_t k) { return align256(rows * kPlanes * 2 * round_up((k + 31) / 32, kSumPad)); }
@@ -86,7 +110,7 @@ LayerBytes layer_bytes(int64_t tokens, int64_t experts, int64_t top_k, int64_t h
                     sums_bytes(tokens, hidden),
                     align256(4 * n * cols),
                     sums_bytes(n, cols),
-                    align256(4 * n * hidden)};
+                    out_bytes(n, hidden, inter)};
 }
 
 }  // namespace
@@ -290,10 +314,14 @@ int32_t qmm_moe_prompt(const qmm_moe_t* m, void* y, void* workspace, int64_t wor
     d.pairs = r.pairs;
     d.top_k = m->top_k;
     d.out = (float*)take(b.out);
+    const grouped::Splits split = grouped::splits_of(d.max_tiles, d.n_blocks, tile_rows, inter, down.group_size);
+    d.splits = (int32_t)split.count;
+    d.split_cols = (int32_t)split.cols;
+    d.out_split = n * hidden;
     if ((int64_t)g.max_tiles * std::max(g.n_blocks, d.n_blocks) >= (1 << 24))
       return report(QMM_ERR_SHAPE, "moe_prompt: tokens * top_k * max(hidden, inter) too large for one call");
 
-    const grouped::SumArgs sum{r.tokens,       m->top_k, r.renormalize, (int32_t)hidden, m->dtype, d.out,
+    const grouped::SumArgs sum{r.tokens,       m->top_k, r.renormalize, (int32_t)hidden, m->dtype, d.splits, d.out,
                                r.pair_share, (uint16_t*)y, m->y_stride};
 
     hipStream_t s = (hipStream_t)stream;

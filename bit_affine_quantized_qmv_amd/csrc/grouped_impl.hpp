@@ -102,7 +102,7 @@ struct Codes {
 typedef uint32_t u32x4_by4 __attribute__((ext_vector_type(4), aligned(4)));
 
 template <class T, class X, int BITS, int GS, int FM, int KIND>
-__global__ __launch_bounds__(kThreads, FM == 2 ? 3 : 2) void grouped_kernel(const Args a) {
+__global__ __launch_bounds__(kThreads, FM == 1 ? 4 : (FM == 2 ? 3 : 2)) void grouped_kernel(const Args a) {
   constexpr int PLANES = KIND == kDown ? 2 : 1;
   constexpr bool kLds = BITS == 4 || BITS == 8;           // other widths: codes from memory to registers
   // columns of a step: what leaves room for two workgroups per CU
@@ -110,7 +110,7 @@ __global__ __launch_bounds__(kThreads, FM == 2 ? 3 : 2) void grouped_kernel(cons
   constexpr int MS = STEP / 32;
   constexpr int kGroupSteps = GS == 0 ? 1 : GS / 32;      // matrix steps of a group
   constexpr int kHalves = kGroupSteps > MS ? kGroupSteps / MS : 1;   // steps of a group
-  constexpr int kDma = PLANES * (STEP / 64) * (FM / 2);   // direct loads of activations per wave and step
+  constexpr int kLoads = PLANES * (STEP / 64) * 2 * FM;   // direct loads of activations per step
   using L = Shared<FM, PLANES, STEP>;
   using C = Codes<kLds ? BITS : 4, GS == 0 ? 32 : GS, STEP>;
   __shared__ u32x4 as0[L::kEntries], as1[L::kEntries];
@@ -142,7 +142,10 @@ __global__ __launch_bounds__(kThreads, FM == 2 ? 3 : 2) void grouped_kernel(cons
   };
   const auto stack = [&](int j) -> const Stack& { return a.w[kTwo && j >= TN / 2 ? 1 : 0]; };
   const int group_shift = __builtin_ctz((unsigned)a.w[0].group_size), groups = a.k >> group_shift;
-  const int steps = (a.k + STEP - 1) / STEP;
+  // the steps of this split
+  const int all_steps = (a.k + STEP - 1) / STEP;
+  const int first_step = KIND == kDown ? (int)blockIdx.y * (a.split_cols / STEP) : 0;
+  const int steps = KIND == kDown ? min(all_steps, first_step + (a.split_cols + STEP - 1) / STEP) : all_steps;
 
   // ---- codes
   __amdgpu_buffer_rsrc_t w_rs[2];
@@ -236,21 +239,23 @@ __global__ __launch_bounds__(kThreads, FM == 2 ? 3 : 2) void grouped_kernel(cons
   const uint32_t x_bytes = KIND == kGated ? a.x_bytes : (uint32_t)(tile.rows * a.x_stride * 2);
   const __amdgpu_buffer_rsrc_t x_rs = decode::make_rsrc(x_base, x_bytes);
   // load d of the wave: 8 rows of one half and plane; the wave's rows are the same in all of them
-  constexpr int kMine = FM / 2;                            // octets of rows of the wave
+  constexpr int kMine = FM == 4 ? 2 : 1;                   // octets of rows of the wave
+  const auto octet = [&](int u) { return FM == 1 ? wave & 1 : wave + 4 * u; };
   uint32_t x_off[kMine];                                   // of the lane's rows and chunk
 #pragma unroll
   for (int u = 0; u < kMine; ++u) {
-    const int m = 8 * (wave + 4 * u) + (lane >> 3);
+    const int m = 8 * octet(u) + (lane >> 3);
     const int chunk = (lane & 7) ^ C::x_place(m);
     x_off[u] = kPast;
     if (m < tile.rows) x_off[u] = (uint32_t)((KIND == kGated ? x_row(m) : m) * a.x_stride * 2) + 16 * chunk;
   }
   const auto load_x = [&](int t, u32x4* buf) {
 #pragma unroll
-    for (int d = 0; d < kDma; ++d) {
-      const int u = d % kMine, half = d / kMine % (STEP / 64), p = d / kMine / (STEP / 64);
-      load_to_lds(x_rs, buf + (p * (STEP / 64) + half) * L::kHalf + 64 * (wave + 4 * u), x_off[u],
-                  2 * (t * STEP + 64 * half + p * (int)a.x_plane));
+    for (int d = 0; d < (kLoads + 3) / 4; ++d) {
+      if (kLoads < 4 && wave >= kLoads) break;
+      const int u = d % kMine, part = FM == 1 ? 2 * d + (wave >> 1) : d / kMine;
+      const int half = part % (STEP / 64), p = part / (STEP / 64);
+      load_to_lds(x_rs, buf + part * L::kHalf + 64 * octet(u), x_off[u], 2 * (t * STEP + 64 * half + p * (int)a.x_plane));
     }
   };
   const int x_entry = C::lane_half(lg) * L::kHalf + 8 * col, x_chunk = C::lane_chunk(lg) ^ C::x_place(col);
@@ -262,14 +267,14 @@ __global__ __launch_bounds__(kThreads, FM == 2 ? 3 : 2) void grouped_kernel(cons
 #pragma unroll
     for (int i = 0; i < FM; ++i) acc[j][i] = part[j][i] = zero4;
 
-  load_scales(0);
-  load_x(0, as0);
-  load_codes(0);
+  load_scales((first_step * STEP) >> group_shift);
+  load_x(first_step, as0);
+  load_codes(first_step / C::kBlockSteps);
   if constexpr (!kLds) {
 #pragma unroll
     for (int j = 0; j < TN; ++j)
 #pragma unroll
-      for (int c = 0; c < MS; ++c) load_generic(j, c, 0);
+      for (int c = 0; c < MS; ++c) load_generic(j, c, first_step);
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   lds_barrier();
@@ -398,20 +403,21 @@ __global__ __launch_bounds__(kThreads, FM == 2 ? 3 : 2) void grouped_kernel(cons
   };
   using First = std::integral_constant<int, 0>;
   using Second = std::integral_constant<int, 1>;
-  int t = 0;
+  int t = first_step;
   for (; t + 1 < steps; t += 2) {
     step(t, as0, as1, First{});
     step(t + 1, as1, as0, Second{});
   }
   if (t < steps) step(t, as0, as1, First{});
 
-  // ---- biases: 32 groups at a time
+  // ---- biases: 32 groups at a time, what a split has whole runs of
   {
     const uint16_t* sum_rows[FM];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
       sum_rows[i] = a.sums + x_row(min(16 * i + col, tile.rows - 1)) * (kPlanes * (int64_t)a.sum_groups) + 8 * lg;
-    for (int g0 = 0; g0 < groups; g0 += 32) {
+    const int last = min(groups, (steps * STEP) >> group_shift);
+    for (int g0 = (first_step * STEP) >> group_shift; g0 < last; g0 += kSplitGroups) {
       bf16x8 sv[kPlanes][FM];
 #pragma unroll
       for (int p = 0; p < kPlanes; ++p)
@@ -463,7 +469,7 @@ __global__ __launch_bounds__(kThreads, FM == 2 ? 3 : 2) void grouped_kernel(cons
       for (int r = 0; r < 4; ++r) {
         const int m = 16 * i + 4 * lg + r;
         if (m >= tile.rows) continue;
-        float* o = a.out + (int64_t)a.pairs[tile.first + m] * a.n;
+        float* o = a.out + blockIdx.y * a.out_split + (int64_t)a.pairs[tile.first + m] * a.n;
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
           const int n = weight_row(j) + col;
@@ -561,11 +567,13 @@ __global__ __launch_bounds__(kThreads, FM == 2 ? 3 : 2) void grouped_kernel(cons
 
 template <class T, class X, int BITS, int GS, int KIND>
 hipError_t launch_kind(const Args& a, int tile_rows, hipStream_t stream) {
-  const unsigned blocks = (unsigned)((a.max_tiles * a.n_blocks + 7) / 8 * 8);
-  if (tile_rows == 64)
-    hipLaunchKernelGGL((grouped_kernel<T, X, BITS, GS, 4, KIND>), dim3(blocks), dim3(kThreads), 0, stream, a);
+  const dim3 grid((unsigned)((a.max_tiles * a.n_blocks + 7) / 8 * 8), KIND == kDown ? (unsigned)a.splits : 1u);
+  if (tile_rows == 16)
+    hipLaunchKernelGGL((grouped_kernel<T, X, BITS, GS, 1, KIND>), grid, dim3(kThreads), 0, stream, a);
+  else if (tile_rows == 64)
+    hipLaunchKernelGGL((grouped_kernel<T, X, BITS, GS, 4, KIND>), grid, dim3(kThreads), 0, stream, a);
   else
-    hipLaunchKernelGGL((grouped_kernel<T, X, BITS, GS, 2, KIND>), dim3(blocks), dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL((grouped_kernel<T, X, BITS, GS, 2, KIND>), grid, dim3(kThreads), 0, stream, a);
   return hipGetLastError();
 }
 

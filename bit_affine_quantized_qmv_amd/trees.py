@@ -16,10 +16,14 @@ _int32 = torch.int32
 
 def _ints(who: str, name: str, t: torch.Tensor, *shape) -> torch.Tensor:
     """An int32 GPU tensor of this shape (None: any), its last stride 1."""
-    if t.dtype != _int32 or not t.is_cuda or t.dim() != len(shape) or any(
-            n is not None and n != m for n, m in zip(shape, t.shape)):
+    sizes = t.shape
+    fits = t.dtype == _int32 and t.is_cuda and len(sizes) == len(shape)
+    if fits:
+        for n, m in zip(shape, sizes):
+            fits = fits and (n is None or n == m)
+    if not fits:
         raise ValueError("%s: %s (%s %s on %s) must be an int32 GPU tensor of shape %s"
-                         % (who, name, t.dtype, tuple(t.shape), t.device, ["any" if n is None else n for n in shape]))
+                         % (who, name, t.dtype, tuple(sizes), t.device, ["any" if n is None else n for n in shape]))
     if t.stride(-1) != 1 and t.size(-1) > 1:
         raise _lib.QmmError(-4, "%s: the last stride of %s must be 1" % (who, name))
     return t

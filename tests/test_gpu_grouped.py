@@ -148,6 +148,19 @@ def test_grouped_rows_are_the_same_in_tiles_of_any_height():
         assert torch.equal(tall[90:150], low)
 
 
+def test_grouped_rows_are_the_same_in_tiles_of_sixteen():
+    import bit_affine_quantized_qmv_amd as q
+    dev = require_gpu()
+    for bits, group in ((4, 32), (4, 64), (4, 128), (8, 32), (8, 128), (6, 64)):
+        w = stack(200, 384, group, bits, "fp16", 2, 1, dev)
+        x = synth.normal_x((190, 384), "fp16", seed=1).to(dev)
+        tall = q.grouped_qmm(x, w, torch.tensor([0, 100, 190], dtype=torch.int32, device=dev))
+        for counts in ((1, 15), (16, 0), (10, 6), (0, 1)):
+            rows = x[100 - counts[0]:100 + counts[1]]
+            low = q.grouped_qmm(rows, w, torch.tensor([0, counts[0], sum(counts)], dtype=torch.int32, device=dev))
+            assert torch.equal(tall[100 - counts[0]:100 + counts[1]], low), (bits, group, counts)
+
+
 def test_grouped_rows_are_their_own():
     """A row's result is the same in any company, NaN rows aside."""
     import bit_affine_quantized_qmv_amd as q
@@ -238,6 +251,23 @@ def test_layer_matches_float64(tokens, hidden, inter, experts, top_k, first, sec
     ref, tol = reference(x, router, gate, up, down, top_k, renormalize, dtype)
     check(y, ref, tol)
     assert torch.equal(y, again)
+
+
+LONG = [
+    # few rows of long ones: the second product's columns are shared out
+    (1, 64, 2080, 3, 1, (4, 32), (4, 32), "bf16"),            # 65 groups: two runs of 32 and one more
+    (5, 160, 2048, 4, 2, (8, 32), (8, 32), "fp16"),
+    (9, 96, 4160, 2, 1, (4, 32), (4, 64), "fp16"),
+    (40, 64, 4160, 2, 2, (4, 32), (8, 64), "bf16"),
+    (130, 128, 8320, 1, 1, (4, 64), (4, 128), "bf16"),
+    (3, 32, 8192, 2, 1, (4, 32), (6, 128), "fp16"),
+    (20, 64, 3200, 2, 1, (3, 32), (3, 32), "bf16"),
+]
+
+
+@pytest.mark.parametrize("tokens,hidden,inter,experts,top_k,first,second,dtype", LONG)
+def test_layer_of_few_rows_and_long_ones(tokens, hidden, inter, experts, top_k, first, second, dtype):
+    test_layer_matches_float64(tokens, hidden, inter, experts, top_k, first, second, dtype, True)
 
 
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
