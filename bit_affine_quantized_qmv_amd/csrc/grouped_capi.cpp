@@ -33,23 +33,35 @@ int64_t max_tiles_of(int64_t rows, int64_t experts) {
 }
 
 int64_t sum_groups_of(int64_t k, int64_t group) { return round_up(k / group, kSumPad); }
-// Splits of the second product's columns: while `tiles` times `blocks` workgroups leave half of the chip's
-// slots empty, as many as fill them, of whole runs of groups.  (A few rows of 14336 columns, 8 experts
-// of [4096, 14336]: 183 us in one piece, 80 in four.)
+// Splits of the second product's columns, of whole runs of groups: what leaves the chip's workgroup slots
+// idle least.  `tiles` times `blocks` workgroups take whole rounds of the slots, and a split more costs its
+// results' way through memory, about what 1024 columns of the product do.  (8 experts of [4096, 14336], one
+// piece against the choice, product and sum: 2 tokens 183 us / 80, 512 348 / 264, 1024 550 / 487, 2047 967 /
+// 875.)
 struct Splits {
   int64_t count, cols;
 };
+constexpr int64_t kSplitRounds = 5;            // rounds of the slots that splits may fill
 Splits splits_of(int64_t tiles, int64_t blocks, int tile_rows, int64_t k, int64_t group) {
-  const int64_t run = kSplitGroups * group, runs = (k + run - 1) / run;
-  const int64_t want = std::max<int64_t>(1, std::min(runs, slots_of(tile_rows) / (tiles * blocks)));
-  const int64_t per = (runs + want - 1) / want;
-  return want == 1 ? Splits{1, k} : Splits{(runs + per - 1) / per, per * run};
+  const int64_t run = kSplitGroups * group, runs = (k + run - 1) / run, slots = slots_of(tile_rows), all = tiles * blocks;
+  Splits best{1, k};
+  double least = 0.0;
+  for (int64_t want = 1; want <= runs && (want == 1 || want * all <= kSplitRounds * slots); ++want) {
+    const int64_t per = (runs + want - 1) / want, count = (runs + per - 1) / per;
+    if (count != want) continue;
+    const double cost = (double)((count * all + slots - 1) / slots * per) / runs + 1024.0 * count * all / ((double)slots * k);
+    if (want == 1 || cost < least) {
+      least = cost;
+      if (want > 1) best = Splits{count, per * run};
+    }
+  }
+  return best;
 }
-// Bytes of their results, [split][pair][n], at most: several splits have no more rows and columns than
-// all slots' tiles.
+// Bytes of their results, [split][pair][n], at most: several splits have no more rows and columns than the
+// tiles of those rounds.
 int64_t out_bytes(int64_t pairs, int64_t n, int64_t k) {
   const int64_t runs = (k + kSplitGroups * 32 - 1) / (kSplitGroups * 32);
-  return align256(4 * std::max(pairs * n, std::min(runs * pairs * n, (int64_t)512 * 64 * kBlockN)));
+  return align256(4 * std::max(pairs * n, std::min(runs * pairs * n, kSplitRounds * 512 * 64 * kBlockN)));
 }
 // Bytes of the staged activations, and of the sums of `rows` rows, whatever the group size.
 int64_t staged_bytes(int64_t rows, int64_t k) { return align256(2 * rows * round_up(k, kStepK)); }
