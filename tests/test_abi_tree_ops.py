@@ -256,3 +256,19 @@ def test_moe_prompt():
                 [40, 4, 2, 128, 2 ** 20 + 1], [65535, 64, 32, 128, 96]):
         assert lib.qmm_moe_prompt_workspace_bytes(*bad) == CODE["QMM_ERR_SHAPE"]
     assert call(tokens=0, x=None, router_logits=None, y=None, ws=None, size=0) == 0
+
+
+def test_moe_prompt_workspace_grows_with_every_size():
+    lib = q.load()
+    base = dict(tokens=3, experts=8, top_k=2, hidden=512, inter=2048)
+    sizes = dict(tokens=[1, 2, 3, 8, 9, 31, 32, 33, 100, 640, 1000, 4000, 20000], experts=[2, 3, 8, 40, 300, 512],
+                 top_k=[1, 2, 5, 8], hidden=[32, 256, 288, 4096, 16384], inter=[32, 1024, 1056, 2080, 14336, 2 ** 17])
+    for big in (1, 60, 1000):
+        for name, values in sizes.items():
+            last = 0
+            for v in values:
+                at = dict(base, tokens=base["tokens"] * big)
+                at[name] = v
+                n = lib.qmm_moe_prompt_workspace_bytes(at["tokens"], at["experts"], at["top_k"], at["hidden"], at["inter"])
+                assert n > 0 and n >= last, (name, v, n, last)
+                last = n

@@ -499,3 +499,51 @@ def test_accepted_path_in_a_replayed_graph():
             q.kv_append(other, k[mine][order], v[mine][order], slots)
             for got, want in zip(held[4:], q.kv_read(other, slots)):
                 assert torch.equal(got[mine], want)
+
+
+def test_beams_over_forked_pages():
+    """Steps of a beam search: fork, page copies, append, attention, each against a cache of its own."""
+    import bit_affine_quantized_qmv_amd as q
+    dev = require_gpu()
+    heads, rep, dim, group, page, dtype, pages = 2, 2, 64, 32, 16, "bf16", 40
+    g = np.random.RandomState(5)
+    text = [13, 31, 16]                                  # tokens of the sequences at first
+    rows = [[[_rows((1, heads, dim), dtype, 1000 * b + 2 * j + side) for side in (0, 1)] for j in range(n)]
+            for b, n in enumerate(text)]
+    cache = q.kv_cache(pages, page, heads, dim, group, dtype, dev)
+    refs = torch.zeros(pages, dtype=torch.int32, device=dev)
+    refs[7] = 1                                          # a page of somebody else's
+    table, _, _, short = q.kv_fork(refs, _ints([[]] * 0, dev).reshape(0, 8), _ints([], dev), _ints([-1] * 3, dev), page,
+                                   _ints(text, dev), blocks=8)
+    at = table.cpu().numpy()
+    slots = [at[b, j // page] * page + j % page for b, n in enumerate(text) for j in range(n)]
+    q.kv_append(cache, *(torch.cat([r[side] for b in rows for r in b]).to(dev) for side in (0, 1)), _ints(slots, dev))
+    assert short.item() == 0
+    for step in range(5):
+        n = [4, 6, 2, 6, 5][step]
+        parents = g.randint(0, len(rows), n).tolist()
+        lengths = [len(r) for r in rows]
+        want = [lengths[p] + 1 for p in parents]
+        table, src, dst, short = q.kv_fork(refs, table, _ints(lengths, dev), _ints(parents, dev), page, _ints(want, dev))
+        q.kv_copy_pages(cache, src, dst)
+        assert short.item() == 0
+        new = [[_rows((1, heads, dim), dtype, 50000 + 100 * step + 2 * b + side) for side in (0, 1)] for b in range(n)]
+        rows = [rows[p] + [new[b]] for b, p in enumerate(parents)]
+        at = table.cpu().numpy()
+        last = _ints([at[b, (m - 1) // page] * page + (m - 1) % page for b, m in enumerate(want)], dev)
+        q.kv_append(cache, *(torch.cat([r[side] for r in new]).to(dev) for side in (0, 1)), last)
+        # the same beams, each in pages of its own
+        own = q.kv_cache(8 * n, page, heads, dim, group, dtype, dev)
+        own_table = torch.arange(8 * n, dtype=torch.int32, device=dev).reshape(n, 8)
+        own_slots = _ints([b * 8 * page + j for b, m in enumerate(want) for j in range(m)], dev)
+        q.kv_append(own, *(torch.cat([r[side] for b in rows for r in b]).to(dev) for side in (0, 1)), own_slots)
+        slots = _ints([at[b, j // page] * page + j % page for b, m in enumerate(want) for j in range(m)], dev)
+        for x, y in zip(q.kv_read(cache, slots), q.kv_read(own, own_slots)):
+            assert torch.equal(x, y)
+        queries = _rows((n, 1, heads * rep, dim), dtype, 900 + step, loud=False).to(dev)
+        assert torch.equal(q.kv_attend(queries, cache, table, _ints(want, dev), max_length=128),
+                           q.kv_attend(queries, own, own_table, _ints(want, dev), max_length=128))
+        # every page is counted as often as the table names it
+        count = np.bincount(at[at >= 0].ravel(), minlength=pages)
+        count[7] += 1
+        assert refs.tolist() == count.tolist()
