@@ -146,7 +146,11 @@ __device__ inline void store4(const AttendArgs& a, int64_t b, int head, int spli
 // once for 32 rows, but their registers leave one or two waves per SIMD: slower at every size
 // measured (20 rows: 63 us against 42; 128 rows: 66 against 43; 8192 tokens, 8 heads of 128).
 // Trees of many query rows take them all the same (R = 2), where the other choice is a workgroup
-// of 256 rows.
+// of 256 rows: 64 nodes of 64 heads over 8 after 131071 tokens, 128 elements in one group, 524 us,
+// 0.52 PFLOP/s of the definition's products (the other form 600 us, one tile 640); the vector units
+// are busy 72% of the time there, the matrix cores 31%.
+// Trees of fewer rows: 16 of 32 nodes after 480 to 8160 tokens, 32 heads over 8, 110 us, 413 vector
+// instructions a step (two groups), also bound by these.
 // What bounds it: a step is 384 vector instructions, about 1600 cycles, for 4.6 KB of codes and
 // scales, so at 5 TB/s the vector units are as busy as the memory; with lengths that differ,
 // what is left is the longest sequences' share.  Measured: 131071 tokens, 8 cached heads of
