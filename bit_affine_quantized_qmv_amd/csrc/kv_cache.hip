@@ -10,8 +10,8 @@
 // tokens that share V's words leave from one wave.  An append moves 2*D + D/2 + 4*D/gs bytes
 // per row, but is bound by its vector instructions, about 30 per element with the exact
 // quotient (a plain division each: 22 us against 19).  Measured, 8191 tokens x 8 heads x 128
-// elements in groups of 32: append 19 us (2.2 TB/s), read 15 us; 32 tokens 3 us each, their
-// launch.
+// elements in groups of 32: append 19 us (2.2 TB/s), read 9.6 us (4.6 TB/s; with a workgroup
+// for each side and V's bytes loaded one by one 15); 32 tokens 3 us each, their launch.
 #include "device_common.hpp"
 #include "kv_cache.hpp"
 
@@ -117,46 +117,57 @@ __global__ __launch_bounds__(kThreads) void append_kernel(const AppendArgs a) {
   }
 }
 
+// A read's workgroup takes both sides: a row's slot, page and place in it are found once for the two.
 template <class T, int D>
 __global__ __launch_bounds__(kThreads) void read_kernel(const ReadArgs a) {
-  constexpr int kLanes = D / 8;
+  constexpr int kLanes = D / 8, KC = D / 32;
   const int lane = threadIdx.x % kLanes;
-  const int heads = a.c.heads;
-  const Place at = place(heads, kThreads / kLanes, threadIdx.x / kLanes);
-  const int64_t n = at.token;
+  const uint32_t heads = (uint32_t)a.c.heads, group = blockIdx.x / heads;
+  const int head = (int)(blockIdx.x - group * heads);
+  const int64_t n = (int64_t)group * (kThreads / kLanes) + threadIdx.x / kLanes;
   if (n >= a.count) return;
-  const int rest = at.rest;
-  const int side = rest >= heads ? 1 : 0;
-  const int head = rest - side * heads;
   const int32_t slot = a.slots[n];
   const bool bad = slot < 0 || slot >= a.c.pages * a.c.page_size;
   int t;
-  const uint32_t* page = page_of(a.c, bad ? 0 : slot, head, &t) + side * a.c.side;
-  const uint32_t sb = page[code_words(a.c.page_size, D) + (8 * lane / a.c.group_size) * a.c.page_size + t];
-  const float s = T::to_f32(sb & 0xFFFFu), b = T::to_f32(sb >> 16);
-  uint32_t word = 0;
-  if (side == 0) {
-    word = page[k_word(t, lane, D)];
-  } else {
-    const uint8_t* bytes = (const uint8_t*)page;
-    const int i = lane >> 1;
+  const uint32_t* keys = page_of(a.c, bad ? 0 : slot, head, &t);
+  const uint32_t* page = keys + a.c.side;
+  const int64_t sb_at = code_words(a.c.page_size, D) + (8 * lane / a.c.group_size) * a.c.page_size + t;
+  const uint32_t word = keys[k_word(t, lane, D)], k_sb = keys[sb_at], v_sb = page[sb_at];
+  // The lane's share of the V words that hold four tokens, of which a token has one byte each, goes to
+  // the lanes that have their elements through LDS, as the row's bytes in the order of v_byte.  (A
+  // row's lanes are in one wave.)
+  const u32x4 words = *(const u32x4*)(page + (t / 4) * (D / 2) + 4 * lane);
+  const uint32_t pick = (uint32_t)(t & 3) * 0x0101u + 0x0400u;    // the token's byte of either word
+  const uint32_t low = __builtin_amdgcn_perm(words[1], words[0], pick);
+  const uint32_t high = __builtin_amdgcn_perm(words[3], words[2], pick);
+  __shared__ uint32_t rows[kThreads];
+  rows[threadIdx.x] = __builtin_amdgcn_perm(high, low, 0x05040100u);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  const int first = threadIdx.x - lane, i = lane >> 1, j = i >> 1, half = lane & 1;
+  const int64_t out = (n * heads + head) * D + 8 * lane;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      word |= (((uint32_t)bytes[v_byte(t, 8 * (lane & 1) + e, i >> 1, D)] >> (4 * (i & 1))) & 15u) << (4 * e);
-  }
-  u32x4 r;
+  for (int side = 0; side < 2; ++side) {
+    const uint32_t sb = side ? v_sb : k_sb;
+    const float s = T::to_f32(sb & 0xFFFFu), b = T::to_f32(sb >> 16);
+    float v[8];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float lo = __builtin_fmaf(s, (float)((word >> (8 * e)) & 15u), b);
-    const float hi = __builtin_fmaf(s, (float)((word >> (8 * e + 4)) & 15u), b);
-    r[e] = bad ? 0x7FFF7FFFu : T::pack2(lo, hi);   // NaN in both types
+    for (int e = 0; e < 8; ++e) {
+      const int byte = (8 * half + e) * KC + j;                     // (j % 4 and e alone decide its place in a word)
+      const int shift = 8 * (KC == 2 ? 2 * (e & 1) + j : j & 3) + 4 * (i & 1);
+      const uint32_t code = (side ? rows[first + byte / 4] >> shift : word >> (4 * e)) & 15u;
+      v[e] = __builtin_fmaf(s, (float)code, b);
+    }
+    u32x4 r;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = bad ? 0x7FFF7FFFu : T::pack2(v[2 * e], v[2 * e + 1]);   // NaN in both types
+    *(u32x4*)((uint16_t*)a.out[side] + out) = r;
   }
-  *(u32x4*)((uint16_t*)a.out[side] + (n * heads + head) * D + 8 * lane) = r;
 }
 
 template <template <class, int> class K, class A>
 hipError_t dispatch(const A& a, int64_t tokens, hipStream_t stream) {
-  const dim3 g((unsigned)copy_blocks(a.c, tokens)), t(kThreads);
+  const dim3 g((unsigned)(copy_blocks(a.c, tokens) / K<Bf16, 64>::kSides)), t(kThreads);
   const bool bf = a.c.dtype == QMM_BF16;
   switch (a.c.head_dim) {
     case 64: bf ? K<Bf16, 64>::go(a, g, t, stream) : K<Fp16, 64>::go(a, g, t, stream); break;
@@ -169,12 +180,14 @@ hipError_t dispatch(const A& a, int64_t tokens, hipStream_t stream) {
 
 template <class T, int D>
 struct Append {
+  static constexpr int kSides = 1;               // of a workgroup
   static void go(const AppendArgs& a, dim3 g, dim3 t, hipStream_t s) {
     hipLaunchKernelGGL((append_kernel<T, D>), g, t, 0, s, a);
   }
 };
 template <class T, int D>
 struct Read {
+  static constexpr int kSides = 2;
   static void go(const ReadArgs& a, dim3 g, dim3 t, hipStream_t s) {
     hipLaunchKernelGGL((read_kernel<T, D>), g, t, 0, s, a);
   }

@@ -119,8 +119,8 @@ struct AttendArgs {
   float* part;            // splits > 1: [batch * heads * rows][splits][head_dim] sums, then their (max, sum) pairs
 };
 
-// Append and read: workgroups of one call, each with the rows of one side of one head; a launch
-// has fewer than 2^32 threads along its grid.
+// Append: workgroups of one call, each with the rows of one side of one head (a read's have both
+// sides, so half as many); a launch has fewer than 2^32 threads along its grid.
 constexpr int kCopyThreads = 256;
 inline int64_t copy_blocks(const CacheArgs& c, int64_t tokens) {
   const int64_t rows = kCopyThreads / (c.head_dim / 8);
