@@ -35,16 +35,18 @@ __global__ __launch_bounds__(256) void copy_pages_kernel(const CopyPagesArgs a) 
   }
 }
 
-// ---- forks.  Three kernels, each of which needs sums over all workgroups of the one before:
+// ---- forks.  Up to three kernels, each of which needs sums over all workgroups of the one before:
 //   fork_count  marks every entry of the new table as a page that stays, none, or fresh, and
 //               counts the fresh ones of a row; counts the free pages of each segment of the pool;
-//   fork_list   numbers the free pages, lowest first;
+//   fork_list   numbers the free pages, lowest first (a pool of one segment's are numbered by
+//               fork_count: a launch less, 14.4 us of a call from Python
+//               against 17.7);
 //   fork_assign gives fresh entry number k (by row, then block) free page number k, and updates
 //               the reference counts: integer atomics, whose order changes nothing.
 // The counts are not touched before the last kernel, so free means free before the call: a page
 // that is taken back by the call is not handed out by it, and may still be the source of a copy.
-// Bound by their three launches at the sizes of a batch (32 rows of 32 blocks 10.4 us, 128 rows of 18
-// blocks 11 us; 18 us with the call from Python).
+// Bound by their launches at the sizes of a batch (in three, 32 rows of 32 blocks 10.4 us, 128 rows of
+// 18 blocks 11 us).
 constexpr int kFresh = -2;                     // a mark in the new table, between the kernels
 constexpr int kMaxCut = 16384;                 // a row's blocks past the new table count up to this: sums fit 31 bits
 
@@ -56,6 +58,33 @@ __device__ inline int block_sum(int v, int* lds) {
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
   __syncthreads();
   return lds[0] + lds[1] + lds[2] + lds[3];
+}
+
+// Number of this thread's set flag among the workgroup's, and their count.
+__device__ inline int block_rank(bool flag, int* lds, int* total) {
+  const uint64_t m = __ballot(flag);
+  const int wave = threadIdx.x >> 6;
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) lds[wave] = __popcll(m);
+  __syncthreads();
+  int before = 0;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) before += w < wave ? lds[w] : 0;
+  *total = lds[0] + lds[1] + lds[2] + lds[3];
+  return before + __popcll(m & ((1ull << (threadIdx.x & 63)) - 1));
+}
+
+// Numbers the free pages of segment s from `at` on.
+__device__ inline void list_segment(const ForkArgs& a, int64_t s, int64_t at, int* lds) {
+  const int64_t p0 = s * kSegment, p1 = min(p0 + kSegment, a.pages);
+  for (int64_t p = p0; p < p1 && at < a.list_size; p += kForkThreads) {
+    const int64_t mine = p + threadIdx.x;
+    const bool open = mine < p1 && a.refs[mine] == 0;
+    int total;
+    const int64_t k = at + block_rank(open, lds, &total);
+    if (open && k < a.list_size) a.list[k] = (int32_t)mine;
+    at += total;
+  }
 }
 
 struct ForkRow {
@@ -85,6 +114,7 @@ __global__ __launch_bounds__(kForkThreads) void fork_count_kernel(const ForkArgs
     for (int64_t p = p0 + threadIdx.x; p < p1; p += kForkThreads) open += a.refs[p] == 0 ? 1 : 0;
     open = block_sum(open, lds);
     if (threadIdx.x == 0) a.open[s] = open;
+    if (a.segments == 1) list_segment(a, 0, 0, lds);       // nothing comes before it
     return;
   }
   const int64_t i = blockIdx.x;
@@ -116,34 +146,12 @@ __global__ __launch_bounds__(kForkThreads) void fork_count_kernel(const ForkArgs
   }
 }
 
-// Number of this thread's set flag among the workgroup's, and their count.
-__device__ inline int block_rank(bool flag, int* lds, int* total) {
-  const uint64_t m = __ballot(flag);
-  const int wave = threadIdx.x >> 6;
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) lds[wave] = __popcll(m);
-  __syncthreads();
-  int before = 0;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) before += w < wave ? lds[w] : 0;
-  *total = lds[0] + lds[1] + lds[2] + lds[3];
-  return before + __popcll(m & ((1ull << (threadIdx.x & 63)) - 1));
-}
-
 __global__ __launch_bounds__(kForkThreads) void fork_list_kernel(const ForkArgs a) {
   __shared__ int lds[4];
-  const int64_t s = blockIdx.x, p0 = s * kSegment, p1 = min(p0 + kSegment, a.pages);
+  const int64_t s = blockIdx.x;
   int before = 0;
   for (int64_t o = threadIdx.x; o < s; o += kForkThreads) before += a.open[o];
-  int64_t at = block_sum(before, lds);
-  for (int64_t p = p0; p < p1 && at < a.list_size; p += kForkThreads) {
-    const int64_t mine = p + threadIdx.x;
-    const bool open = mine < p1 && a.refs[mine] == 0;
-    int total;
-    const int64_t k = at + block_rank(open, lds, &total);
-    if (open && k < a.list_size) a.list[k] = (int32_t)mine;
-    at += total;
-  }
+  list_segment(a, s, block_sum(before, lds), lds);
 }
 
 __global__ __launch_bounds__(kForkThreads) void fork_assign_kernel(const ForkArgs a) {
@@ -206,9 +214,11 @@ hipError_t launch_fork(const ForkArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL(fork_count_kernel, dim3((unsigned)a.rows + segments), dim3(kForkThreads), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(fork_list_kernel, dim3(segments), dim3(kForkThreads), 0, stream, a);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  if (segments > 1) {
+    hipLaunchKernelGGL(fork_list_kernel, dim3(segments), dim3(kForkThreads), 0, stream, a);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   hipLaunchKernelGGL(fork_assign_kernel, dim3((unsigned)(a.rows + std::max<int64_t>(a.batch, 1))), dim3(kForkThreads), 0, stream, a);
   return hipGetLastError();
 }

@@ -14,24 +14,21 @@ _byref = ctypes.byref
 _int32 = torch.int32
 
 
-def _ints(who: str, name: str, t: torch.Tensor, *shape) -> torch.Tensor:
-    """An int32 GPU tensor of this shape (None: any), its last stride 1."""
+def _ints(who: str, name: str, t: torch.Tensor, *shape) -> int:
+    """The row stride of an int32 GPU tensor of this shape (None: any), its last stride 1; that of a
+    single row may be anything."""
     sizes = t.shape
     fits = t.dtype == _int32 and t.is_cuda and len(sizes) == len(shape)
-    if fits:
+    if fits and sizes != shape:
         for n, m in zip(shape, sizes):
             fits = fits and (n is None or n == m)
     if not fits:
         raise ValueError("%s: %s (%s %s on %s) must be an int32 GPU tensor of shape %s"
                          % (who, name, t.dtype, tuple(sizes), t.device, ["any" if n is None else n for n in shape]))
-    if t.stride(-1) != 1 and t.size(-1) > 1:
+    strides = t.stride()
+    if strides[-1] != 1 and sizes[-1] > 1:
         raise _lib.QmmError(-4, "%s: the last stride of %s must be 1" % (who, name))
-    return t
-
-
-def _row_stride(t: torch.Tensor) -> int:
-    """The row stride of a matrix; that of a single row may be anything."""
-    return t.stride(0) if t.size(0) > 1 else t.size(1)
+    return strides[0] if sizes[0] > 1 else sizes[-1]
 
 
 def tree_mask(parents: torch.Tensor, window: int = 0):
@@ -41,11 +38,11 @@ def tree_mask(parents: torch.Tensor, window: int = 0):
     path a node sees.  Node i of a sequence whose tree starts at position c stands for position
     c + depth[i]."""
     lib = _lib.load()
-    _ints("tree_mask", "parents", parents, None, None)
+    stride = _ints("tree_mask", "parents", parents, None, None)
     batch, nodes = parents.shape
     mask = parents.new_empty((batch, nodes, (nodes + 31) // 32))
     depth = parents.new_empty((batch, nodes))
-    _lib.check(lib.qmm_tree_mask(parents.data_ptr(), _row_stride(parents), batch, nodes, window, mask.data_ptr(),
+    _lib.check(lib.qmm_tree_mask(parents.data_ptr(), stride, batch, nodes, window, mask.data_ptr(),
                                  depth.data_ptr(), raw_stream(parents)))
     return mask, depth
 
@@ -77,7 +74,7 @@ def kv_attend_tree(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, l
     if q.dim() != 4:
         raise ValueError("kv_attend_tree: q %s must be [batch, nodes, q_heads, head_dim]" % (tuple(q.shape),))
     batch, nodes = q.shape[:2]
-    _ints("kv_attend_tree", "block_table", block_table, batch, None)
+    table_stride = _ints("kv_attend_tree", "block_table", block_table, batch, None)
     _ints("kv_attend_tree", "lengths", lengths, batch)
     _ints("kv_attend_tree", "mask", mask, batch, nodes, (nodes + 31) // 32)
     if depth is not None:
@@ -88,7 +85,7 @@ def kv_attend_tree(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, l
         raise _lib.QmmError(-2, "q and the cache must share one dtype")
     blocks = block_table.size(1)
     d = _attend_desc(q, cache, cache.head_dim ** -0.5 if scale is None else scale, 1, window, block_table.data_ptr(),
-                     _row_stride(block_table), blocks, lengths.data_ptr(),
+                     table_stride, blocks, lengths.data_ptr(),
                      blocks * cache.page_size if max_length is None else max_length)
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
@@ -110,15 +107,14 @@ def tree_accept(parents: torch.Tensor, tokens: torch.Tensor, sampled: torch.Tens
     and sampled tokens, int32 [batch, nodes] each: (path int32 [batch, nodes], -1 after its end,
     count int32 [batch], last int32 [batch]: the token sampled after the path's end)."""
     lib = _lib.load()
-    _ints("tree_accept", "parents", parents, None, None)
-    batch, nodes = parents.shape
-    _ints("tree_accept", "tokens", tokens, batch, nodes)
-    _ints("tree_accept", "sampled", sampled, batch, nodes)
+    parents_stride = _ints("tree_accept", "parents", parents, None, None)
+    shape = batch, nodes = parents.shape
+    tokens_stride = _ints("tree_accept", "tokens", tokens, batch, nodes)
+    sampled_stride = _ints("tree_accept", "sampled", sampled, batch, nodes)
     same_device("tree_accept", parents, tokens, sampled)
-    path = parents.new_empty((batch, nodes))
-    count, last = parents.new_empty((2, batch)).unbind(0)
-    a = _lib.TreeAcceptDesc(parents.data_ptr(), tokens.data_ptr(), sampled.data_ptr(), _row_stride(parents),
-                            _row_stride(tokens), _row_stride(sampled), batch, nodes)
+    path, count, last = parents.new_empty(shape), parents.new_empty(batch), parents.new_empty(batch)
+    a = _lib.TreeAcceptDesc(parents.data_ptr(), tokens.data_ptr(), sampled.data_ptr(), parents_stride, tokens_stride,
+                            sampled_stride, batch, nodes)
     _lib.check(lib.qmm_tree_accept(_byref(a), path.data_ptr(), count.data_ptr(), last.data_ptr(), raw_stream(parents)))
     return path, count, last
 
@@ -130,19 +126,19 @@ def kv_move(cache: KVCache, block_table: torch.Tensor, index: torch.Tensor, star
     pages the indices have to ascend and no row may move up; with to_table the rows go to its pages,
     of which the call may read none."""
     lib = _lib.load()
-    _ints("kv_move", "index", index, None, None)
+    index_stride = _ints("kv_move", "index", index, None, None)
     batch, count = index.shape
-    _ints("kv_move", "block_table", block_table, batch, None)
+    table_stride = _ints("kv_move", "block_table", block_table, batch, None)
     _ints("kv_move", "start", start, batch)
     if origin is not None:
         _ints("kv_move", "origin", origin, batch)
     to, to_stride, to_blocks = None, 0, 0
     if to_table is not None:
-        _ints("kv_move", "to_table", to_table, batch, None)
-        to, to_stride, to_blocks = to_table.data_ptr(), _row_stride(to_table), to_table.size(1)
+        to_stride = _ints("kv_move", "to_table", to_table, batch, None)
+        to, to_blocks = to_table.data_ptr(), to_table.size(1)
     same_device("kv_move", index, block_table, start, origin, to_table, cache.data)
-    a = _lib.KVMoveDesc(block_table.data_ptr(), _row_stride(block_table), block_table.size(1), to, to_stride, to_blocks,
-                        index.data_ptr(), _row_stride(index), batch, count,
+    a = _lib.KVMoveDesc(block_table.data_ptr(), table_stride, block_table.size(1), to, to_stride, to_blocks,
+                        index.data_ptr(), index_stride, batch, count,
                         origin.data_ptr() if origin is not None else None, start.data_ptr())
     _lib.check(lib.qmm_kv_move(_byref(cache._desc), _byref(a), raw_stream(index)))
 
@@ -167,7 +163,7 @@ def kv_fork(refs: torch.Tensor, block_table: torch.Tensor, lengths: torch.Tensor
     (-1: none), and int32 [1], how many entries got no page."""
     lib = _lib.load()
     _ints("kv_fork", "refs", refs, None)
-    _ints("kv_fork", "block_table", block_table, None, None)
+    table_stride = _ints("kv_fork", "block_table", block_table, None, None)
     batch, old_blocks = block_table.shape
     _ints("kv_fork", "lengths", lengths, batch)
     _ints("kv_fork", "parents", parents, None)
@@ -179,7 +175,7 @@ def kv_fork(refs: torch.Tensor, block_table: torch.Tensor, lengths: torch.Tensor
     table = parents.new_empty((rows, max(blocks, 0)))
     pairs = parents.new_empty(2 * rows + 1)
     at = pairs.data_ptr()
-    a = _lib.KVForkDesc(refs.data_ptr(), refs.size(0), page_size, block_table.data_ptr(), _row_stride(block_table),
+    a = _lib.KVForkDesc(refs.data_ptr(), refs.size(0), page_size, block_table.data_ptr(), table_stride,
                         old_blocks, lengths.data_ptr(), batch, parents.data_ptr(),
                         want.data_ptr() if want is not None else None, rows, table.data_ptr(), blocks, blocks)
     n = lib.qmm_kv_fork_workspace_bytes(_byref(a))

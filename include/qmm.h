@@ -455,7 +455,7 @@ int32_t qmm_kv_copy_pages(const qmm_kv_cache_t* cache, const int32_t* src, const
  * Entries outside [0, pages) name no page.  new_table must not overlap the old one.
  * copy_src, copy_dst: DEVICE int32 [rows]; short_of: DEVICE int32 [1]; workspace: DEVICE, 4-byte
  * aligned, qmm_kv_fork_workspace_bytes(args) bytes of any content; one serves any number of calls
- * in stream order.  Three kernels.  batch, rows <= 65535; rows * new_blocks <= 2^30; the limits of
+ * in stream order.  Two or three kernels.  batch, rows <= 65535; rows * new_blocks <= 2^30; the limits of
  * pages and page_size are the cache's. */
 typedef struct {
   int32_t* refs;                /* DEVICE int32 [pages]                                    */
