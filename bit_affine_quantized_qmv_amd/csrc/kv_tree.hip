@@ -84,7 +84,8 @@ __global__ __launch_bounds__(64) void tree_accept_kernel(const TreeAcceptArgs a)
 // the steps are independent workgroups.
 // Bound by latency for a path (table, rows, barrier, stores: 64 paths of 63 nodes, 8 heads of 128, 6 us),
 // by memory for long moves (10240 rows of 8 heads of 128 to other pages 11.4 us, 26 MB in all,
-// 2.3 TB/s: codes come in runs of 64 bytes, a V row's as one byte of each word of four tokens).
+// 2.3 TB/s; in whole sectors, of which a kept row's V bytes, scales and biases are a part each, about
+// 48 MB).
 template <int D>
 __global__ __launch_bounds__(kThreads) void move_kernel(const MoveArgs a) {
   constexpr int kStep = 64;
