@@ -63,7 +63,7 @@ TREES = [
     ([50, 333], 50, 1, 4, 64, 32, 16, 37, "fp16"),                   # a window that starts in the context
     ([100, 999], 30, 2, 2, 128, 64, 16, 3, "bf16"),                  # one that starts in the tree, mostly
     ([40, 500], 20, 1, 2, 128, 128, 16, 1, "bf16"),                  # a window of the node itself
-    ([64, 200, 0], 64, 2, 4, 128, 64, 64, 0, "bf16"),                # 256 rows: waves of their own rows
+    ([64, 200, 0], 64, 2, 4, 128, 64, 64, 0, "bf16"),                # 256 rows: two tiles of 16 per wave
     ([211, 330], 211, 1, 3, 128, 32, 48, 0, "fp16"),
     ([130, 600], 130, 1, 2, 128, 128, 16, 100, "bf16"),
     ([256, 400], 256, 1, 4, 64, 64, 16, 0, "fp16"),
