@@ -60,6 +60,16 @@ __device__ inline int block_sum(int v, int* lds) {
   return lds[0] + lds[1] + lds[2] + lds[3];
 }
 
+// Largest number of the workgroup's.
+__device__ inline int block_max(int v, int* lds) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v = max(v, __shfl_xor(v, d));
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return max(max(lds[0], lds[1]), max(lds[2], lds[3]));
+}
+
 // Number of this thread's set flag among the workgroup's, and their count.
 __device__ inline int block_rank(bool flag, int* lds, int* total) {
   const uint64_t m = __ballot(flag);
@@ -119,10 +129,13 @@ __global__ __launch_bounds__(kForkThreads) void fork_count_kernel(const ForkArgs
   }
   const int64_t i = blockIdx.x;
   const ForkRow r = fork_row(a, i);
-  int earlier = 0;                             // rows before this one with the same parent
+  // The parent's first row keeps its old pages from the first block on that no other row of the parent
+  // shares: it writes there, and a row that keeps more tokens reads them.
+  int shared = 0;                              // blocks that another row names; all of them for later rows
   if (r.parent >= 0)
-    for (int64_t o = threadIdx.x; o < i; o += kForkThreads) earlier |= a.parents[o] == r.parent ? 1 : 0;
-  const bool first = block_sum(earlier, lds) == 0;
+    for (int64_t o = threadIdx.x; o < a.rows; o += kForkThreads)
+      if (a.parents[o] == r.parent && o != i) shared = max(shared, o < i ? 0x7FFFFFFF : (int)fork_row(a, o).full);
+  shared = block_max(shared, lds);
   int need = 0;
   for (int64_t j = threadIdx.x; j < a.new_blocks; j += kForkThreads) {
     const int32_t page = r.parent >= 0 && j < a.blocks ? a.table[r.parent * a.table_stride + j] : -1;
@@ -131,7 +144,7 @@ __global__ __launch_bounds__(kForkThreads) void fork_count_kernel(const ForkArgs
     if (j < r.full) {
       entry = valid ? page : -1;
     } else if (j < r.cover) {
-      const bool keeps = first && valid && a.refs[page] == 1;
+      const bool keeps = j >= shared && valid && a.refs[page] == 1;
       entry = keeps ? page : kFresh;
       need += keeps ? 0 : 1;
     }

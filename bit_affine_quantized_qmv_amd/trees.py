@@ -158,7 +158,8 @@ def kv_fork(refs: torch.Tensor, block_table: torch.Tensor, lengths: torch.Tensor
     """Block tables that continue others, begin, grow, are cut back or end (qmm_kv_fork).  refs
     int32 [pages] counts the table entries that name each page and is brought up to date.  Row i of
     the new table [rows, blocks] (blocks: as many as the old one has) continues row parents[i] of
-    block_table (outside it: begins empty) with room for want[i] tokens (None: its length).  Returns
+    block_table (outside it: begins empty) with room for want[i] tokens (None: its length); the pages
+    from its first min(length, want[i]) tokens on are its own to write to.  Returns
     (table, copy_src, copy_dst, short): the pages to copy with kv_copy_pages in every layer's cache
     (-1: none), and int32 [1], how many entries got no page."""
     lib = _lib.load()

@@ -444,10 +444,11 @@ int32_t qmm_kv_copy_pages(const qmm_kv_cache_t* cache, const int32_t* src, const
  * [0, batch).  It keeps the first min(length, want) tokens and has room for want[i] (NULL: the
  * parent's length); with s = page_size
  *   - blocks of which every token stays name the old page, which all such rows share;
- *   - the block that is kept in part, and those after it up to ceil(want / s), go to the first row
- *     (lowest i) of a parent where its old page is held by nobody else (refs 1); otherwise they get
- *     fresh pages: entry number k of these, by row and block, gets the k-th lowest page that was
- *     free before the call.  Rows of a fresh page for a block kept in part are to be copied:
+ *   - the block that is kept in part, and those after it up to ceil(want / s), are the row's own, to
+ *     write to.  The first row (lowest i) of a parent has the old page there if nobody else holds it: no
+ *     other table (refs 1), and no other row of the parent, of which the block's every token stays.
+ *     Otherwise they are fresh pages: entry number k of these, by row and block, gets the k-th lowest
+ *     page that was free before the call.  Rows of a fresh page for a block kept in part are to be copied:
  *     copy_src[i] -> copy_dst[i] with qmm_kv_copy_pages, for each layer's cache (-1: nothing);
  *   - other entries are -1, and so are those for which no page is left or new_blocks is too small:
  *     *short_of counts these (of each row at most 16384 past new_blocks).
