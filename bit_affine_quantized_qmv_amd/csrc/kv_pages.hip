@@ -154,7 +154,7 @@ __global__ __launch_bounds__(kForkThreads) void fork_count_kernel(const ForkArgs
   need = block_sum(need, lds);
   if (threadIdx.x == 0) {
     a.need[i] = need;
-    a.cut[i] = (int32_t)min((int64_t)kMaxCut, max((int64_t)0, r.cover - max(a.new_blocks, r.full)));
+    a.cut[i] = (int32_t)min((int64_t)kMaxCut, max((int64_t)0, r.cover - a.new_blocks));
     if (r.full >= a.new_blocks) a.copy_src[i] = -1;
   }
 }

@@ -161,7 +161,7 @@ def kv_fork(refs: torch.Tensor, block_table: torch.Tensor, lengths: torch.Tensor
     block_table (outside it: begins empty) with room for want[i] tokens (None: its length); the pages
     from its first min(length, want[i]) tokens on are its own to write to.  Returns
     (table, copy_src, copy_dst, short): the pages to copy with kv_copy_pages in every layer's cache
-    (-1: none), and int32 [1], how many entries got no page."""
+    (-1: none), and int32 [1], how many entries got no page or no place in the table."""
     lib = _lib.load()
     _ints("kv_fork", "refs", refs, None)
     table_stride = _ints("kv_fork", "block_table", block_table, None, None)

@@ -451,7 +451,8 @@ int32_t qmm_kv_copy_pages(const qmm_kv_cache_t* cache, const int32_t* src, const
  *     page that was free before the call.  Rows of a fresh page for a block kept in part are to be copied:
  *     copy_src[i] -> copy_dst[i] with qmm_kv_copy_pages, for each layer's cache (-1: nothing);
  *   - other entries are -1, and so are those for which no page is left or new_blocks is too small:
- *     *short_of counts these (of each row at most 16384 past new_blocks).
+ *     *short_of counts these, of kept tokens too (of each row at most 16384 past new_blocks).  A kept
+ *     block that had no page before the call has none after it, and is not counted.
  * refs is brought up to date: pages that only old rows named become free for the next call.
  * Entries outside [0, pages) name no page.  new_table must not overlap the old one.
  * copy_src, copy_dst: DEVICE int32 [rows]; short_of: DEVICE int32 [1]; workspace: DEVICE, 4-byte

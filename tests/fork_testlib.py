@@ -38,7 +38,7 @@ def fork_rule(refs, table, lengths, parents, page, want, blocks):
             short += row[j] < 0
             if j == keep // page and keep % page and was >= 0 and row[j] >= 0:
                 copy = (was, row[j])
-        short += min(16384, max(0, -(-w // page) - max(blocks, keep // page)))
+        short += min(16384, max(0, -(-w // page) - blocks))
         out.append(row)
         src.append(copy[0])
         dst.append(copy[1])
