@@ -91,6 +91,17 @@ struct TreeRow {
     return (uint32_t)(((((uint64_t)hi) << 32) | lo) >> (node & 31));
   }
 };
+// The first token that a tree's query sees with a window, of the tokens before the tree, which ends at
+// `off`.  Depths may be the caller's own: any from 0 on (below 2^30, as positions are), less counts as 0.
+__device__ inline int tree_row_begin(const AttendArgs& a, int64_t b, int query, int off) {
+  return off + min(max(a.depth[b * a.q_len + query], 0), 1 << 30) - a.window + 1;
+}
+// Largest v of the wave, the same in every lane; lanes 16 apart hold the same row.
+__device__ inline int max_of_rows(int v) {
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) v = max(v, __shfl_xor(v, d));
+  return __builtin_amdgcn_readfirstlane(v);
+}
 // A sequence's length is in order: its tree fits in it, or it is empty.
 template <bool TREE>
 __device__ inline bool length_bad(const AttendArgs& a, int len) {
@@ -184,11 +195,11 @@ __global__ __launch_bounds__(kThreads, (R > 1 ? 2 : workgroups<D, GS>())) void a
   // token ranges: [lo_min, hi_max) is seen by some row of the wave, [lo_max, hi_min) by all
   const int off = len - a.q_len;
   const int i_first = base / a.rep, i_last = (min(a.rows, base + kRows) - 1) / a.rep;
-  // (a tree's rows lie between depth 0 and its number of nodes, whatever their order)
+  // (a tree's rows have depths from 0 on, whatever their order; lo_max comes from them)
   const int hi_max = TREE ? len : (a.causal ? max(0, off + i_last + 1) : len);
   const int hi_min = TREE ? max(0, off) : (a.causal ? max(0, off + i_first + 1) : len);
   const int lo_min = a.window ? max(0, off + (TREE ? 0 : i_first) - a.window + 1) : 0;
-  const int lo_max = a.window ? max(0, off + (TREE ? a.q_len - 1 : i_last) - a.window + 1) : 0;
+  int lo_max = a.window && !TREE ? max(0, off + i_last - a.window + 1) : 0;
   const int c0 = (lo_min & ~(kStep - 1)) + split * a.chunk;
   const int c1 = min(c0 + a.chunk, hi_max);
   const int stride = kStep * kWaves;
@@ -300,7 +311,10 @@ __global__ __launch_bounds__(kThreads, (R > 1 ? 2 : workgroups<D, GS>())) void a
     row_lo[k] = a.window ? off + query - a.window + 1 : 0;
     if constexpr (TREE) {
       tree[k].setup(a, b, query);
-      row_lo[k] = a.window ? off + a.depth[b * a.q_len + query] - a.window + 1 : 0;
+      if (a.window) {
+        row_lo[k] = tree_row_begin(a, b, query, off);
+        lo_max = max(lo_max, max_of_rows(row_lo[k]));
+      }
     }
   }
 
@@ -550,7 +564,7 @@ __global__ __launch_bounds__(64 * row_waves(D), 1) void attend_rows_kernel(const
   const bool bad = length_bad<TREE>(a, len);
   if (bad) len = 0;
   const int off = len - a.q_len;
-  // (a tree's rows lie between depth 0 and its number of nodes, whatever their order)
+  // (a tree's rows have depths from 0 on, whatever their order; lo_max comes from them)
   const auto row_end = [&](int r) { return TREE || !a.causal ? len : max(0, off + r / a.rep + 1); };
   const auto row_begin = [&](int r) { return a.window ? max(0, off + (TREE ? 0 : r / a.rep) - a.window + 1) : 0; };
   // ranges of the workgroup, and of this wave (empty for a wave without rows)
@@ -559,7 +573,7 @@ __global__ __launch_bounds__(64 * row_waves(D), 1) void attend_rows_kernel(const
   const bool live = base < a.rows;
   const int last = min(a.rows, base + kRows) - 1;
   const int lo_min = live ? row_begin(base) : 0, hi_max = live ? row_end(last) : 0;
-  const int lo_max = !live ? 0 : (!TREE ? row_begin(last) : (a.window ? max(0, len - a.window) : 0));
+  int lo_max = live && !TREE ? row_begin(last) : 0;
   const int hi_min = !live ? 0 : (!TREE ? row_end(base) : max(0, off));
   const int c0 = (wg_lo & ~(kStep - 1)) + split * a.chunk;
   const int c1 = min(c0 + a.chunk, wg_hi);
@@ -705,7 +719,10 @@ __global__ __launch_bounds__(64 * row_waves(D), 1) void attend_rows_kernel(const
   TreeRow tree;
   if constexpr (TREE) {
     tree.setup(a, b, query);
-    row_lo = a.window ? off + a.depth[b * a.q_len + query] - a.window + 1 : 0;
+    if (a.window) {
+      row_lo = tree_row_begin(a, b, query, off);
+      lo_max = max_of_rows(row_lo);
+    }
   }
 #pragma unroll
   for (int j = 0; j < NT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};

@@ -68,8 +68,8 @@ def kv_attend_tree(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, l
     """Attention of drafted trees (qmm_kv_attend_tree): q [batch, nodes, q_heads, head_dim] (any
     strides, the last 1) are the trees' nodes, the last `nodes` tokens of each sequence.  A node
     sees the tokens before its tree (with a window those near enough to its depth) and the nodes of
-    its row of mask; mask and depth are tree_mask's, with the same window.  What is no node gives
-    zeros.  The other arguments are kv_attend's."""
+    its row of mask; mask and depth are tree_mask's, with the same window, or the caller's own (any
+    depths from 0 on).  What is no node gives zeros.  The other arguments are kv_attend's."""
     lib = _lib.load()
     if q.dim() != 4:
         raise ValueError("kv_attend_tree: q %s must be [batch, nodes, q_heads, head_dim]" % (tuple(q.shape),))

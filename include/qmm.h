@@ -382,7 +382,8 @@ int32_t qmm_tree_mask(const int32_t* parents, int64_t parents_stride, int64_t ba
  * tokens j < c before the tree, with a window only j > c + depth[i] - window, and the nodes of its
  * row of `mask`; a row of zeros sees nothing and gives zeros.  mask and depth (read with a window
  * only, which may then not be NULL) are qmm_tree_mask's for this batch and q_len = nodes at most
- * QMM_TREE_MAX_NODES, or the caller's own; a window is applied to a mask by qmm_tree_mask.  causal
+ * QMM_TREE_MAX_NODES, or the caller's own (a depth may pass the number of nodes; one below 0 counts as
+ * 0); a window is applied to a mask by qmm_tree_mask.  causal
  * must be set.  A length of zero gives zeros; another one below q_len, like one above max_length,
  * makes the sequence's outputs NaN. */
 int32_t qmm_kv_attend_tree(const qmm_kv_cache_t* cache, const qmm_kv_attend_t* args, const uint32_t* mask,
