@@ -10,11 +10,6 @@ namespace {
 // 2048 elements of a row (thread `at` of 256 has eight of them) as the products take them, and the
 // sums of their groups in three bfloat16 parts; what a row is padded to is zero.  Sums in float32,
 // eight in order, then the lanes in pairs.  Bound by memory.
-__host__ __device__ inline int64_t blocks_per_row(const PrepareArgs& a) {
-  const int64_t sums = (int64_t)a.sum_groups * a.group, n = sums > a.cols ? sums : a.cols;
-  return (n + 8 * kThreads - 1) / (8 * kThreads);
-}
-
 template <class T>
 __device__ inline void stage_rows(const PrepareArgs& a, int64_t block, int at) {
   const int per_row = (int)blocks_per_row(a);
@@ -38,7 +33,6 @@ __device__ inline void stage_rows(const PrepareArgs& a, int64_t block, int at) {
 }
 
 // Inclusive prefix of one number per thread of the first 512, over the workgroup (kMake threads).
-constexpr int kMake = 1024;
 __device__ inline int block_prefix(int v, int* lds) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
@@ -235,11 +229,11 @@ hipError_t launch_sum(const SumArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_prepare(const PrepareArgs& a, hipStream_t stream) {
-  const int64_t per = kMake / kThreads, blocks = (a.rows * blocks_per_row(a) + per - 1) / per + 1;
+  const dim3 grid((unsigned)prepare_blocks(a));
   if (a.dtype == QMM_BF16)
-    hipLaunchKernelGGL(prepare_kernel<Bf16>, dim3((unsigned)blocks), dim3(kMake), 0, stream, a);
+    hipLaunchKernelGGL(prepare_kernel<Bf16>, grid, dim3(kMake), 0, stream, a);
   else
-    hipLaunchKernelGGL(prepare_kernel<Fp16>, dim3((unsigned)blocks), dim3(kMake), 0, stream, a);
+    hipLaunchKernelGGL(prepare_kernel<Fp16>, grid, dim3(kMake), 0, stream, a);
   return hipGetLastError();
 }
 

@@ -90,6 +90,23 @@ struct PrepareArgs {
   int32_t* tile_count;
 };
 
+// Workgroups of kThreads threads that take a row of x, 2048 columns each: its columns and what they and
+// the sums are padded to.
+__host__ __device__ inline int64_t blocks_per_row(const PrepareArgs& a) {
+  const int64_t sums = (int64_t)a.sum_groups * a.group, n = sums > a.cols ? sums : a.cols;
+  return (n + 8 * kThreads - 1) / (8 * kThreads);
+}
+// Workgroups of prepare_kernel, of kMake threads: those of the rows, and one for the tiles.
+constexpr int kMake = 1024;
+inline int64_t prepare_blocks(const PrepareArgs& a) {
+  constexpr int64_t per = kMake / kThreads;
+  return (a.rows * blocks_per_row(a) + per - 1) / per + 1;
+}
+// Workgroups along x of a product: an equal run of the work for each of the eight XCDs.
+inline int64_t product_blocks(const Args& a) { return ((int64_t)a.max_tiles * a.n_blocks + 7) / 8 * 8; }
+// A launch has fewer threads than this along its grid.
+constexpr int64_t kLaunchThreads = 1ll << 32;
+
 // Routing of the expert layer: each token's choices, then the rows of every expert.
 struct RouteArgs {
   const uint16_t* router;

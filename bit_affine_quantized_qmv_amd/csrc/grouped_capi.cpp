@@ -198,7 +198,9 @@ int32_t qmm_grouped(const void* x, int64_t x_stride, int64_t rows, const qmm_exp
     a.n_blocks = (int32_t)((n + grouped::kBlockN - 1) / grouped::kBlockN);
     a.y = (uint16_t*)y;
     a.y_stride = y_stride;
-    if ((int64_t)a.max_tiles * a.n_blocks >= (1 << 24))
+    if (grouped::prepare_blocks(p) * grouped::kMake >= grouped::kLaunchThreads)
+      return report(QMM_ERR_SHAPE, "grouped: rows * K too large for one call (up to 2^35 - 2^15, K rounded up to 4096, always fits)");
+    if (grouped::product_blocks(a) * grouped::kThreads >= grouped::kLaunchThreads)
       return report(QMM_ERR_SHAPE, "grouped: rows * N too large for one call");
     hipStream_t s = (hipStream_t)stream;
     hipError_t e = grouped::launch_prepare(p, s);
@@ -330,7 +332,7 @@ int32_t qmm_moe_prompt(const qmm_moe_t* m, void* y, void* workspace, int64_t wor
     d.splits = (int32_t)split.count;
     d.split_cols = (int32_t)split.cols;
     d.out_split = n * hidden;
-    if ((int64_t)g.max_tiles * std::max(g.n_blocks, d.n_blocks) >= (1 << 24))
+    if (std::max(grouped::product_blocks(g), grouped::product_blocks(d)) * grouped::kThreads >= grouped::kLaunchThreads)
       return report(QMM_ERR_SHAPE, "moe_prompt: tokens * top_k * max(hidden, inter) too large for one call");
 
     const grouped::SumArgs sum{r.tokens,       m->top_k, r.renormalize, (int32_t)hidden, m->dtype, d.splits, d.out,

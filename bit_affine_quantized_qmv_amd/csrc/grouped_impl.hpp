@@ -575,7 +575,7 @@ __global__ __launch_bounds__(kThreads, FM == 1 ? 4 : (FM == 2 ? 3 : 2)) void gro
 
 template <class T, class X, int BITS, int GS, int KIND>
 hipError_t launch_kind(const Args& a, int tile_rows, hipStream_t stream) {
-  const dim3 grid((unsigned)((a.max_tiles * a.n_blocks + 7) / 8 * 8), KIND == kDown ? (unsigned)a.splits : 1u);
+  const dim3 grid((unsigned)product_blocks(a), KIND == kDown ? (unsigned)a.splits : 1u);
   if (tile_rows == 16)
     hipLaunchKernelGGL((grouped_kernel<T, X, BITS, GS, 1, KIND>), grid, dim3(kThreads), 0, stream, a);
   else if (tile_rows == 64)

@@ -537,7 +537,8 @@ int64_t qmm_moe_workspace_bytes(int64_t tokens, int64_t experts, int64_t top_k, 
  * rows start where those of all before it have ended.  Rows of y that belong to no expert are left
  * as they are.  y: DEVICE [rows, y_stride] of dtype, 2-byte aligned, y_stride >= N.  rows at most
  * 2^20, num_experts at most QMM_MOE_MAX_EXPERTS, N and K at most 2^20; the limits and alignments
- * of qmm_moe's stacks.  workspace: DEVICE, 16-byte aligned, qmm_grouped_workspace_bytes(rows, weights)
+ * of qmm_moe's stacks.  Calls that no launch holds are refused: rows * K (K rounded up to 4096) up to
+ * 2^35 - 2^15 and (rows / 16 + num_experts) * N (N rounded up to 256) up to 2^32 - 2^11 always fit.  workspace: DEVICE, 16-byte aligned, qmm_grouped_workspace_bytes(rows, weights)
  * bytes of any content; one serves any number of calls in stream order, calls that may overlap need
  * their own.  A row's result depends on nothing but the row and its expert.  rows == 0 is a no-op.  Two kernels. */
 int32_t qmm_grouped(const void* x, int64_t x_stride, int64_t rows, const qmm_expert_stack_t* weights,
@@ -549,8 +550,10 @@ int32_t qmm_grouped(const void* x, int64_t x_stride, int64_t rows, const qmm_exp
 int64_t qmm_grouped_workspace_bytes(int64_t rows, const qmm_expert_stack_t* weights);
 
 /* The layer of qmm_moe for any number of tokens (at most 65535, tokens * top_k at most 2^20,
- * tokens * hidden, each row rounded up to 128, below 2^29): arguments, formula, arithmetic and alignments are qmm_moe's, the
- * workspace is qmm_moe_prompt_workspace_bytes(...) bytes.  tokens == 0 is a no-op.  Five kernels.
+ * tokens * hidden, each row rounded up to 128, below 2^29; (tokens * top_k / 16 + num_experts) times the
+ * larger of hidden and 2 * inter, rounded up to 256, always fits up to 2^32 - 2^11, and calls that no launch
+ * holds are refused): arguments, formula, arithmetic and alignments are qmm_moe's, the workspace is
+ * qmm_moe_prompt_workspace_bytes(...) bytes.  tokens == 0 is a no-op.  Five kernels.
  * For fewer than about 12 tokens qmm_moe is the faster one (8 experts of 4096 x 14336, 4 bits: 1 token
  * 54 us against 75, 8 tokens 200 / 238, 16 tokens 239 / 242, 32 tokens 345 / 239). */
 int32_t qmm_moe_prompt(const qmm_moe_t* args, void* y, void* workspace, int64_t workspace_bytes, void* stream);
