@@ -76,12 +76,9 @@ hipError_t launch(const Args& a, Kind kind, int dtype, int tile_rows, hipStream_
                    : (bits == 8 ? launch_b8(a, kind, dtype, tile_rows, s) : launch_bn(a, kind, dtype, tile_rows, s));
 }
 
-// The kernels address a workgroup's weight rows, some past the last, with 32-bit byte offsets.
-int32_t check_rows(const char* who, const Stack& k, int64_t n) {
-  if ((n + kBlockN) * k.w_row_stride * 4 >= (1ll << 31) || (n + kBlockN) * k.sb_row_stride * 2 >= (1ll << 31))
-    return report(QMM_ERR_SHAPE, std::string(who) + ": one expert's codes must be smaller than 1 GiB");
-  return QMM_OK;
-}
+// The kernels address a workgroup's weight rows, up to kBlockN past the last, with 32-bit byte offsets:
+// moe::check_stack keeps N + 128 rows below 2^30 bytes, so N + 256 stay below 2^31.
+static_assert(kBlockN <= 256, "rows past the last");
 
 int32_t check_grouped(int64_t rows, const qmm_expert_stack_t* w, bool pointers, Stack* out) {
   if (!w) return report(QMM_ERR_NULL, "grouped: weights must be non-NULL");
@@ -91,9 +88,7 @@ int32_t check_grouped(int64_t rows, const qmm_expert_stack_t* w, bool pointers, 
   if (w->w.N < 1 || w->w.N > (1 << 20) || w->w.K < 1 || w->w.K > (1 << 20))
     return report(QMM_ERR_SHAPE, "grouped: need 1 <= N, K <= 2^20");
   if (!pointers) return QMM_OK;
-  int32_t rc = moe::check_stack("grouped", w, w->w.N, w->w.K, (int32_t)w->num_experts, w->w.dtype, out);
-  if (rc == QMM_OK) rc = check_rows("grouped", *out, w->w.N);
-  return rc;
+  return moe::check_stack("grouped", w, w->w.N, w->w.K, (int32_t)w->num_experts, w->w.dtype, out);
 }
 
 int32_t check_sizes(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, int64_t inter) {
@@ -231,9 +226,6 @@ int32_t qmm_moe_prompt(const qmm_moe_t* m, void* y, void* workspace, int64_t wor
     rc = moe::check_stack("moe_prompt: gate", m->gate, inter, hidden, (int32_t)experts, m->dtype, &gate);
     if (rc == QMM_OK) rc = moe::check_stack("moe_prompt: up", m->up, inter, hidden, (int32_t)experts, m->dtype, &up);
     if (rc == QMM_OK) rc = moe::check_stack("moe_prompt: down", m->down, hidden, inter, (int32_t)experts, m->dtype, &down);
-    if (rc == QMM_OK) rc = grouped::check_rows("moe_prompt: gate", gate, inter);
-    if (rc == QMM_OK) rc = grouped::check_rows("moe_prompt: up", up, inter);
-    if (rc == QMM_OK) rc = grouped::check_rows("moe_prompt: down", down, hidden);
     if (rc != QMM_OK) return rc;
     if (up.bits != gate.bits || up.group_size != gate.group_size)
       return report(QMM_ERR_UNSUPPORTED, "moe_prompt: gate and up must share bits and group_size");
