@@ -44,7 +44,23 @@ class QuantizedWeight:
         return d
 
 
+_gpus = 0                                # of the process, once asked for
+
+
+def check_current(index: int) -> None:
+    """Kernels are launched on the current GPU: tensors of another one are refused.  (Asking for the
+    current one takes 0.3 us, so a process of one GPU does not.)"""
+    global _gpus
+    if _gpus != 1:
+        _gpus = torch.cuda.device_count()
+        if index >= 0 and index != torch.cuda.current_device():
+            raise ValueError("the tensors are on cuda:%d, but the current GPU is cuda:%d; make theirs current "
+                             "(torch.cuda.device)" % (index, torch.cuda.current_device()))
+
+
 def _stream(device) -> int:
+    if _gpus != 1 and device.type == "cuda":
+        check_current(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 

@@ -8,15 +8,18 @@ from dataclasses import dataclass
 
 import torch
 
-from . import _lib
+from . import _lib, api
 from .api import _DTYPE_CODE, _DTYPE_NAME
 
 _byref = ctypes.byref
 
 
 def raw_stream(t: torch.Tensor) -> int:
-    """The current stream of t's device, as an address."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+    """The current stream of t's device, which has to be the current one, as an address."""
+    index = t.get_device()
+    if api._gpus != 1:
+        api.check_current(index)
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def same_device(who: str, first: torch.Tensor, *others) -> None:

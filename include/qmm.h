@@ -16,8 +16,8 @@
  *     safe.
  *   - Strides are in elements.  A tensor pointer points at the view's first element (a view's
  *     storage offset is already applied).
- *   - `stream` is a hipStream_t (NULL = the default stream).  Work is enqueued asynchronously;
- *     the library never synchronizes.
+ *   - `stream` is a hipStream_t of the current device (NULL = its default stream).  Work is
+ *     enqueued asynchronously; the library never synchronizes.
  *   - Every argument is validated before anything is launched; on error nothing is written,
  *     the call returns a negative QMM_ERR_* code and qmm_last_error() describes it
  *     (candle pitfall page "Metal 上批量 matmul 结果不对", section 现象: a structured error that
