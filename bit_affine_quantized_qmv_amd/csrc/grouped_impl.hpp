@@ -21,10 +21,11 @@
 // 4094 rows, 4096 x 14336, took 1240 us (gate, up) and 1040 (down).
 //
 // Measured: 4094 rows, 8 experts of [14336, 4096] in 4 bits, groups of 128: gate and up 1010 us, 0.95
-// PFLOP/s, the matrix cores busy half of the time; down (two passes for the two parts of h) 830 us, busy
-// 64%.  What is between them is the unpacking and the scaling, three vector instructions for each
-// matrix instruction, and a clock that falls to about 2 GHz under both.  509 rows, 128 experts of [704,
-// 1408] in 8 bits: 33 us, 4.3 TB/s.  Codes two steps ahead instead of one, waiting for the older half of
+// PFLOP/s, the matrix cores busy half of the time; down (two passes for the two parts of h) 805 us, busy
+// 64%.  The unpacking and the scaling are 2.9 vector instructions for each matrix instruction (1.5 in down,
+// whose two passes share them; 4.0 in groups of 64), and with two waves per SIMD their cycles add up: gate and
+// up issue 2.34e8 of 4 cycles and 6.58e7 of 16, 0.97 ms at the about 2 GHz that the clock falls to under both.
+// 509 rows, 128 experts of [704, 1408] in 8 bits: 32 us, 4.4 TB/s.  Codes two steps ahead instead of one, waiting for the older half of
 // the loads only: no faster (gate and up of 32 rows 139 us against 142, of 384 rows in 128 experts 39
 // against 34).
 #pragma once

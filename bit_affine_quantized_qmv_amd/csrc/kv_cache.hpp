@@ -134,7 +134,7 @@ hipError_t launch_read(const ReadArgs& a, hipStream_t stream);
 // What the waves of a workgroup share out: the tokens, for 16 query rows or (trees) for two tiles
 // of 16, or the query rows.
 enum AttendForm { kTokensForm, kPairsForm, kRowsForm };
-// Two tiles' registers fit two waves per SIMD.
+// Two tiles' registers fit two waves per SIMD (groups of 32 do not; 64 elements were not tried).
 constexpr bool has_pairs(int head_dim, int group) { return head_dim == 128 && group >= 64; }
 
 // Splits of the token range and tokens per split of an attention call (host only).
