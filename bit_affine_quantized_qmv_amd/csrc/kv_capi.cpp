@@ -107,7 +107,9 @@ int64_t part_floats(const AttendArgs& a, int64_t splits) {
 // 1, 8192 tokens, 256 rows 42 / 59; one group, 512 rows, 131071 tokens 526 / 600; the other way
 // only for a single long sequence in two groups: 65536 tokens, 256 rows 182 / 162).  With fewer
 // rows they gain where lengths are alike (128 rows, batch 16, 8192 tokens 176 us / 212) and lose
-// where they differ (121 / 112) or three do not fill a CU (batch 12: 118 / 100).
+// where they differ (121 / 112) or three do not fill a CU (batch 12: 118 / 100).  Trees of 64 or 256
+// elements keep the prompts' limit of 1024 rows, which is low for them: 64 elements, batch 16, 512 to 8192
+// tokens, 1020 rows in the first form 478 us, 1024 in the prompts' 624.
 namespace {
 
 struct Shape {
